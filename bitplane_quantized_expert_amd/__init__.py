@@ -34,6 +34,14 @@ PM_BATCH_MFMA = 2
 PM_READ_ONCE = 4
 PM_DETERMINISTIC = 8
 PM_GEMV_NOALLOC_MAX_PARTIALS = 524288
+PM_F32 = 0
+PM_F16 = 1
+PM_BF16 = 2
+PM_GROUPED_GATHER = 1
+PM_GROUPED_SCATTER = 2
+PM_GROUPED_SWIGLU = 4
+PM_ROUTE_MAX_EXPERTS = 4096
+PM_ROUTE_MAX_TOPK = 64
 
 _STATUS = {0: "PM_OK", -1: "PM_ERR_ARG", -2: "PM_ERR_SHAPE", -3: "PM_ERR_PREFIX",
            -4: "PM_ERR_NOT_RESIDENT", -5: "PM_ERR_OOM", -6: "PM_ERR_HIP", -7: "PM_ERR_STATE"}
@@ -53,6 +61,16 @@ class pm_expert_shape(ctypes.Structure):
     _fields_ = [("hidden", ctypes.c_int32), ("inter", ctypes.c_int32), ("group", ctypes.c_int32)]
 
 
+class pm_grouped_shape(ctypes.Structure):
+    _fields_ = [("n_experts", ctypes.c_int32), ("rows", ctypes.c_int32),
+                ("cols", ctypes.c_int32)]
+
+
+class pm_grouped_rows(ctypes.Structure):
+    _fields_ = [("n_rows", ctypes.c_int32), ("top_k", ctypes.c_int32),
+                ("d_offsets", ctypes.c_void_p), ("d_order", ctypes.c_void_p)]
+
+
 _c = ctypes
 _P = ctypes.c_void_p
 _I = ctypes.c_int
@@ -60,6 +78,9 @@ _Z = ctypes.c_size_t
 _U32 = ctypes.c_uint32
 _MS = pm_matrix_shape
 _ES = pm_expert_shape
+_GS = pm_grouped_shape
+_GR = pm_grouped_rows
+_L = ctypes.c_int64
 
 # name -> (restype, argtypes)
 SIGNATURES = {
@@ -104,6 +125,12 @@ SIGNATURES = {
     "pm_gemv_fp16": (_I, [_MS, _P, _P, _P, _P]),
     "pm_materialize_fp16_batch": (_I, [_I, _P, _P, _P, _P, _P, _P, _P]),
     "pm_gemv_fp16_batch": (_I, [_I, _P, _P, _P, _P, _P]),
+    "pm_route_workspace_bytes": (_Z, [_I, _I, _I]),
+    "pm_route_topk_device": (_I, [_I, _I, _I, _P, _I, _L, _P, _P, _P, _P, _P, _Z, _P]),
+    "pm_grouped_gemm": (_I, [_GS, _I, _P, _GR, _P, _L, _P, _I, _L, _U32, _P]),
+    "pm_grouped_gemm_w4": (_I, [_GS, _I, _P, _P, _P, _GR, _P, _I, _L, _P, _I, _L, _U32, _P]),
+    "pm_encode_w4_device": (_I, [_MS, _P, _I, _P, _P, _P, _P]),
+    "pm_combine_uses": (_I, [_I, _I, _I, _P, _I, _L, _P, _P, _I, _L, _P]),
 }
 
 _lib = None
@@ -309,6 +336,160 @@ def pm_allocate_bits(ids, w, err_profiles, budget):
     _check(lib().pm_allocate_bits(n, top_k, _hptr(ids), _hptr(w), err.shape[0], _hptr(err),
                                   int(budget), _hptr(k)))
     return k
+
+
+# ---------------------------------------------------------------- routed experts on the device
+# These take torch tensors only: types, sizes and strides come from them.
+_TYPES = {"torch.float32": PM_F32, "torch.float16": PM_F16, "torch.bfloat16": PM_BF16}
+
+
+def _on_device(*tensors):
+    """Every tensor (None allowed) is on the current HIP device, where the
+    call's kernels run."""
+    import torch
+    cur = torch.cuda.current_device() if torch.cuda.is_initialized() else 0
+    for t in tensors:
+        if t is not None and not (t.is_cuda and t.get_device() == cur):
+            raise ValueError(f"a tensor on {t.device}, not on the current device cuda:{cur}")
+
+
+def _type(t, what):
+    try:
+        return _TYPES[str(t.dtype)]
+    except KeyError:
+        raise ValueError(f"{what}: float32, float16 or bfloat16, not {t.dtype}") from None
+
+
+def _vec(t, dtype, n, what):
+    """A contiguous tensor of `dtype` (its name) with at least n elements (None passes)."""
+    if t is None:
+        return
+    if str(t.dtype) != dtype or not t.is_contiguous() or t.numel() < n:
+        raise ValueError(f"{what}: contiguous {dtype} of at least {n} elements")
+
+
+def _rows2d(t, n, cols, what):
+    """A 2-D tensor of at least n rows of `cols` adjacent elements: its row
+    distance in elements."""
+    if t.dim() != 2 or t.shape[0] < n or t.shape[1] != cols or (cols > 1 and t.stride(1) != 1):
+        raise ValueError(f"{what}: at least {n} rows of {cols} adjacent elements, not "
+                         f"{tuple(t.shape)} with strides {t.stride()}")
+    # one row, or none, has no distance to the next
+    return t.stride(0) if t.shape[0] > 1 else cols
+
+
+def pm_route_workspace_bytes(n_tokens, n_experts, top_k):
+    return lib().pm_route_workspace_bytes(n_tokens, n_experts, top_k)
+
+
+def pm_route_topk_device(d_logits, top_k, d_ids, d_w, d_offsets=None, d_order=None, d_ws=None,
+                         stream=None):
+    """d_logits [n_tokens][n_experts] (float32, float16 or bfloat16, any row
+    distance) -> d_ids int32, d_w float32 [n_tokens][top_k], and the uses
+    sorted by expert: d_offsets int32 [n_experts + 1], d_order int32
+    [n_tokens * top_k], with d_ws of pm_route_workspace_bytes bytes."""
+    if d_logits.dim() != 2:
+        raise ValueError("logits: [n_tokens][n_experts]")
+    n, e = d_logits.shape
+    ld = _rows2d(d_logits, n, e, "logits")
+    _on_device(d_logits, d_ids, d_w, d_offsets, d_order, d_ws)
+    uses = n * top_k
+    _vec(d_ids, "torch.int32", uses, "ids")
+    _vec(d_w, "torch.float32", uses, "w")
+    _vec(d_offsets, "torch.int32", e + 1, "offsets")
+    _vec(d_order, "torch.int32", uses, "order")
+    ws_bytes = 0
+    if d_ws is not None:
+        if not d_ws.is_contiguous():
+            raise ValueError("workspace: contiguous")
+        ws_bytes = d_ws.numel() * d_ws.element_size()
+    return _check(lib().pm_route_topk_device(
+        n, e, top_k, d_logits.data_ptr(), _type(d_logits, "logits"), ld, _dptr(d_ids),
+        _dptr(d_w), _dptr(d_offsets), _dptr(d_order), _dptr(d_ws), ws_bytes, _stream(stream)))
+
+
+def _grouped_args(n_experts, rows, cols, d_x, d_y, d_offsets, d_order, top_k, flags):
+    """The shape, the rows and the row distances of x and y of a grouped product."""
+    if d_x.dim() != 2 or d_y.dim() != 2:
+        raise ValueError("x and y are 2-D")
+    if top_k < 1:
+        raise ValueError("top_k: at least 1")
+    n = d_y.shape[0] if d_order is None else d_order.numel()
+    _vec(d_offsets, "torch.int32", n_experts + 1, "offsets")
+    _vec(d_order, "torch.int32", n, "order")
+    nx = (n + top_k - 1) // top_k if flags & PM_GROUPED_GATHER else n
+    ldx = _rows2d(d_x, nx, cols, "x")
+    ldy = _rows2d(d_y, n, rows // 2 if flags & PM_GROUPED_SWIGLU else rows, "y")
+    return (pm_grouped_shape(n_experts, rows, cols),
+            pm_grouped_rows(n, top_k, _dptr(d_offsets), _dptr(d_order)), ldx, ldy)
+
+
+def pm_grouped_gemm(d_w, d_x, d_y, d_offsets, d_order=None, top_k=1, flags=0, stream=None):
+    """d_w [n_experts][rows][cols] float16 or bfloat16, contiguous; d_x rows
+    of cols of the same type; d_y rows of that type or float32."""
+    if d_w.dim() != 3 or not d_w.is_contiguous():
+        raise ValueError("w: contiguous [n_experts][rows][cols]")
+    t = _type(d_w, "w")
+    if d_x.dtype != d_w.dtype:
+        raise ValueError(f"x of {d_x.dtype} with weights of {d_w.dtype}")
+    _on_device(d_w, d_x, d_y, d_offsets, d_order)
+    e, rows, cols = d_w.shape
+    s, r, ldx, ldy = _grouped_args(e, rows, cols, d_x, d_y, d_offsets, d_order, top_k, flags)
+    return _check(lib().pm_grouped_gemm(s, t, d_w.data_ptr(), r, d_x.data_ptr(), ldx,
+                                        d_y.data_ptr(), _type(d_y, "y"), ldy, flags,
+                                        _stream(stream)))
+
+
+def pm_grouped_gemm_w4(d_q, d_scales, d_zeros, group, d_x, d_y, d_offsets, d_order=None,
+                       top_k=1, flags=0, stream=None):
+    """d_q uint8 [n_experts][rows][cols/2], d_scales float16 and d_zeros uint8
+    (or None) [n_experts][rows][cols/group]; d_x rows of cols, d_y rows of x's
+    type or float32."""
+    if d_q.dim() != 3 or not d_q.is_contiguous() or str(d_q.dtype) != "torch.uint8":
+        raise ValueError("q: contiguous uint8 [n_experts][rows][cols/2]")
+    e, rows, half = d_q.shape
+    cols = 2 * half
+    n_groups = e * rows * (cols // group) if group > 0 else 0
+    _on_device(d_q, d_scales, d_zeros, d_x, d_y, d_offsets, d_order)
+    _vec(d_scales, "torch.float16", n_groups, "scales")
+    _vec(d_zeros, "torch.uint8", n_groups, "zeros")
+    s, r, ldx, ldy = _grouped_args(e, rows, cols, d_x, d_y, d_offsets, d_order, top_k, flags)
+    return _check(lib().pm_grouped_gemm_w4(s, group, d_q.data_ptr(), _dptr(d_scales),
+                                           _dptr(d_zeros), r, d_x.data_ptr(), _type(d_x, "x"),
+                                           ldx, d_y.data_ptr(), _type(d_y, "y"), ldy, flags,
+                                           _stream(stream)))
+
+
+def pm_encode_w4_device(d_w, group, d_q, d_scales, d_zeros=None, stream=None):
+    """d_w [rows][cols] (contiguous) -> d_q uint8 [rows][cols/2], d_scales
+    float16 and, for an asymmetric code, d_zeros uint8 [rows][cols/group]."""
+    if d_w.dim() != 2 or not d_w.is_contiguous():
+        raise ValueError("w: contiguous [rows][cols]")
+    rows, cols = d_w.shape
+    n_groups = rows * (cols // group) if group > 0 else 0
+    _on_device(d_w, d_q, d_scales, d_zeros)
+    _vec(d_q, "torch.uint8", rows * cols // 2, "q")
+    _vec(d_scales, "torch.float16", n_groups, "scales")
+    _vec(d_zeros, "torch.uint8", n_groups, "zeros")
+    return _check(lib().pm_encode_w4_device(pm_matrix_shape(rows, cols, group), d_w.data_ptr(),
+                                            _type(d_w, "w"), _dptr(d_q), _dptr(d_scales),
+                                            _dptr(d_zeros), _stream(stream)))
+
+
+def pm_combine_uses(d_z, d_w, d_y, stream=None):
+    """d_y[t] = sum_j d_w[t][j] * d_z[t * top_k + j]: d_w float32
+    [n_tokens][top_k], d_z rows of hidden, d_y rows of z's type or float32."""
+    if d_w.dim() != 2 or d_z.dim() != 2 or d_y.dim() != 2:
+        raise ValueError("z, w and y are 2-D")
+    n, top_k = d_w.shape
+    hidden = d_y.shape[1]
+    _vec(d_w, "torch.float32", n * top_k, "w")
+    _on_device(d_z, d_w, d_y)
+    ldz = _rows2d(d_z, n * top_k, hidden, "z")
+    ldy = _rows2d(d_y, n, hidden, "y")
+    return _check(lib().pm_combine_uses(n, top_k, hidden, d_z.data_ptr(), _type(d_z, "z"), ldz,
+                                        d_w.data_ptr(), d_y.data_ptr(), _type(d_y, "y"), ldy,
+                                        _stream(stream)))
 
 
 # ---------------------------------------------------------------- handles

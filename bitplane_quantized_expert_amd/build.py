@@ -23,7 +23,9 @@ TARGETS = [
      [os.path.join(PKG, "csrc", "pm_host.cpp"), os.path.join(PKG, "csrc", "pm_cache.cpp"),
       os.path.join(PKG, "csrc", "pm_kernels.hip"), os.path.join(PKG, "csrc", "pm_lut.hip"),
       os.path.join(PKG, "csrc", "pm_encoder.hip"),
-      os.path.join(PKG, "csrc", "pm_mfma.hip")]),
+      os.path.join(PKG, "csrc", "pm_mfma.hip"), os.path.join(PKG, "csrc", "pm_routed.cpp"),
+      os.path.join(PKG, "csrc", "pm_route.hip"), os.path.join(PKG, "csrc", "pm_grouped.hip"),
+      os.path.join(PKG, "csrc", "pm_combine.hip")]),
     (os.path.join(ROOT, "synth", "libpmsynth.so"),
      [os.path.join(ROOT, "synth", "synth_device.hip")]),
 ]

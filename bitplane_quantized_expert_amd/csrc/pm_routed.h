@@ -1,0 +1,57 @@
+// Routed experts on the device: the router, the products grouped by expert,
+// the combine and the 4-bit encoder (pm_route.hip, pm_grouped.hip,
+// pm_combine.hip; entry points in pm_routed.cpp).  Not part of the public ABI.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "../../include/pm.h"
+
+namespace pm {
+
+inline size_t type_bytes(int t) { return t == PM_F32 ? 4 : 2; }
+
+// ---------------------------------------------------------------- router
+struct RouteCall {
+    const void* logits;            // [n_tokens] rows of n_experts, ld apart
+    int64_t ld;
+    int32_t* ids;
+    float* w;
+    int32_t* offsets;              // null: no sorting
+    int32_t* order;
+    uint16_t* hist;                // workspace [blocks][n_experts]
+    int32_t n_tokens, n_experts, top_k, type;
+    int32_t block_tokens, n_blocks;   // tokens per histogram block, blocks
+};
+// Tokens of one histogram block and the number of blocks.
+void route_blocks(int n_tokens, int* block_tokens, int* n_blocks);
+hipError_t launch_route(const RouteCall& C, hipStream_t st);
+
+// ---------------------------------------------------------------- grouped products
+enum { kW16 = 0, kW4 = 1 };
+struct GroupedCall {
+    const void* w;                 // 16-bit weights, or packed 4-bit codes
+    const uint16_t* scales;        // 4-bit: fp16, one per group of inputs
+    const uint8_t* zeros;          // 4-bit: zero points (null: 8)
+    const void* x;
+    void* y;
+    const int32_t* offsets;
+    const int32_t* order;
+    int64_t ldx, ldy;
+    int32_t n_experts, rows, cols, group;
+    int32_t n_rows, top_k;
+    int32_t w_type, x_type, y_type;   // w_type: PM_F16 / PM_BF16 (16-bit weights)
+    uint32_t flags;
+};
+hipError_t launch_grouped(const GroupedCall& C, int kind, hipStream_t st);
+
+// ---------------------------------------------------------------- 4-bit encoder, combine
+hipError_t launch_encode_w4(size_t n_groups, int group, const void* w, int type, uint8_t* q,
+                            uint16_t* scales, uint8_t* zeros, hipStream_t st);
+hipError_t launch_combine_uses(int n_tokens, int top_k, int hidden, const void* z, int z_type,
+                               int64_t ldz, const float* w, void* y, int y_type, int64_t ldy,
+                               hipStream_t st);
+
+}  // namespace pm

@@ -360,6 +360,109 @@ pm_status pm_moe_token_forward(pm_store* s, int layer, int n_tokens, int top_k,
                                const int32_t* h_ids, const float* h_w, const uint8_t* h_k,
                                const float* d_x, float* d_y, void* compute, uint32_t flags);
 
+/* ---------------------------------------------------------------- routed experts on the device
+ * A layer whose experts are kept as 16-bit or 4-bit matrices, with the
+ * routing on the device: no host copy and no allocation, so every call can be
+ * captured into a HIP graph that serves new tokens.  A use is (token, slot)
+ * and has the number token * top_k + slot.  One layer:
+ *   pm_route_topk_device   logits -> ids, weights, uses sorted by expert;
+ *   pm_grouped_gemm        gate and up with PM_GROUPED_GATHER | _SWIGLU: h of
+ *                          every use, in sorted order;
+ *   pm_grouped_gemm        down with PM_GROUPED_SCATTER: one row per use;
+ *   pm_combine_uses        y[t] = sum_j w[t][j] * row (t, j).
+ * pm_grouped_gemm_w4 takes the place of pm_grouped_gemm for 4-bit experts.
+ * Sums run in fp32 in a fixed order (no atomics); each output is rounded
+ * once, to nearest even, to its type.  Element types: */
+enum { PM_F32 = 0, PM_F16 = 1, PM_BF16 = 2 };
+
+/* Router [T c4], the selection of pm_route_topk on the device.
+ *   d_logits [n_tokens] rows of n_experts values of logits_type, ld apart
+ *   (in elements, >= n_experts).
+ *   d_ids int32, d_w fp32 [n_tokens][top_k]: largest logit first, ties to the
+ *   lower id; softmax over the selected, in fp64, rounded to fp32.
+ * A logit that is -inf or NaN is never selected: a token with fewer than
+ * top_k others has id -1 and weight 0 in its last slots, and one with none
+ * (padding) is routed nowhere.  Several +inf share the weight equally.
+ *   d_offsets int32 [n_experts + 1], d_order int32 [n_tokens * top_k], both
+ *   null (no sorting) or neither (d_order may be null without tokens): the uses of expert e are d_order[d_offsets[e] ..
+ *   d_offsets[e+1]), in ascending order.  Entries of d_order from
+ *   d_offsets[n_experts] on are left as they were.
+ *   d_ws: pm_route_workspace_bytes(...) bytes of workspace, 16-byte aligned
+ *   (null when that is 0 or d_order is null); its contents need not be kept
+ *   or cleared, and calls that may overlap need one each.
+ * n_experts <= PM_ROUTE_MAX_EXPERTS and top_k <= PM_ROUTE_MAX_TOPK (else
+ * PM_ERR_SHAPE), top_k <= n_experts, n_tokens * top_k < 2^31 (PM_ERR_ARG).
+ * The outputs may not overlap the logits. */
+#define PM_ROUTE_MAX_EXPERTS 4096
+#define PM_ROUTE_MAX_TOPK 64
+size_t pm_route_workspace_bytes(int n_tokens, int n_experts, int top_k);
+pm_status pm_route_topk_device(int n_tokens, int n_experts, int top_k, const void* d_logits,
+                               int logits_type, int64_t ld, int32_t* d_ids, float* d_w,
+                               int32_t* d_offsets, int32_t* d_order, void* d_ws,
+                               size_t ws_bytes, void* stream);
+
+/* Products grouped by expert.  W[e] is rows x cols; sorted row i belongs to
+ * expert e when d_offsets[e] <= i < d_offsets[e+1]:
+ *     p = W[e] x[xr],   y[yr] = p,
+ * with u = d_order[i] (i where d_order is null), xr = u / top_k under
+ * PM_GROUPED_GATHER and i otherwise, yr = u under PM_GROUPED_SCATTER and i
+ * otherwise.  Under PM_GROUPED_SWIGLU the first rows/2 rows of W[e] are the
+ * gate and the others the up matrix, y has rows/2 columns and
+ *     y[yr] = SiLU(p[0 .. rows/2)) * p[rows/2 .. rows),  SiLU(g) = g / (1 + e^-g).
+ *   s.n_experts >= 1; n_rows is the number of entries of d_order, at least
+ *   d_offsets[n_experts]; d_offsets[0] = 0 and they do not decrease (other
+ *   offsets read and write nothing out of bounds, but give unspecified
+ *   rows).  Rows of y that no i maps to are left as they were, and an
+ *   i whose u is outside 0 .. n_rows-1 is left out.  A u that occurs twice under
+ *   PM_GROUPED_SCATTER leaves one of its results in each element.
+ *   d_x: rows ldx elements apart, (n_rows - 1) / top_k + 1 of them under
+ *   PM_GROUPED_GATHER, else n_rows.  d_y: n_rows rows, ldy elements apart.
+ *   An expert without rows is not read, and NaN in rows of x that no i maps
+ *   to reach no output.
+ * Alignment: weights, d_x and each row of x 16 bytes (ldx a multiple of 16
+ * bytes), d_y its element.  x and y may not overlap (PM_ERR_ARG).  One
+ * matrix holds fewer than 2^30 weights (PM_ERR_SHAPE).  cols == 0 gives
+ * zeros. */
+typedef struct { int32_t n_experts, rows, cols; } pm_grouped_shape;
+typedef struct {
+    int32_t n_rows, top_k;
+    const int32_t* d_offsets;
+    const int32_t* d_order;
+} pm_grouped_rows;
+enum { PM_GROUPED_GATHER = 1u, PM_GROUPED_SCATTER = 2u, PM_GROUPED_SWIGLU = 4u };
+/* 16-bit weights [n_experts][rows][cols] of `type` (PM_F16 or PM_BF16), x of
+ * the same type, y of that type or fp32.  cols % 8 == 0 (PM_ERR_SHAPE). */
+pm_status pm_grouped_gemm(pm_grouped_shape s, int type, const void* d_w, pm_grouped_rows r,
+                          const void* d_x, int64_t ldx, void* d_y, int y_type, int64_t ldy,
+                          uint32_t flags, void* stream);
+/* 4-bit weights: W[e][o][c] = (q - z) * scale, exact before the product.
+ *   d_q uint8 [n_experts][rows][cols/2]: q of column c in the low (c even) or
+ *   high (c odd) four bits of byte c/2.
+ *   d_scales fp16, d_zeros uint8 [n_experts][rows][cols/group]: one scale and
+ *   zero point per `group` inputs of one row; d_zeros null: z = 8.
+ *   group % 32 == 0, cols % group == 0 (PM_ERR_SHAPE).
+ * x and y are fp32, fp16 or bf16, y fp32 or of x's type. */
+pm_status pm_grouped_gemm_w4(pm_grouped_shape s, int group, const uint8_t* d_q,
+                             const uint16_t* d_scales, const uint8_t* d_zeros,
+                             pm_grouped_rows r, const void* d_x, int x_type, int64_t ldx,
+                             void* d_y, int y_type, int64_t ldy, uint32_t flags, void* stream);
+/* Encoder of the 4-bit format from weights d_w [rows][cols] of `type`, per
+ * group, in fp32: without d_zeros scale = fp16(max|w| / 7) and
+ * q = clamp(rint(w / scale), -8, 7) + 8; with d_zeros, lo = min(w, 0) and
+ * hi = max(w, 0), scale = fp16((hi - lo) / 15), z = clamp(rint(-lo / scale), 0, 15)
+ * and q = clamp(rint(w / scale) + z, 0, 15).  A scale of 0 gives q = 8
+ * (q = z = 0 with d_zeros).  Weights must be finite (other values give
+ * unspecified codes).  d_w and d_q 16-byte aligned. */
+pm_status pm_encode_w4_device(pm_matrix_shape s, const void* d_w, int type, uint8_t* d_q,
+                              uint16_t* d_scales, uint8_t* d_zeros, void* stream);
+/* y[t] = sum_j w[t][j] * z[t * top_k + j], the terms added in slot order in
+ * fp32.  A term of weight 0 is left out and its row not read (a slot that
+ * the router left empty).  z: n_tokens * top_k rows of `hidden`, ldz apart,
+ * of z_type; y: fp32 or z_type.  z and y may not overlap (PM_ERR_ARG). */
+pm_status pm_combine_uses(int n_tokens, int top_k, int hidden, const void* d_z, int z_type,
+                          int64_t ldz, const float* d_w, void* d_y, int y_type, int64_t ldy,
+                          void* stream);
+
 /* ---------------------------------------------------------------- checks and baselines
  * Bit-exact views of what the kernels decode (not on the hot path):
  *   pm_debug_unpack_prefix: d_prefix_out uint8 [rows][cols], the k-bit prefix.
