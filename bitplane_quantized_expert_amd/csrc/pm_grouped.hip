@@ -8,6 +8,7 @@
 
 #include "pm_convert.h"
 #include "pm_device.h"
+#include "pm_grouped_rows.h"
 #include "pm_routed.h"
 
 namespace pm {
@@ -54,15 +55,6 @@ __device__ inline Tile find_tile(const GroupedCall& C, int mt, int i) {
     }
     return Tile{-1, 0, 0};
 }
-
-// The use of sorted row i (-1: left out).
-__device__ inline int use_of(const GroupedCall& C, int i) {
-    if (!C.order) return i;
-    const int u = C.order[i];
-    return u >= 0 && u < C.n_rows ? u : -1;
-}
-
-__device__ inline float silu_up(float g, float u) { return g / (1.0f + expf(-g)) * u; }
 
 template <int KIND, int WT>
 __device__ inline float weight(const GroupedCall& C, int e, int o, int c) {
@@ -123,6 +115,10 @@ hipError_t run_simple(const GroupedCall& C, hipStream_t st) {
 hipError_t launch_grouped(const GroupedCall& C, int kind, hipStream_t st) {
     const bool f32 = C.y_type == PM_F32;
     if (kind == kW16) {
+        const int64_t xrows = C.flags & PM_GROUPED_GATHER ? (C.n_rows - 1) / C.top_k + 1 : 256;
+        if (C.n_rows >= 48 * int64_t(std::min(C.n_experts, C.n_rows)) &&
+            (xrows * C.ldx + C.cols) * 2 < 0xFFFFFFF0ll)
+            return launch_grouped_tiles(C, st);
         if (C.w_type == PM_F16)
             return f32 ? run_simple<kW16, PM_F16, PM_F16, PM_F32>(C, st)
                        : run_simple<kW16, PM_F16, PM_F16, PM_F16>(C, st);

@@ -2,6 +2,10 @@
 // checks and launches.  Nothing here allocates, copies or waits, so every
 // call can be captured into a HIP graph.
 #include <algorithm>
+#include <atomic>
+#include <mutex>
+#include <set>
+#include <utility>
 
 #include "pm_error.h"
 #include "pm_routed.h"
@@ -31,6 +35,36 @@ static size_t span(size_t n, int64_t ld, size_t cols, int type) {
 // Rows of any buffer and their distance stay below this, so that byte
 // addresses of a valid call never wrap.
 static constexpr int64_t kMaxLd = int64_t(1) << 31;
+
+// ---------------------------------------------------------------- device properties
+static constexpr int kMaxDevices = 64;
+
+int pm::compute_units() {
+    static std::atomic<int> known[kMaxDevices];
+    int dev = 0, n = 0;
+    if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= kMaxDevices) return 256;
+    n = known[dev].load(std::memory_order_relaxed);
+    if (n > 0) return n;
+    if (hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || n < 1)
+        n = 256;
+    known[dev].store(n, std::memory_order_relaxed);
+    return n;
+}
+
+hipError_t pm::allow_lds(const void* kernel, int bytes) {
+    // never destroyed: no destructor of this library runs at process exit
+    static std::mutex& mu = *new std::mutex();
+    static std::set<std::pair<const void*, int>>& done =
+        *new std::set<std::pair<const void*, int>>();
+    int dev = 0;
+    hipError_t e = hipGetDevice(&dev);
+    if (e != hipSuccess) return e;
+    std::lock_guard<std::mutex> lk(mu);
+    if (done.count({kernel, dev})) return hipSuccess;
+    e = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == hipSuccess) done.insert({kernel, dev});
+    return e;
+}
 
 // ---------------------------------------------------------------- router
 void pm::route_blocks(int n_tokens, int* block_tokens, int* n_blocks) {
@@ -117,6 +151,9 @@ static pm_status check_grouped(pm_grouped_shape s, pm_grouped_rows r, const void
                                uint32_t flags) {
     if (s.n_experts < 1 || s.rows < 0 || s.cols < 0)
         return failf(PM_ERR_SHAPE, "grouped: %d experts of %d x %d", s.n_experts, s.rows, s.cols);
+    if (s.n_experts > kMaxGroupedExperts)
+        return failf(PM_ERR_SHAPE, "grouped: %d experts, above %d", s.n_experts,
+                     kMaxGroupedExperts);
     if (int64_t(s.rows) * s.cols >= (int64_t(1) << 30))
         return failf(PM_ERR_SHAPE, "grouped: a matrix of %d x %d holds 2^30 weights or more",
                      s.rows, s.cols);

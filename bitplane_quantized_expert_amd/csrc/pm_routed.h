@@ -45,7 +45,18 @@ struct GroupedCall {
     int32_t w_type, x_type, y_type;   // w_type: PM_F16 / PM_BF16 (16-bit weights)
     uint32_t flags;
 };
+// Experts of one call (the kernels keep a table of them in LDS).
+constexpr int kMaxGroupedExperts = PM_GROUPED_MAX_EXPERTS;
 hipError_t launch_grouped(const GroupedCall& C, int kind, hipStream_t st);
+// 256 x 256 tiles (pm_grouped_tile.hip), 16-bit weights; the offsets of a
+// tile's rows in x must fit 32 bits.
+hipError_t launch_grouped_tiles(const GroupedCall& C, hipStream_t st);
+
+// Compute units of the current device.
+int compute_units();
+// Lets a kernel take up to `bytes` of dynamic LDS on the current device.
+constexpr int kTileMaxLds = 160 * 1024 - 1024;
+hipError_t allow_lds(const void* kernel, int bytes);
 
 // ---------------------------------------------------------------- 4-bit encoder, combine
 hipError_t launch_encode_w4(size_t n_groups, int group, const void* w, int type, uint8_t* q,

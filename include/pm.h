@@ -409,7 +409,7 @@ pm_status pm_route_topk_device(int n_tokens, int n_experts, int top_k, const voi
  * otherwise.  Under PM_GROUPED_SWIGLU the first rows/2 rows of W[e] are the
  * gate and the others the up matrix, y has rows/2 columns and
  *     y[yr] = SiLU(p[0 .. rows/2)) * p[rows/2 .. rows),  SiLU(g) = g / (1 + e^-g).
- *   s.n_experts >= 1; n_rows is the number of entries of d_order, at least
+ *   s.n_experts in 1 .. PM_GROUPED_MAX_EXPERTS (else PM_ERR_SHAPE); n_rows is the number of entries of d_order, at least
  *   d_offsets[n_experts]; d_offsets[0] = 0 and they do not decrease (other
  *   offsets read and write nothing out of bounds, but give unspecified
  *   rows).  Rows of y that no i maps to are left as they were, and an
@@ -423,6 +423,7 @@ pm_status pm_route_topk_device(int n_tokens, int n_experts, int top_k, const voi
  * bytes), d_y its element.  x and y may not overlap (PM_ERR_ARG).  One
  * matrix holds fewer than 2^30 weights (PM_ERR_SHAPE).  cols == 0 gives
  * zeros. */
+#define PM_GROUPED_MAX_EXPERTS 4096
 typedef struct { int32_t n_experts, rows, cols; } pm_grouped_shape;
 typedef struct {
     int32_t n_rows, top_k;

@@ -87,6 +87,7 @@ def w4(s=None, group=32, q=A, sc=A + (1 << 34), z=None, r=None, x=B, xt=pm.PM_F3
 @pytest.mark.parametrize("call", [gemm, w4])
 def test_grouped_refusals(call):
     refused(call(s=shape(e=0)), pm.PM_ERR_SHAPE)
+    refused(call(s=shape(e=pm.PM_GROUPED_MAX_EXPERTS + 1)), pm.PM_ERR_SHAPE, "experts")
     refused(call(s=shape(r=-1)), pm.PM_ERR_SHAPE)
     refused(call(s=shape(r=1 << 15, c=1 << 15)), pm.PM_ERR_SHAPE, "2^30")
     refused(call(s=shape(r=63), flags=pm.PM_GROUPED_SWIGLU), pm.PM_ERR_SHAPE, "gate")
