@@ -25,7 +25,10 @@ TARGETS = [
       os.path.join(PKG, "csrc", "pm_encoder.hip"),
       os.path.join(PKG, "csrc", "pm_mfma.hip"), os.path.join(PKG, "csrc", "pm_routed.cpp"),
       os.path.join(PKG, "csrc", "pm_route.hip"), os.path.join(PKG, "csrc", "pm_grouped.hip"),
-      os.path.join(PKG, "csrc", "pm_grouped_tile.hip"), os.path.join(PKG, "csrc", "pm_combine.hip")]),
+      os.path.join(PKG, "csrc", "pm_grouped_tile.hip"),
+      os.path.join(PKG, "csrc", "pm_grouped_stream16.hip"),
+      os.path.join(PKG, "csrc", "pm_grouped_stream4.hip"),
+      os.path.join(PKG, "csrc", "pm_grouped_stream4f.hip"), os.path.join(PKG, "csrc", "pm_combine.hip")]),
     (os.path.join(ROOT, "synth", "libpmsynth.so"),
      [os.path.join(ROOT, "synth", "synth_device.hip")]),
 ]
