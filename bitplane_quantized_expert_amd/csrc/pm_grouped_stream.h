@@ -28,10 +28,12 @@
 // are 4 pieces of it, else a 4 x 4 exchange of words between the lanes (four
 // v_permlane swaps) makes them 32 adjacent inputs.
 //
-// Activations meet 4-bit weights as fp16, scaled by a power of two per row
-// and wave so that the largest lies in [2^14, 2^15): what is lost is below
-// 2^-39 of the largest.  An fp32 row takes two columns, its value rounded to
-// fp16 and the rest (times 2^11) rounded again, together 2^-24 of the value.
+// Activations meet 4-bit weights as fp16; bf16 and fp32 are scaled by a power
+// of two per row and wave so that the largest lies in [2^14, 2^15): what is
+// lost is below 2^-39 of the largest.  An fp32 row takes two columns, its
+// value rounded to fp16 and the rest (times 2^11) rounded again, together
+// 2^-24 of the value.  The waves convert a few columns at a time into LDS and
+// take their operands from there.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -55,7 +57,8 @@ struct StreamPlan {
 
 namespace {
 
-constexpr int kStreamThreads = 512, kStreamWaves = 8, kChunk = 4;
+constexpr int kStreamThreads = 512, kStreamWaves = 8;
+constexpr int kSteps = 4;                       // row tiles of an unrolled group
 // An offset beyond any buffer (all are below 2 GiB), with any immediate added.
 constexpr uint32_t kNowhere = 0x80000000u;
 constexpr int kRawBuffer = 0x00020000;
@@ -107,14 +110,6 @@ __device__ inline u32x4 codes_to_f16(const CodeBits& k, uint32_t w, f16x2 za, f1
     const f16x2 d = __builtin_bit_cast(f16x2, (w8 & k.odd) | k.k64) - zb;
     return u32x4{__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b),
                  __builtin_bit_cast(uint32_t, c), __builtin_bit_cast(uint32_t, d)};
-}
-
-// 8 halves in the order of codes_to_f16.
-__device__ inline u32x4 code_order(u32x4 d) {
-    return u32x4{__builtin_amdgcn_perm(d[2], d[0], 0x05040100u),
-                 __builtin_amdgcn_perm(d[2], d[0], 0x07060302u),
-                 __builtin_amdgcn_perm(d[3], d[1], 0x05040100u),
-                 __builtin_amdgcn_perm(d[3], d[1], 0x07060302u)};
 }
 
 // 4 x 4 transposition of the words of lanes i, i + 16, i + 32, i + 48.
@@ -215,64 +210,53 @@ __device__ inline TileRows find_tile_rows(const GroupedCall& C, int mt, const Ti
 struct F8 {
     float v[8];
 };
-// Eight activations at `p`, or zeros: `ok` says whether they count (p can be
-// read in any case).
-__device__ inline u32x4 load_x16(const char* p, bool ok) {
-    const u32x4 d = *reinterpret_cast<const u32x4*>(p);
-    return ok ? d : u32x4{0, 0, 0, 0};
-}
-__device__ inline F8 load_x32(const char* p, bool ok) {
-    const f32x4 a = *reinterpret_cast<const f32x4*>(p), b = *reinterpret_cast<const f32x4*>(p + 16);
-    F8 r;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        r.v[i] = ok ? a[i] : 0.0f;
-        r.v[4 + i] = ok ? b[i] : 0.0f;
-    }
-    return r;
-}
-__device__ inline F8 widen_bf16(u32x4 d) {
-    F8 r;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        r.v[2 * i] = __uint_as_float(d[i] << 16);
-        r.v[2 * i + 1] = __uint_as_float(d[i] & 0xFFFF0000u);
-    }
-    return r;
-}
-__device__ inline float max_finite(const F8& x, float m) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float a = fabsf(x.v[i]);
-        m = a < INFINITY ? fmaxf(m, a) : m;
-    }
-    return m;
-}
-// For a row of which the wave's largest finite value is `big` (a lane's part
-// of it): 2^k that brings it to [2^14, 2^15), and 2^-k.
-struct RowScale {
-    float up, down;
+// Eight activations at p, and whether they count (p can be read in any case).
+template <bool X32>
+struct RawX {
+    u32x4 d[X32 ? 2 : 1];
 };
-__device__ inline RowScale row_scale(float big) {
-    big = fmaxf(big, __shfl_xor(big, 16));
-    big = fmaxf(big, __shfl_xor(big, 32));
-    const int k = min(max(14 - (int(__float_as_uint(big) >> 23) - 127), -113), 126);
-    return RowScale{__uint_as_float(uint32_t(127 + k) << 23), __uint_as_float(uint32_t(127 - k) << 23)};
-}
-// x * up as halves (lo: what that rounding leaves, times 2^11).
-__device__ inline u32x4 to_f16(const F8& x, float up, bool lo) {
-    uint32_t h[8];
+template <bool X32>
+__device__ inline F8 widen(const RawX<X32>& x, bool bf16) {
+    F8 r;
+    if constexpr (X32) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float s = x.v[i] * up;
-        _Float16 f = _Float16(s);
-        if (lo) {
-            const float hi = float(f);
-            f = fabsf(hi) < INFINITY ? _Float16((s - hi) * 2048.0f) : _Float16(0.0f);
+        for (int i = 0; i < 8; ++i) r.v[i] = __uint_as_float(x.d[i >> 2][i & 3]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t w = x.d[0][i];
+            r.v[2 * i] = bf16 ? __uint_as_float(w << 16) : half_bits(w);
+            r.v[2 * i + 1] = bf16 ? __uint_as_float(w & 0xFFFF0000u) : half_bits(w >> 16);
         }
-        h[i] = __builtin_bit_cast(uint16_t, f);
     }
-    return u32x4{h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16};
+    return r;
+}
+
+template <int CTRL, int ROW_MASK>
+__device__ inline float dpp_fmax(float v) {
+    const int b = __builtin_bit_cast(int, v);
+    return fmaxf(v, __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(b, b, CTRL, ROW_MASK, 0xF,
+                                                                         false)));
+}
+__device__ inline float wave_fmax(float v) {
+    v = dpp_fmax<0xB1, 0xF>(v);
+    v = dpp_fmax<0x4E, 0xF>(v);
+    v = dpp_fmax<0x141, 0xF>(v);
+    v = dpp_fmax<0x140, 0xF>(v);
+    v = dpp_fmax<0x142, 0xA>(v);
+    v = dpp_fmax<0x143, 0xC>(v);
+    return __builtin_bit_cast(float,
+                              __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 63));
+}
+
+// Halves, rounded to nearest even, in the order of codes_to_f16.
+__device__ inline u32x4 pack_codes(const _Float16* h) {
+    u32x4 r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        r[i] = uint32_t(__builtin_bit_cast(uint16_t, h[i])) |
+               uint32_t(__builtin_bit_cast(uint16_t, h[i + 4])) << 16;
+    return r;
 }
 
 // f(0), .., f(N - 1) with constant arguments.
@@ -297,7 +281,12 @@ __global__ __launch_bounds__(kStreamThreads, 2) void stream_kernel(const Grouped
     // (as many as 256 registers hold beside the activations)
     constexpr int kSlots =
         GM == kAnyGroup || (GM == kGroup32 && KB == 4) || kLoads * MT > 8 ? 2 : 4;
-    __shared__ __attribute__((aligned(16))) float part[2][kStreamWaves][kChunk][MT * 256];
+    // sums of a chunk: [buffer][wave][row tile][columns of x / 4][16][4], room
+    // for 4 row tiles of all columns; the buffer to be filled next holds the
+    // converted activations before
+    constexpr int kPart = kSteps * MT * 256;
+    __shared__ __attribute__((aligned(16))) float part[2][kStreamWaves][kPart];
+    __shared__ float xscale[16 * MT][kStreamWaves];
     __shared__ int use_row[2][16 * MT];
     const int lane = threadIdx.x & 63, wv = uni(threadIdx.x >> 6);
     const int i16 = lane & 15, q = lane >> 4;
@@ -403,85 +392,142 @@ __global__ __launch_bounds__(kStreamThreads, 2) void stream_kernel(const Grouped
             }
         };
 
-        // ---- activations of this wave's inputs, as matrix operands
-        u32x4 xf[KB * 4][MT] = {};
-        float xs[MT][4] = {};                              // of columns 4q + r
-        const char* xrow[MT];
-        bool xok[MT];
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-            // column v = 16 m + i16: a row, or the value (lower half) or rest
-            // (upper half) of an fp32 row
-            const int v = m * 16 + i16, r = X32 ? v & (8 * MT - 1) : v;
-            const int u = r < g.n ? use_of(C, g.row0 + r) : -1;
+        auto issue_step = [&](auto slot, int c, int step, int panel) {
+            // c row tiles on from row tile `step` of this wave in `panel`; past
+            // the group, of the panel or group after it
+            if (c >= kSteps) {
+                c -= kSteps;
+                if (++panel == P.panels) {
+                    panel = 0;
+                    step += kSteps;
+                }
+            }
+            issue(slot, rt0 + (step + c) * rw + rg, panel);
+        };
+        steps_to<kSlots - 1>([&](auto c) { issue(c, rt0 + c * rw + rg, 0); });
+
+        // ---- activations of this wave's inputs, as matrix operands.  Column v
+        // is row v, or the value (even v) or rest (odd v) of fp32 row v / 2
+        const int nv = X32 ? 2 * g.n : g.n;
+        int vlog = 2;
+        while ((1 << vlog) < nv) ++vlog;
+        const int u_lane = lane < g.n ? use_of(C, g.row0 + lane) : -1;
+        if (wv == 0 && lane < g.n)
+            use_row[seg][lane] =
+                u_lane < 0 ? -1 : (C.flags & PM_GROUPED_SCATTER ? u_lane : g.row0 + lane);
+        u32x4 xf[KB * 4][MT];
+        float xs[MT][4];                                   // of columns 4q + r
+        // row r of x (any row where r is not a row of the group)
+        auto x_row = [&](int u, int r) {
             const int64_t xr = u < 0 ? 0 : gather ? u / C.top_k : g.row0 + r;
-            xok[m] = u >= 0;
-            xrow[m] = static_cast<const char*>(C.x) + xr * C.ldx * (X32 ? 4 : 2);
-            if (wv == 0 && q == 0 && r < g.n && !(X32 && v >= 8 * MT))
-                use_row[seg][r] = u < 0 ? -1 : (C.flags & PM_GROUPED_SCATTER ? u : g.row0 + r);
-        }
+            return static_cast<const char*>(C.x) + xr * C.ldx * (X32 ? 4 : 2);
+        };
         auto load_x = [&](int panel) {
-            if (C.cols == 0) return;
-            // first of operand f's 8 inputs: c0 + (f / 4) * 128 + (f % 4) * step
-            // (computed here each time: kept over the row tiles it would
-            // take the registers that hold the weights)
-            const int step = kWhole ? 8 : 32;
-            int c0 = first_block(panel) * 128 + q * (kWhole ? 32 : 8);
-            asm volatile("" : "+v"(c0));
-            const int last = C.cols - 8;
+            const int c0 = first_block(panel) * 128;       // the wave's inputs
+            if constexpr (KIND != kW4) {
 #pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                float down = 1.0f;
-                if constexpr (!X32) {
+                for (int m = 0; m < MT; ++m) {
+                    const int u = __shfl(u_lane, m * 16 + i16);
+                    const char* p = x_row(u, m * 16 + i16);
+                    int c = c0 + q * 8;
+                    asm volatile("" : "+v"(c));            // (addresses are not kept)
 #pragma unroll
                     for (int f = 0; f < KB * 4; ++f) {
-                        const int c = c0 + (f >> 2) * 128 + (f & 3) * step;
-                        xf[f][m] = load_x16(xrow[m] + size_t(min(c, last)) * 2, xok[m] && c <= last);
+                        const bool ok = u >= 0 && c + f * 32 < C.cols;
+                        const u32x4 d = *reinterpret_cast<const u32x4*>(
+                            p + size_t(max(min(c + f * 32, C.cols - 8), 0)) * 2);
+                        xf[f][m] = ok ? d : u32x4{0, 0, 0, 0};
                     }
-                    if (KIND == kW4 && C.x_type == PM_BF16) {
-                        float big = 0.0f;
+                }
+            } else {
+                // vper columns at a time: halves [column][inputs of the panel]
+                char* const stage = reinterpret_cast<char*>(&part[buf][0][0]);
+                const int width = KB * 128 << P.kw_log;
+                const int vper = min(1 << vlog, kStreamWaves * kPart * 2 / width);
+                const int rper = X32 ? vper >> 1 : vper;
+                const bool bf16 = C.x_type == PM_BF16;
+                const bool scaled = X32 || bf16;
+                for (int v0 = 0; v0 < nv; v0 += vper) {
+                    const int r0 = X32 ? v0 >> 1 : v0;
+                    const int c = c0 + lane * 8;
+                    const bool mine = rg == 0 && lane < KB * 16;
+                    // 4 rows of x are on their way together
+#pragma unroll 1
+                    for (int rb = r0; rg == 0 && rb < min(r0 + rper, g.n); rb += 4) {
+                        RawX<X32> raw[4];
 #pragma unroll
-                        for (int f = 0; f < KB * 4; ++f) big = max_finite(widen_bf16(xf[f][m]), big);
-                        const RowScale k = row_scale(big);
+                        for (int k = 0; k < 4; ++k) {
+                            const int u = __builtin_amdgcn_readlane(u_lane, min(rb + k, g.n - 1));
+                            const char* p = x_row(u, min(rb + k, g.n - 1)) +
+                                            size_t(min(c, C.cols - 8)) * (X32 ? 4 : 2);
+                            const bool ok = u >= 0 && c < C.cols && mine;
 #pragma unroll
-                        for (int f = 0; f < KB * 4; ++f) {
-                            __builtin_amdgcn_sched_barrier(0);
-                            xf[f][m] = to_f16(widen_bf16(xf[f][m]), k.up, false);
+                            for (int h = 0; h < (X32 ? 2 : 1); ++h) {
+                                const u32x4 d = *reinterpret_cast<const u32x4*>(p + 16 * h);
+                                raw[k].d[h] = ok ? d : u32x4{0, 0, 0, 0};
+                            }
                         }
-                        down = k.down;
-                    }
-                } else {
-                    auto load = [&](int f) {
-                        const int c = c0 + (f >> 2) * 128 + (f & 3) * step;
-                        return load_x32(xrow[m] + size_t(min(c, last)) * 4, xok[m] && c <= last);
-                    };
-                    float big = 0.0f;
 #pragma unroll
-                    for (int f = 0; f < KB * 4; ++f) {
-                        if (f % 4 == 0) __builtin_amdgcn_sched_barrier(0);
-                        big = max_finite(load(f), big);
-                    }
-                    const RowScale k = row_scale(big);
-                    const bool lo = m * 16 + i16 >= 8 * MT;
-                    asm volatile("" : "+v"(c0));
+                        for (int k = 0; k < 4; ++k) {
+                            const int v = X32 ? 2 * (rb + k) : rb + k;
+                            if (rb + k >= min(r0 + rper, g.n)) break;
+                            const F8 x = widen<X32>(raw[k], bf16);
+                            float up = 1.0f, down = 1.0f;
+                            if (scaled) {
+                                float big = 0.0f;
 #pragma unroll
-                    for (int f = 0; f < KB * 4; ++f) {
-                        if (f % 4 == 0) __builtin_amdgcn_sched_barrier(0);
-                        xf[f][m] = to_f16(load(f), k.up, lo);
+                                for (int i = 0; i < 8; ++i)
+                                    big = fabsf(x.v[i]) < INFINITY ? fmaxf(big, fabsf(x.v[i])) : big;
+                                big = wave_fmax(big);
+                                // 2^e brings the largest to [2^14, 2^15)
+                                const int e = min(
+                                    max(14 - (int(__float_as_uint(big) >> 23) - 127), -113), 126);
+                                up = __uint_as_float(uint32_t(127 + e) << 23);
+                                down = __uint_as_float(uint32_t(127 - e) << 23);
+                            }
+                            _Float16 hi[8], lo[8];
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                const float s = x.v[i] * up;
+                                hi[i] = _Float16(s);
+                                const float back = float(hi[i]);
+                                lo[i] = fabsf(back) < INFINITY ? _Float16((s - back) * 2048.0f)
+                                                               : _Float16(0.0f);
+                            }
+                            char* at = stage + (size_t(v - v0) * width + (ks * KB * 128) + lane * 8) * 2;
+                            if (mine) {
+                                *reinterpret_cast<u32x4*>(at) = pack_codes(hi);
+                                if constexpr (X32)
+                                    *reinterpret_cast<u32x4*>(at + size_t(width) * 2) = pack_codes(lo);
+                            }
+                            if (lane == 0) {
+                                xscale[v][ks] = down;
+                                if constexpr (X32) xscale[v + 1][ks] = down * (1.0f / 2048.0f);
+                            }
+                        }
                     }
-                    down = lo ? k.down * (1.0f / 2048.0f) : k.down;
+                    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+#pragma unroll
+                    for (int m = 0; m < MT; ++m) {
+                        // (a column without a row takes another's operands; its
+                        // sums are not used)
+                        const int v = m * 16 + i16 - v0;
+                        const char* p = stage + (size_t(v & (vper - 1)) * width + ks * KB * 128 +
+                                                 (kWhole ? q * 32 : q * 8)) * 2;
+                        if (v0 == 0 || (v >= 0 && v < vper)) {
+#pragma unroll
+                            for (int f = 0; f < KB * 4; ++f)
+                                xf[f][m] = *reinterpret_cast<const u32x4*>(
+                                    p + ((f >> 2) * 128 + (f & 3) * (kWhole ? 8 : 32)) * 2);
+                        }
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) xs[m][r] = xscale[m * 16 + 4 * q + r][ks];
+                    }
+                    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
                 }
-                if constexpr (KIND == kW4) {
-#pragma unroll
-                    for (int f = 0; f < KB * 4; ++f) xf[f][m] = code_order(xf[f][m]);
-                }
-#pragma unroll
-                for (int r = 0; r < 4; ++r) xs[m][r] = __shfl(down, 4 * q + r);
-                __builtin_amdgcn_sched_barrier(0);
             }
         };
 
-        f32x4 acc[kChunk][MT];
         auto multiply = [&](auto slot, int panel, f32x4* a) {
             constexpr int S = decltype(slot)::value;
             f32x4 sum[MT];
@@ -546,67 +592,79 @@ __global__ __launch_bounds__(kStreamThreads, 2) void stream_kernel(const Grouped
                     a[m][r] = KIND == kW4 ? fmaf(sum[m][r], xs[m][r], a[m][r]) : a[m][r] + sum[m][r];
         };
 
-        const int per_chunk = rw * kChunk;
-        // step c of (rtb, panel); c >= kChunk is of the panel or chunk after it
-        auto issue_step = [&](auto slot, int c, int rtb, int panel) {
-            if (c >= kChunk) {
-                c -= kChunk;
-                if (++panel == P.panels) {
-                    panel = 0;
-                    rtb += per_chunk;
-                }
-            }
-            issue(slot, rtb + c * rw + rg, panel);
-        };
-        steps_to<kSlots - 1>([&](auto c) { issue(c, rt0 + c * rw + rg, 0); });
+        f32x4 acc[kSteps][MT];
         int nlog = 0;
         while ((1 << nlog) < g.n) ++nlog;
         const int plog = glu ? 3 : 4;
-
-        for (int rtb = rt0; rtb < rt1; rtb += per_chunk) {
+        // row tiles of a wave per chunk, and floats of one
+        const int clog = P.panels > 1 ? 2 : min(4, 6 + MT - 1 - vlog);
+        const int tile_floats = 16 << vlog;
+        bool first = true;
+        for (int rtb = rt0, step = 0; rtb < rt1; rtb += rw << clog) {
+            int here = 0;                                  // row tiles of the chunk so far
+            do {
 #pragma unroll
-            for (int c = 0; c < kChunk; ++c)
+                for (int c = 0; c < kSteps; ++c)
 #pragma unroll
-                for (int m = 0; m < MT; ++m) acc[c][m] = f32x4{0.f, 0.f, 0.f, 0.f};
-            for (int panel = 0; panel < P.panels; ++panel) {
-                if (P.panels > 1 || rtb == rt0) load_x(panel);
-                steps_to<kChunk>([&](auto c) {
-                    constexpr int kNext = (c + kSlots - 1) % kSlots;
-                    issue_step(std::integral_constant<int, kNext>{}, c + kSlots - 1, rtb, panel);
-                    __builtin_amdgcn_sched_barrier(0);
-                    multiply(std::integral_constant<int, c % kSlots>{}, panel, acc[c]);
-                    // registers: a row tile's decoded weights live in its own step
-                    __builtin_amdgcn_sched_barrier(0);
-                });
-            }
+                    for (int m = 0; m < MT; ++m) acc[c][m] = f32x4{0.f, 0.f, 0.f, 0.f};
+                for (int panel = 0; panel < P.panels; ++panel) {
+                    if (C.cols > 0 && (P.panels > 1 || first)) load_x(panel);
+                    first = false;
+                    steps_to<kSteps>([&](auto c) {
+                        constexpr int kNext = (c + kSlots - 1) % kSlots;
+                        issue_step(std::integral_constant<int, kNext>{}, c + kSlots - 1, step, panel);
+                        __builtin_amdgcn_sched_barrier(0);
+                        if (C.cols > 0 && rt0 + (step + c) * rw + rg < rt1)
+                            multiply(std::integral_constant<int, c % kSlots>{}, panel, acc[c]);
+                        // registers: a row tile's decoded weights live in its own step
+                        __builtin_amdgcn_sched_barrier(0);
+                    });
+                }
 #pragma unroll
-            for (int c = 0; c < kChunk; ++c)
+                for (int c = 0; c < kSteps; ++c)
 #pragma unroll
-                for (int m = 0; m < MT; ++m)
-                    *reinterpret_cast<f32x4*>(&part[buf][wv][c][m * 256 + lane * 4]) = acc[c][m];
+                    for (int m = 0; m < MT; ++m)
+                        if (m * 16 + 4 * q < 1 << vlog)
+                            *reinterpret_cast<f32x4*>(
+                                &part[buf][wv][(here + c) * tile_floats + m * 256 + lane * 4]) =
+                                acc[c][m];
+                here += kSteps;
+                step += kSteps;
+            } while (here < 1 << clog && rtb + here * rw < rt1);
             // LDS only: the weights under way are not waited for
             asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-            const int items = per_chunk << (nlog + plog);
+            // kw adjacent lanes per output, one for each wave's part
+            const int items = (rw << clog) << (nlog + plog + P.kw_log);
+#pragma unroll 1
             for (int it = threadIdx.x; it < items; it += kStreamThreads) {
-                const int col = it & ((1 << plog) - 1);
-                const int r = (it >> plog) & ((1 << nlog) - 1), t = it >> (plog + nlog);
+                const int item = it >> P.kw_log;
+                const int col = item & ((1 << plog) - 1);
+                const int r = (item >> plog) & ((1 << nlog) - 1), t = item >> (plog + nlog);
                 const int rt = rtb + t, o = rt * per_tile + col;
                 if (r >= g.n || rt >= rt1 || o >= out) continue;
-                const int yr = use_row[seg][r];
-                if (yr < 0) continue;
-                const int c = t >> (3 - P.kw_log), first = (t & (rw - 1)) << P.kw_log;
-                auto total = [&](int v, int column) {
-                    const float* p = &part[buf][first][c][(v >> 4) * 256 +
-                                                          (((v >> 2) & 3) * 16 + column) * 4 + (v & 3)];
-                    float s = 0.0f;
-                    for (int k = 0; k < kw; ++k) s += p[k * kChunk * MT * 256];
-                    return s;
-                };
-                float p0 = total(r, col), p1 = glu ? total(r, col + 8) : 0.0f;
-                if (X32) {
-                    p0 += total(r + 8 * MT, col);
-                    if (glu) p1 += total(r + 8 * MT, col + 8);
+                const int v = X32 ? 2 * r : r;
+                const float* p = &part[buf][((t & (rw - 1)) << P.kw_log) + (it & (kw - 1))]
+                                      [(t >> (3 - P.kw_log)) * tile_floats + (v >> 2) * 64 +
+                                       col * 4 + (v & 3)];
+                float p0 = p[0], p1 = glu ? p[32] : 0.0f;
+                if constexpr (X32) {
+                    p0 += p[1];
+                    if (glu) p1 += p[33];
                 }
+                if (kw > 1) {
+                    p0 += dpp<0xB1, 0xF>(p0);
+                    p1 += dpp<0xB1, 0xF>(p1);
+                }
+                if (kw > 2) {
+                    p0 += dpp<0x4E, 0xF>(p0);
+                    p1 += dpp<0x4E, 0xF>(p1);
+                }
+                if (kw > 4) {
+                    p0 += dpp<0x141, 0xF>(p0);
+                    p1 += dpp<0x141, 0xF>(p1);
+                }
+                const int yr = use_row[seg][r];
+                if ((it & (kw - 1)) != 0 || yr < 0) continue;
                 const float y = glu ? silu_up(p0, p1) : p0;
                 const int64_t at = int64_t(yr) * C.ldy + o;
                 if (C.y_type == PM_F32) store_f32<PM_F32>(C.y, at, y);
