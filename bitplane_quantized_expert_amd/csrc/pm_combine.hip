@@ -11,20 +11,58 @@ namespace pm {
 
 namespace {
 
-template <int ZT, int YT>
+// y[t][c] = sum_j w[t][j] z[t * top_k + j][c]: bound by reading z once.  A
+// wave takes 64 * V adjacent columns of one token, so that the weights are
+// scalars; V elements are 16 bytes of z (rows need no alignment beyond their
+// element's: the hardware splits the accesses that cross a line).  U rows are
+// on their way together.
+template <int ZT, int YT, int U>
 __global__ __launch_bounds__(256) void combine_uses_kernel(int n_tokens, int top_k, int hidden,
-                                                           const void* z, int64_t ldz,
+                                                           int chunks, const void* z, int64_t ldz,
                                                            const float* w, void* y, int64_t ldy) {
-    const size_t n = size_t(n_tokens) * hidden;
-    const size_t i = size_t(blockIdx.x) * 256 + threadIdx.x;
-    if (i >= n) return;
-    const size_t t = i / hidden, c = i % hidden;
-    float s = 0.0f;
-    for (int j = 0; j < top_k; ++j) {
-        const float wj = w[t * top_k + j];
-        if (wj != 0.0f) s = fmaf(wj, load_f32<ZT>(z, (t * top_k + j) * ldz + c), s);
+    constexpr int V = ZT == PM_F32 ? 4 : 8, ZB = ZT == PM_F32 ? 4 : 2, YB = YT == PM_F32 ? 4 : 2;
+    const int64_t id = int64_t(blockIdx.x) * 4 + uni(threadIdx.x >> 6);
+    const int64_t t = id / chunks;
+    if (t >= n_tokens) return;
+    // (lanes past the row stay: each holds one weight)
+    const int c = min((int(id - t * chunks) * kWave + int(threadIdx.x & 63)) * V, hidden - 1);
+    // the last columns of a row are taken as a whole vector that ends there;
+    // rows of fewer columns element by element
+    const bool whole = hidden >= V;
+    const int c0 = whole ? min(c, hidden - V) : c;
+    const char* zp = static_cast<const char*>(z) + (t * top_k * ldz + c0) * ZB;
+    const float* wp = w + t * top_k;
+    float s[V] = {};
+    if (whole) {
+        for (int j0 = 0; j0 < top_k; j0 += U) {
+            uint32_t d[U][4];
+            const int jl = j0 + int(threadIdx.x & 63);
+            const float wl = jl < top_k ? wp[jl] : 0.0f;
+#pragma unroll
+            for (int k = 0; k < U; ++k)
+                __builtin_memcpy(d[k], zp + min(j0 + k, top_k - 1) * ldz * ZB, 16);
+#pragma unroll
+            for (int k = 0; k < U; ++k) {
+                const float wj = __builtin_bit_cast(
+                    float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, wl), k));
+                if (wj != 0.0f) {
+#pragma unroll
+                    for (int i = 0; i < V; ++i) s[i] = fmaf(wj, load_f32<ZT>(d[k], i), s[i]);
+                }
+            }
+        }
+        alignas(16) char o[V * YB];
+#pragma unroll
+        for (int i = 0; i < V; ++i) store_f32<YT>(o, i, s[i]);
+        __builtin_memcpy(static_cast<char*>(y) + (t * ldy + c0) * YB, o, V * YB);
+        return;
     }
-    store_f32<YT>(y, t * ldy + c, s);
+    for (int i = 0; i < hidden - c0; ++i) {
+        float v = 0.0f;
+        for (int j = 0; j < top_k; ++j)
+            if (wp[j] != 0.0f) v = fmaf(wp[j], load_f32<ZT>(zp + j * ldz * ZB, i), v);
+        store_f32<YT>(y, t * ldy + c0 + i, v);
+    }
 }
 
 // One thread per group of inputs of one row.
@@ -85,9 +123,16 @@ hipError_t launch_encode_w4(size_t n_groups, int group, const void* w, int type,
 template <int ZT, int YT>
 static hipError_t combine_typed(int n_tokens, int top_k, int hidden, const void* z, int64_t ldz,
                                 const float* w, void* y, int64_t ldy, hipStream_t st) {
-    const size_t n = size_t(n_tokens) * hidden;
-    hipLaunchKernelGGL((combine_uses_kernel<ZT, YT>), dim3(grid_for(n, 256)), dim3(256), 0, st,
-                       n_tokens, top_k, hidden, z, ldz, w, y, ldy);
+    const int per_wave = kWave * (ZT == PM_F32 ? 4 : 8);
+    const int chunks = (hidden + per_wave - 1) / per_wave;
+    const dim3 grid(unsigned((int64_t(n_tokens) * chunks + 3) / 4));
+    // all rows of a token together where they are 10 at most
+    auto* f = &combine_uses_kernel<ZT, YT, 8>;
+    if (top_k <= 2) f = &combine_uses_kernel<ZT, YT, 2>;
+    else if (top_k <= 4) f = &combine_uses_kernel<ZT, YT, 4>;
+    else if (top_k == 9 || top_k == 10) f = &combine_uses_kernel<ZT, YT, 10>;
+    hipLaunchKernelGGL(f, grid, dim3(256), 0, st, n_tokens, top_k, hidden, chunks, z, ldz, w, y,
+                       ldy);
     return hipGetLastError();
 }
 

@@ -21,7 +21,8 @@ struct RouteCall {
     float* w;
     int32_t* offsets;              // null: no sorting
     int32_t* order;
-    uint16_t* hist;                // workspace [blocks][n_experts]
+    uint16_t* hist;                // workspace [blocks][hist_stride]
+    int32_t hist_stride;           // n_experts, or one more to be even
     int32_t n_tokens, n_experts, top_k, type;
     int32_t block_tokens, n_blocks;   // tokens per histogram block, blocks
 };

@@ -457,7 +457,7 @@ pm_status pm_grouped_gemm_w4(pm_grouped_shape s, int group, const uint8_t* d_q,
 pm_status pm_encode_w4_device(pm_matrix_shape s, const void* d_w, int type, uint8_t* d_q,
                               uint16_t* d_scales, uint8_t* d_zeros, void* stream);
 /* y[t] = sum_j w[t][j] * z[t * top_k + j], the terms added in slot order in
- * fp32.  A term of weight 0 is left out and its row not read (a slot that
+ * fp32.  A term of weight 0 is left out, whatever its row holds (a slot that
  * the router left empty).  z: n_tokens * top_k rows of `hidden`, ldz apart,
  * of z_type; y: fp32 or z_type.  z and y may not overlap (PM_ERR_ARG). */
 pm_status pm_combine_uses(int n_tokens, int top_k, int hidden, const void* d_z, int z_type,
