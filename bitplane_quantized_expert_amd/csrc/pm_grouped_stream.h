@@ -53,6 +53,7 @@ namespace pm {
 struct StreamPlan {
     int kw_log, panels, row_tiles;
     int rows_per_tile;             // sorted rows of a tile: 16 * MT, halved for fp32 x
+    int vec;                       // y takes 4 elements at a time
 };
 
 namespace {
@@ -137,36 +138,42 @@ __device__ inline int wave_scan(int v) {
 }
 
 // The tiles of `mt` sorted rows of all experts, by one wave without LDS: a
-// lane holds the count of its run of adjacent experts and of those before.
+// lane holds the count of its run of `per` adjacent experts and of those
+// before.
 struct TileScan {
-    int before, mine, total;
+    int before, mine, total, per;
 };
 
-// Tiles of experts e .. e + 7 below `end`, their offsets loaded together.
-__device__ inline void tiles_of_8(const GroupedCall& C, int mt, int e, int end, int* tiles,
-                                  int* row0, int* n) {
+// 8 adjacent experts' offsets, loaded together.
+struct Eight {
     int o[9];
+};
+__device__ inline Eight load_eight(const GroupedCall& C, int e) {
+    Eight r;
 #pragma unroll
-    for (int k = 0; k < 9; ++k) o[k] = C.offsets[min(e + k, C.n_experts)];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-        row0[k] = min(max(o[k], 0), C.n_rows);
-        n[k] = e + k < end ? max(min(o[k + 1], C.n_rows) - row0[k], 0) : 0;
-        tiles[k] = (n[k] + mt - 1) / mt;
-    }
+    for (int k = 0; k < 9; ++k) r.o[k] = C.offsets[min(e + k, C.n_experts)];
+    return r;
+}
+// First row and rows of expert e + k of them, none from `end` on.
+__device__ inline RowRange range_of(const GroupedCall& C, const Eight& s, int e, int k, int end) {
+    RowRange r;
+    r.row0 = min(max(s.o[k], 0), C.n_rows);
+    r.n = e + k < end ? max(min(s.o[k + 1], C.n_rows) - r.row0, 0) : 0;
+    return r;
 }
 
-__device__ inline TileScan scan_tiles(const GroupedCall& C, int mt) {
+__device__ inline TileScan scan_tiles(const GroupedCall& C, int mt, Eight* first) {
     const int lane = threadIdx.x & 63;
-    const int per = (C.n_experts + kWave - 1) / kWave;
-    const int e0 = min(lane * per, C.n_experts), e1 = min(e0 + per, C.n_experts);
     TileScan s;
+    s.per = (C.n_experts + kWave - 1) / kWave;
+    const int e0 = lane * s.per, e1 = min(e0 + s.per, C.n_experts);
     s.mine = 0;
-    for (int b = 0; b < per; b += 8) {
-        int tiles[8], row0[8], n[8];
-        tiles_of_8(C, mt, e0 + b, e1, tiles, row0, n);
+    for (int b = 0; b < s.per; b += 8) {
+        const Eight o = load_eight(C, e0 + b);
+        if (b == 0) *first = o;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) s.mine += tiles[k];
+        for (int k = 0; k < 8; ++k)
+            s.mine += (range_of(C, o, e0 + b, k, e1).n + mt - 1) / mt;
     }
     const int incl = wave_scan(s.mine);
     s.before = incl - s.mine;
@@ -175,29 +182,31 @@ __device__ inline TileScan scan_tiles(const GroupedCall& C, int mt) {
 }
 
 // Row tile i < total: its expert, first row and rows, the same in every lane.
+// `known`: the lanes' first 8 experts, where they are at hand.
 struct TileRows {
     int e, row0, n;
 };
-__device__ inline TileRows find_tile_rows(const GroupedCall& C, int mt, const TileScan& s, int i) {
+__device__ inline TileRows find_tile_rows(const GroupedCall& C, int mt, const TileScan& s, int i,
+                                          const Eight* known) {
     const int lane = threadIdx.x & 63;
-    const int per = (C.n_experts + kWave - 1) / kWave;
-    const int e0 = min(lane * per, C.n_experts), e1 = min(e0 + per, C.n_experts);
+    const int e0 = lane * s.per, e1 = min(e0 + s.per, C.n_experts);
     const uint64_t hit = __ballot(i >= s.before && i < s.before + s.mine);
     TileRows r{0, 0, 0};
     if (!hit) return r;                                   // (bad offsets only)
     int at = s.before;
-    for (int b = 0; b < per; b += 8) {
-        int tiles[8], row0[8], n[8];
-        tiles_of_8(C, mt, e0 + b, e1, tiles, row0, n);
+    for (int b = 0; b < s.per; b += 8) {
+        const Eight o = known && b == 0 ? *known : load_eight(C, e0 + b);
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-            if (i >= at && i < at + tiles[k]) {
+            const RowRange g = range_of(C, o, e0 + b, k, e1);
+            const int tiles = (g.n + mt - 1) / mt;
+            if (i >= at && i < at + tiles) {
                 const int skip = (i - at) * mt;
                 r.e = e0 + b + k;
-                r.row0 = row0[k] + skip;
-                r.n = min(n[k] - skip, mt);
+                r.row0 = g.row0 + skip;
+                r.n = min(g.n - skip, mt);
             }
-            at += tiles[k];
+            at += tiles;
         }
     }
     const int l = __builtin_ctzll(hit);
@@ -259,6 +268,11 @@ __device__ inline u32x4 pack_codes(const _Float16* h) {
     return r;
 }
 
+// Where the sum of column v lies in a row tile's [columns][16] of LDS: the 4
+// columns that a lane holds are turned against those of its neighbours, so
+// that a wave's writes fall in distinct banks.
+__device__ inline int sum_at(int v) { return (v >> 2) * 64 + (((v & 3) + (v >> 2)) & 3) * 16; }
+
 // f(0), .., f(N - 1) with constant arguments.
 template <int N, int I = 0, class F>
 __device__ inline void steps_to(F&& f) {
@@ -281,7 +295,7 @@ __global__ __launch_bounds__(kStreamThreads, 2) void stream_kernel(const Grouped
     // (as many as 256 registers hold beside the activations)
     constexpr int kSlots =
         GM == kAnyGroup || (GM == kGroup32 && KB == 4) || kLoads * MT > 8 ? 2 : 4;
-    // sums of a chunk: [buffer][wave][row tile][columns of x / 4][16][4], room
+    // sums of a chunk: [buffer][wave][row tile][column of x][16], room
     // for 4 row tiles of all columns; the buffer to be filled next holds the
     // converted activations before
     constexpr int kPart = kSteps * MT * 256;
@@ -296,23 +310,36 @@ __global__ __launch_bounds__(kStreamThreads, 2) void stream_kernel(const Grouped
     const int out = glu ? C.rows / 2 : C.rows;
     const int per_tile = glu ? 8 : 16;
 
-    const TileScan scan = scan_tiles(C, P.rows_per_tile);
+    Eight eight;
+    const TileScan scan = scan_tiles(C, P.rows_per_tile, &eight);
+    // Few groups: a whole number of workgroups each, which costs up to 1 part
+    // in 8 of the workgroups but no workgroup prepares two groups' rows
+    // (that takes as long as some 6 row tiles of 32 KiB).  Else equal parts of
+    // the sequence.
+    const int wps = scan.total > 0 ? int(gridDim.x) / scan.total : 0;
+    const bool apart = wps >= 8;
     const int64_t all = int64_t(scan.total) * P.row_tiles;
-    int64_t pos = all * blockIdx.x / gridDim.x;
-    const int64_t end = all * (blockIdx.x + 1) / gridDim.x;
+    int64_t pos = all * blockIdx.x / gridDim.x, end = all * (blockIdx.x + 1) / gridDim.x;
+    if (apart) {
+        const int s = int(blockIdx.x) / wps, k = int(blockIdx.x) % wps;
+        pos = int64_t(s) * P.row_tiles + int64_t(P.row_tiles) * k / wps;
+        end = s < scan.total ? int64_t(s) * P.row_tiles + int64_t(P.row_tiles) * (k + 1) / wps : pos;
+    }
+    if (pos >= end) return;
+    TileRows g = find_tile_rows(C, P.rows_per_tile, scan, int(pos / P.row_tiles), &eight);
 
     const uint32_t row_bytes = KIND == kW4 ? uint32_t(C.cols) / 2 : uint32_t(C.cols) * 2;
     const size_t w_bytes = size_t(C.rows) * row_bytes;
     const int ng = KIND == kW4 ? C.cols / C.group : 0;
     const CodeBits bits = code_bits();
     int buf = 0, seg = 0;
-    while (pos < end) {
+    for (;;) {
         const int mt = int(pos / P.row_tiles);
         const int rt0 = int(pos - int64_t(mt) * P.row_tiles);
         const int rt1 = int(min(int64_t(P.row_tiles), rt0 + (end - pos)));
         pos += rt1 - rt0;
-        const TileRows g = find_tile_rows(C, P.rows_per_tile, scan, mt);
-        if (g.n <= 0) continue;                           // (bad offsets only)
+        // loads return in order: the uses come before any weights
+        const int u_lane = lane < g.n ? use_of(C, g.row0 + lane) : -1;
 
         const auto wbuf = __builtin_amdgcn_make_buffer_rsrc(
             uni_ptr(const_cast<char*>(static_cast<const char*>(C.w)) + size_t(g.e) * w_bytes), 0,
@@ -404,14 +431,13 @@ __global__ __launch_bounds__(kStreamThreads, 2) void stream_kernel(const Grouped
             }
             issue(slot, rt0 + (step + c) * rw + rg, panel);
         };
-        steps_to<kSlots - 1>([&](auto c) { issue(c, rt0 + c * rw + rg, 0); });
+        issue(std::integral_constant<int, 0>{}, rt0 + rg, 0);
 
         // ---- activations of this wave's inputs, as matrix operands.  Column v
         // is row v, or the value (even v) or rest (odd v) of fp32 row v / 2
         const int nv = X32 ? 2 * g.n : g.n;
         int vlog = 2;
         while ((1 << vlog) < nv) ++vlog;
-        const int u_lane = lane < g.n ? use_of(C, g.row0 + lane) : -1;
         if (wv == 0 && lane < g.n)
             use_row[seg][lane] =
                 u_lane < 0 ? -1 : (C.flags & PM_GROUPED_SCATTER ? u_lane : g.row0 + lane);
@@ -422,7 +448,26 @@ __global__ __launch_bounds__(kStreamThreads, 2) void stream_kernel(const Grouped
             const int64_t xr = u < 0 ? 0 : gather ? u / C.top_k : g.row0 + r;
             return static_cast<const char*>(C.x) + xr * C.ldx * (X32 ? 4 : 2);
         };
-        auto load_x = [&](int panel) {
+        // kRaw rows of x from row rb on, this lane's 8 inputs of the panel
+        constexpr int kRaw = KIND != kW4 ? 1 : X32 ? 2 : 4;
+        RawX<X32> raw[kRaw];
+        auto load_raw = [&](int panel, int rb) {
+            const int c = first_block(panel) * 128 + lane * 8;
+            const bool in = rg == 0 && lane < KB * 16 && c < C.cols;
+#pragma unroll
+            for (int k = 0; k < kRaw; ++k) {
+                const int r = min(rb + k, g.n - 1);
+                const int u = __builtin_amdgcn_readlane(u_lane, r);
+                const char* p = x_row(u, r) + size_t(max(min(c, C.cols - 8), 0)) * (X32 ? 4 : 2);
+#pragma unroll
+                for (int h = 0; h < (X32 ? 2 : 1); ++h) {
+                    const u32x4 d = *reinterpret_cast<const u32x4*>(p + 16 * h);
+                    raw[k].d[h] = in && u >= 0 ? d : u32x4{0, 0, 0, 0};
+                }
+            }
+        };
+        // (first: the first rows of panel 0 are in `raw` already)
+        auto load_x = [&](int panel, bool first) {
             const int c0 = first_block(panel) * 128;       // the wave's inputs
             if constexpr (KIND != kW4) {
 #pragma unroll
@@ -448,30 +493,16 @@ __global__ __launch_bounds__(kStreamThreads, 2) void stream_kernel(const Grouped
                 const bool bf16 = C.x_type == PM_BF16;
                 const bool scaled = X32 || bf16;
                 for (int v0 = 0; v0 < nv; v0 += vper) {
-                    const int r0 = X32 ? v0 >> 1 : v0;
-                    const int c = c0 + lane * 8;
-                    const bool mine = rg == 0 && lane < KB * 16;
-                    // 4 rows of x are on their way together
+                    const int r0 = X32 ? v0 >> 1 : v0, r1 = min(r0 + rper, g.n);
 #pragma unroll 1
-                    for (int rb = r0; rg == 0 && rb < min(r0 + rper, g.n); rb += 4) {
-                        RawX<X32> raw[4];
+                    for (int rb = r0; rg == 0 && rb < r1; rb += kRaw) {
+                        if (!(first && rb == 0)) load_raw(panel, rb);
+#pragma unroll 1
+                        for (int r = rb; r < min(rb + kRaw, r1); ++r) {
+                            const F8 x = widen<X32>(raw[0], bf16);
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const int u = __builtin_amdgcn_readlane(u_lane, min(rb + k, g.n - 1));
-                            const char* p = x_row(u, min(rb + k, g.n - 1)) +
-                                            size_t(min(c, C.cols - 8)) * (X32 ? 4 : 2);
-                            const bool ok = u >= 0 && c < C.cols && mine;
-#pragma unroll
-                            for (int h = 0; h < (X32 ? 2 : 1); ++h) {
-                                const u32x4 d = *reinterpret_cast<const u32x4*>(p + 16 * h);
-                                raw[k].d[h] = ok ? d : u32x4{0, 0, 0, 0};
-                            }
-                        }
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const int v = X32 ? 2 * (rb + k) : rb + k;
-                            if (rb + k >= min(r0 + rper, g.n)) break;
-                            const F8 x = widen<X32>(raw[k], bf16);
+                            for (int k = 0; k + 1 < kRaw; ++k) raw[k] = raw[k + 1];
+                            const int v = X32 ? 2 * r : r;
                             float up = 1.0f, down = 1.0f;
                             if (scaled) {
                                 float big = 0.0f;
@@ -495,7 +526,7 @@ __global__ __launch_bounds__(kStreamThreads, 2) void stream_kernel(const Grouped
                                                                : _Float16(0.0f);
                             }
                             char* at = stage + (size_t(v - v0) * width + (ks * KB * 128) + lane * 8) * 2;
-                            if (mine) {
+                            if (lane < KB * 16) {
                                 *reinterpret_cast<u32x4*>(at) = pack_codes(hi);
                                 if constexpr (X32)
                                     *reinterpret_cast<u32x4*>(at + size_t(width) * 2) = pack_codes(lo);
@@ -527,6 +558,12 @@ __global__ __launch_bounds__(kStreamThreads, 2) void stream_kernel(const Grouped
                 }
             }
         };
+        if constexpr (KIND == kW4) {
+            if (C.cols > 0) load_raw(0, 0);
+        }
+        steps_to<kSlots - 2>([&](auto c) {
+            issue(std::integral_constant<int, c + 1>{}, rt0 + (c + 1) * rw + rg, 0);
+        });
 
         auto multiply = [&](auto slot, int panel, f32x4* a) {
             constexpr int S = decltype(slot)::value;
@@ -599,6 +636,7 @@ __global__ __launch_bounds__(kStreamThreads, 2) void stream_kernel(const Grouped
         // row tiles of a wave per chunk, and floats of one
         const int clog = P.panels > 1 ? 2 : min(4, 6 + MT - 1 - vlog);
         const int tile_floats = 16 << vlog;
+        if (C.cols > 0) load_x(0, true);
         bool first = true;
         for (int rtb = rt0, step = 0; rtb < rt1; rtb += rw << clog) {
             int here = 0;                                  // row tiles of the chunk so far
@@ -608,7 +646,7 @@ __global__ __launch_bounds__(kStreamThreads, 2) void stream_kernel(const Grouped
 #pragma unroll
                     for (int m = 0; m < MT; ++m) acc[c][m] = f32x4{0.f, 0.f, 0.f, 0.f};
                 for (int panel = 0; panel < P.panels; ++panel) {
-                    if (C.cols > 0 && (P.panels > 1 || first)) load_x(panel);
+                    if (P.panels > 1 && !first) load_x(panel, false);
                     first = false;
                     steps_to<kSteps>([&](auto c) {
                         constexpr int kNext = (c + kSlots - 1) % kSlots;
@@ -624,56 +662,54 @@ __global__ __launch_bounds__(kStreamThreads, 2) void stream_kernel(const Grouped
                 for (int c = 0; c < kSteps; ++c)
 #pragma unroll
                     for (int m = 0; m < MT; ++m)
-                        if (m * 16 + 4 * q < 1 << vlog)
-                            *reinterpret_cast<f32x4*>(
-                                &part[buf][wv][(here + c) * tile_floats + m * 256 + lane * 4]) =
-                                acc[c][m];
+                        if (m * 16 + 4 * q < 1 << vlog) {
+#pragma unroll
+                            for (int r = 0; r < 4; ++r)
+                                part[buf][wv][(here + c) * tile_floats + sum_at(m * 16 + 4 * q + r) +
+                                              i16] = acc[c][m][r];
+                        }
                 here += kSteps;
                 step += kSteps;
             } while (here < 1 << clog && rtb + here * rw < rt1);
             // LDS only: the weights under way are not waited for
             asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-            // kw adjacent lanes per output, one for each wave's part
-            const int items = (rw << clog) << (nlog + plog + P.kw_log);
+            // 4 adjacent outputs of a row per thread
+            const int items = (rw << clog) << (nlog + plog - 2);
 #pragma unroll 1
             for (int it = threadIdx.x; it < items; it += kStreamThreads) {
-                const int item = it >> P.kw_log;
-                const int col = item & ((1 << plog) - 1);
-                const int r = (item >> plog) & ((1 << nlog) - 1), t = item >> (plog + nlog);
+                const int col = (it & ((1 << plog) / 4 - 1)) * 4;
+                const int r = (it >> (plog - 2)) & ((1 << nlog) - 1), t = it >> (plog - 2 + nlog);
                 const int rt = rtb + t, o = rt * per_tile + col;
                 if (r >= g.n || rt >= rt1 || o >= out) continue;
-                const int v = X32 ? 2 * r : r;
-                const float* p = &part[buf][((t & (rw - 1)) << P.kw_log) + (it & (kw - 1))]
-                                      [(t >> (3 - P.kw_log)) * tile_floats + (v >> 2) * 64 +
-                                       col * 4 + (v & 3)];
-                float p0 = p[0], p1 = glu ? p[32] : 0.0f;
-                if constexpr (X32) {
-                    p0 += p[1];
-                    if (glu) p1 += p[33];
-                }
-                if (kw > 1) {
-                    p0 += dpp<0xB1, 0xF>(p0);
-                    p1 += dpp<0xB1, 0xF>(p1);
-                }
-                if (kw > 2) {
-                    p0 += dpp<0x4E, 0xF>(p0);
-                    p1 += dpp<0x4E, 0xF>(p1);
-                }
-                if (kw > 4) {
-                    p0 += dpp<0x141, 0xF>(p0);
-                    p1 += dpp<0x141, 0xF>(p1);
-                }
                 const int yr = use_row[seg][r];
-                if ((it & (kw - 1)) != 0 || yr < 0) continue;
-                const float y = glu ? silu_up(p0, p1) : p0;
+                if (yr < 0) continue;
+                const int v = X32 ? 2 * r : r;
+                const float* p = &part[buf][(t & (rw - 1)) << P.kw_log]
+                                      [(t >> (3 - P.kw_log)) * tile_floats + col];
+                const int a0 = sum_at(v), a1 = sum_at(v + 1);
+                f32x4 p0 = {0.f, 0.f, 0.f, 0.f}, p1 = p0;
+#pragma unroll 2
+                for (int k = 0; k < kw; ++k, p += kPart) {
+                    p0 += *reinterpret_cast<const f32x4*>(p + a0);
+                    if constexpr (X32) p0 += *reinterpret_cast<const f32x4*>(p + a1);
+                    if (glu) {
+                        p1 += *reinterpret_cast<const f32x4*>(p + a0 + 8);
+                        if constexpr (X32) p1 += *reinterpret_cast<const f32x4*>(p + a1 + 8);
+                    }
+                }
+                float y[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) y[i] = glu ? silu_up(p0[i], p1[i]) : p0[i];
                 const int64_t at = int64_t(yr) * C.ldy + o;
-                if (C.y_type == PM_F32) store_f32<PM_F32>(C.y, at, y);
-                else if (C.y_type == PM_F16) store_f32<PM_F16>(C.y, at, y);
-                else store_f32<PM_BF16>(C.y, at, y);
+                if (C.y_type == PM_F32) store4<PM_F32>(C.y, at, out - o, P.vec, y);
+                else if (C.y_type == PM_F16) store4<PM_F16>(C.y, at, out - o, P.vec, y);
+                else store4<PM_BF16>(C.y, at, out - o, P.vec, y);
             }
             buf ^= 1;
         }
         seg ^= 1;
+        if (pos >= end) break;
+        g = find_tile_rows(C, P.rows_per_tile, scan, mt + 1, nullptr);
     }
 #endif
 }
@@ -701,6 +737,7 @@ inline StreamPlan plan_stream(const GroupedCall& C, bool x32, int mt, int* kb) {
     const int per_tile = C.flags & PM_GROUPED_SWIGLU ? 8 : 16;
     P.row_tiles = (out + per_tile - 1) / per_tile;
     P.rows_per_tile = 16 * mt / (x32 ? 2 : 1);
+    P.vec = stores_by_4(C);
     return P;
 }
 

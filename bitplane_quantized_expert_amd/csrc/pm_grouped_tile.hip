@@ -61,26 +61,6 @@ __device__ inline f32x4 mfma16(const u32x4& a, const u32x4& b, const f32x4& c) {
                                                        __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
 }
 
-// Four adjacent outputs of row y + at, those below `left`.
-template <int YT>
-__device__ inline void store4(void* y, int64_t at, int left, bool vec, const float* v) {
-    if (vec && left >= 4) {
-        if constexpr (YT == PM_F32) {
-            *reinterpret_cast<f32x4*>(static_cast<float*>(y) + at) = f32x4{v[0], v[1], v[2], v[3]};
-        } else {
-            uint16_t h[4];
-#pragma unroll
-            for (int r = 0; r < 4; ++r) store_f32<YT>(h, r, v[r]);
-            *reinterpret_cast<uint64_t*>(static_cast<uint16_t*>(y) + at) =
-                uint64_t(h[0]) | uint64_t(h[1]) << 16 | uint64_t(h[2]) << 32 | uint64_t(h[3]) << 48;
-        }
-        return;
-    }
-#pragma unroll
-    for (int r = 0; r < 4; ++r)
-        if (r < left) store_f32<YT>(y, at + r, v[r]);
-}
-
 template <int WT, int YT, bool GLU>
 __global__ __launch_bounds__(kTileThreads, 2) void tile_kernel(const GroupedCall C, int nt,
                                                                bool vec) {
@@ -324,8 +304,7 @@ hipError_t run_tiles(const GroupedCall& C, hipStream_t st) {
     auto* f = tile_kernel<WT, YT, GLU>;
     hipError_t e = allow_lds(reinterpret_cast<const void*>(f), kTileMaxLds);
     if (e != hipSuccess) return e;
-    const int align = 4 * int(type_bytes(YT));
-    const bool vec = reinterpret_cast<uintptr_t>(C.y) % align == 0 && C.ldy % 4 == 0;
+    const bool vec = stores_by_4(C);
     const int64_t tiles = (int64_t(std::min(C.n_rows, C.n_experts)) + C.n_rows / kTileM) * nt;
     const unsigned grid = unsigned(std::min<int64_t>(tiles, compute_units()));
     hipLaunchKernelGGL(f, dim3(grid), dim3(kTileThreads), lds, st, C, nt, vec);
