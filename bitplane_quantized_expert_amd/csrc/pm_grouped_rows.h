@@ -24,6 +24,12 @@ __device__ inline RowRange group_rows(const GroupedCall& C, int e) {
     return r;
 }
 
+// The number of row tiles of mt rows, no more than offsets that do not
+// decrease can give, so that others end as soon.
+__device__ inline int most_tiles(const GroupedCall& C, int mt, int total) {
+    return min(max(total, 0), min(C.n_experts, C.n_rows) + C.n_rows / mt);
+}
+
 // The use of sorted row i (-1: left out).
 __device__ inline int use_of(const GroupedCall& C, int i) {
     if (!C.order) return i;
@@ -86,7 +92,7 @@ __device__ inline int tile_table(const GroupedCall& C, int mt, int* before) {
         at += (group_rows(C, e).n + mt - 1) / mt;
     }
     if (threadIdx.x == 0) before[C.n_experts] = total;
-    return uni(total);
+    return uni(most_tiles(C, mt, total));
 }
 
 // The expert of row tile i < total: the last e with before[e] <= i.  Two

@@ -52,7 +52,6 @@ namespace pm {
 // KW * KB * 128 inputs, row tiles of a matrix.
 struct StreamPlan {
     int kw_log, panels, row_tiles;
-    int rows_per_tile;             // sorted rows of a tile: 16 * MT, halved for fp32 x
     int vec;                       // y takes 4 elements at a time
 };
 
@@ -137,7 +136,7 @@ __device__ inline int wave_scan(int v) {
     return v;
 }
 
-// The tiles of `mt` sorted rows of all experts, by one wave without LDS: a
+// The tiles of MTILE (a power of two) sorted rows of all experts, by one wave without LDS: a
 // lane holds the count of its run of `per` adjacent experts and of those
 // before.
 struct TileScan {
@@ -162,7 +161,8 @@ __device__ inline RowRange range_of(const GroupedCall& C, const Eight& s, int e,
     return r;
 }
 
-__device__ inline TileScan scan_tiles(const GroupedCall& C, int mt, Eight* first) {
+template <int MTILE>
+__device__ inline TileScan scan_tiles(const GroupedCall& C, Eight* first) {
     const int lane = threadIdx.x & 63;
     TileScan s;
     s.per = (C.n_experts + kWave - 1) / kWave;
@@ -173,11 +173,11 @@ __device__ inline TileScan scan_tiles(const GroupedCall& C, int mt, Eight* first
         if (b == 0) *first = o;
 #pragma unroll
         for (int k = 0; k < 8; ++k)
-            s.mine += (range_of(C, o, e0 + b, k, e1).n + mt - 1) / mt;
+            s.mine += (range_of(C, o, e0 + b, k, e1).n + MTILE - 1) / MTILE;
     }
     const int incl = wave_scan(s.mine);
     s.before = incl - s.mine;
-    s.total = __builtin_amdgcn_readlane(incl, 63);
+    s.total = most_tiles(C, MTILE, __builtin_amdgcn_readlane(incl, 63));
     return s;
 }
 
@@ -186,7 +186,8 @@ __device__ inline TileScan scan_tiles(const GroupedCall& C, int mt, Eight* first
 struct TileRows {
     int e, row0, n;
 };
-__device__ inline TileRows find_tile_rows(const GroupedCall& C, int mt, const TileScan& s, int i,
+template <int MTILE>
+__device__ inline TileRows find_tile_rows(const GroupedCall& C, const TileScan& s, int i,
                                           const Eight* known) {
     const int lane = threadIdx.x & 63;
     const int e0 = lane * s.per, e1 = min(e0 + s.per, C.n_experts);
@@ -199,12 +200,12 @@ __device__ inline TileRows find_tile_rows(const GroupedCall& C, int mt, const Ti
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
             const RowRange g = range_of(C, o, e0 + b, k, e1);
-            const int tiles = (g.n + mt - 1) / mt;
+            const int tiles = (g.n + MTILE - 1) / MTILE;
             if (i >= at && i < at + tiles) {
-                const int skip = (i - at) * mt;
+                const int skip = (i - at) * MTILE;
                 r.e = e0 + b + k;
                 r.row0 = g.row0 + skip;
-                r.n = min(g.n - skip, mt);
+                r.n = min(g.n - skip, MTILE);
             }
             at += tiles;
         }
@@ -311,22 +312,41 @@ __global__ __launch_bounds__(kStreamThreads, 2) void stream_kernel(const Grouped
     const int per_tile = glu ? 8 : 16;
 
     Eight eight;
-    const TileScan scan = scan_tiles(C, P.rows_per_tile, &eight);
+    // sorted rows of a tile: an fp32 row takes two columns
+    constexpr int kTileRows = 16 * MT / (X32 ? 2 : 1);
+    const TileScan scan = scan_tiles<kTileRows>(C, &eight);
     // Few groups: a whole number of workgroups each, which costs up to 1 part
     // in 8 of the workgroups but no workgroup prepares two groups' rows
     // (that takes as long as some 6 row tiles of 32 KiB).  Else equal parts of
     // the sequence.
     const int wps = scan.total > 0 ? int(gridDim.x) / scan.total : 0;
     const bool apart = wps >= 8;
-    const int64_t all = int64_t(scan.total) * P.row_tiles;
-    int64_t pos = all * blockIdx.x / gridDim.x, end = all * (blockIdx.x + 1) / gridDim.x;
+    // row tiles of the sequence, this workgroup's first and their number: the
+    // group mt, the row tile rt0 in it
+    int mt, rt0, left;
     if (apart) {
-        const int s = int(blockIdx.x) / wps, k = int(blockIdx.x) % wps;
-        pos = int64_t(s) * P.row_tiles + int64_t(P.row_tiles) * k / wps;
-        end = s < scan.total ? int64_t(s) * P.row_tiles + int64_t(P.row_tiles) * (k + 1) / wps : pos;
+        mt = int(blockIdx.x) / wps;
+        const int k = int(blockIdx.x) - mt * wps;
+        rt0 = int(int64_t(P.row_tiles) * k / wps);
+        left = mt < scan.total ? int(int64_t(P.row_tiles) * (k + 1) / wps) - rt0 : 0;
+    } else {
+        const uint64_t all = uint64_t(scan.total) * P.row_tiles;
+        const uint32_t b = blockIdx.x, n = gridDim.x;
+        uint64_t pos;
+        if (all >> 31 == 0) {                             // (64-bit divisions are long)
+            const uint32_t q0 = uint32_t(all) / n, rest = uint32_t(all) - q0 * n;
+            pos = q0 * b + min(b, rest);
+            left = int(q0) + (b < rest ? 1 : 0);
+            mt = int(uint32_t(pos) / uint32_t(P.row_tiles));
+        } else {
+            pos = all / n * b + min(uint64_t(b), all % n);
+            left = int(all / n) + (b < all % n ? 1 : 0);
+            mt = int(pos / P.row_tiles);
+        }
+        rt0 = int(pos - uint64_t(mt) * P.row_tiles);
     }
-    if (pos >= end) return;
-    TileRows g = find_tile_rows(C, P.rows_per_tile, scan, int(pos / P.row_tiles), &eight);
+    if (left <= 0) return;
+    TileRows g = find_tile_rows<kTileRows>(C, scan, mt, &eight);
 
     const uint32_t row_bytes = KIND == kW4 ? uint32_t(C.cols) / 2 : uint32_t(C.cols) * 2;
     const size_t w_bytes = size_t(C.rows) * row_bytes;
@@ -334,10 +354,8 @@ __global__ __launch_bounds__(kStreamThreads, 2) void stream_kernel(const Grouped
     const CodeBits bits = code_bits();
     int buf = 0, seg = 0;
     for (;;) {
-        const int mt = int(pos / P.row_tiles);
-        const int rt0 = int(pos - int64_t(mt) * P.row_tiles);
-        const int rt1 = int(min(int64_t(P.row_tiles), rt0 + (end - pos)));
-        pos += rt1 - rt0;
+        const int rt1 = min(P.row_tiles, rt0 + left);
+        left -= rt1 - rt0;
         // loads return in order: the uses come before any weights
         const int u_lane = lane < g.n ? use_of(C, g.row0 + lane) : -1;
 
@@ -708,15 +726,17 @@ __global__ __launch_bounds__(kStreamThreads, 2) void stream_kernel(const Grouped
             buf ^= 1;
         }
         seg ^= 1;
-        if (pos >= end) break;
-        g = find_tile_rows(C, P.rows_per_tile, scan, mt + 1, nullptr);
+        if (left <= 0) break;
+        rt0 = 0;
+        g = find_tile_rows<kTileRows>(C, scan, ++mt, nullptr);
     }
 #endif
 }
 
 template <int KIND, bool BF16, bool X32, int KB, int MT, int GM, bool ZEROS>
 hipError_t run_stream(const GroupedCall& C, const StreamPlan& P, hipStream_t st) {
-    const int64_t tiles = int64_t(std::min(C.n_rows, C.n_experts)) + C.n_rows / P.rows_per_tile;
+    const int64_t tiles =
+        int64_t(std::min(C.n_rows, C.n_experts)) + C.n_rows / (16 * MT / (X32 ? 2 : 1));
     const unsigned grid = unsigned(std::min<int64_t>(tiles * P.row_tiles, compute_units()));
     hipLaunchKernelGGL((stream_kernel<KIND, BF16, X32, KB, MT, GM, ZEROS>), dim3(grid),
                        dim3(kStreamThreads), 0, st, C, P);
@@ -725,7 +745,7 @@ hipError_t run_stream(const GroupedCall& C, const StreamPlan& P, hipStream_t st)
 
 // The split of the inputs: 4 blocks of 128 per wave where there are as many,
 // over up to 8 waves, then panels.
-inline StreamPlan plan_stream(const GroupedCall& C, bool x32, int mt, int* kb) {
+inline StreamPlan plan_stream(const GroupedCall& C, int mt, int* kb) {
     StreamPlan P{};
     const int blocks = std::max(1, (C.cols + 127) / 128);
     while (P.kw_log < 3 && (4 << P.kw_log) < blocks) ++P.kw_log;
@@ -736,7 +756,6 @@ inline StreamPlan plan_stream(const GroupedCall& C, bool x32, int mt, int* kb) {
     const int out = C.flags & PM_GROUPED_SWIGLU ? C.rows / 2 : C.rows;
     const int per_tile = C.flags & PM_GROUPED_SWIGLU ? 8 : 16;
     P.row_tiles = (out + per_tile - 1) / per_tile;
-    P.rows_per_tile = 16 * mt / (x32 ? 2 : 1);
     P.vec = stores_by_4(C);
     return P;
 }

@@ -8,7 +8,7 @@ namespace {
 template <bool BF16, int MT>
 hipError_t run16(const GroupedCall& C, hipStream_t st) {
     int kb;
-    const StreamPlan P = plan_stream(C, false, MT, &kb);
+    const StreamPlan P = plan_stream(C, MT, &kb);
     switch (kb) {
     case 1: return run_stream<kW16, BF16, false, 1, MT, kNoGroup, false>(C, P, st);
     case 2: return run_stream<kW16, BF16, false, 2, MT, kNoGroup, false>(C, P, st);

@@ -26,7 +26,7 @@ hipError_t run4_group(const GroupedCall& C, const StreamPlan& P, hipStream_t st)
 template <bool X32, int MT, bool ZEROS>
 hipError_t run4(const GroupedCall& C, hipStream_t st) {
     int kb;
-    const StreamPlan P = plan_stream(C, X32, MT, &kb);
+    const StreamPlan P = plan_stream(C, MT, &kb);
     switch (kb) {
     case 1: return run4_group<X32, 1, MT, ZEROS>(C, P, st);
     case 2: return run4_group<X32, 2, MT, ZEROS>(C, P, st);
