@@ -57,32 +57,44 @@ __device__ inline double row16_sum_f64(double v) {
     return v;
 }
 
-// The selection of one token by one wave: lane j < top_k gets the expert and
-// key of slot j (key 0: none).
+// Every 64th logit of token t, from logit `lane` on.
+template <int VPT>
+struct Logits {
+    float v[VPT];
+};
 template <int VPT, int TYPE>
-__device__ inline void select_topk(const RouteCall& C, int t, int lane, uint32_t* key_out,
-                                   int* id_out) {
-    uint32_t key[VPT];
+__device__ inline Logits<VPT> load_logits(const RouteCall& C, int t, int lane) {
+    Logits<VPT> l;
     const int64_t base = int64_t(t) * C.ld;
 #pragma unroll
-    for (int v = 0; v < VPT; ++v) {
-        const int e = v * kWave + lane;
-        key[v] = order_key(load_f32<TYPE>(C.logits, base + min(e, C.n_experts - 1)));
-        if (e >= C.n_experts) key[v] = 0;
-    }
+    for (int v = 0; v < VPT; ++v)
+        l.v[v] = load_f32<TYPE>(C.logits, base + min(v * kWave + lane, C.n_experts - 1));
+    return l;
+}
+
+// The selection of one token by one wave: lane j < top_k gets the expert and
+// key of slot j (key 0: none).
+template <int VPT>
+__device__ inline void select_topk(const RouteCall& C, const Logits<VPT>& logits, int lane,
+                                   uint32_t* key_out, int* id_out) {
+    uint32_t key[VPT];
+#pragma unroll
+    for (int v = 0; v < VPT; ++v)
+        key[v] = v * kWave + lane < C.n_experts ? order_key(logits.v[v]) : 0u;
     uint32_t m = key[0];
 #pragma unroll
     for (int v = 1; v < VPT; ++v) m = m > key[v] ? m : key[v];
-    // the largest bound that top_k lanes meet
+    // a bound that top_k lanes meet: the largest, or any that just top_k meet
     uint32_t bound = 0;
-#pragma unroll
-    for (int b = 31; b >= 0; --b) {
-        const uint32_t c = bound | 1u << b;
-        if (__popcll(__ballot(m >= c)) >= C.top_k) bound = c;
+    for (uint32_t bit = 1u << 31; bit; bit >>= 1) {
+        const uint32_t c = bound | bit;
+        const int n = __popcll(__ballot(m >= c));
+        if (n >= C.top_k) bound = c;
+        if (n == C.top_k) break;
     }
     bound = bound ? bound : 1u;
-    uint32_t mine = 0;                                      // sorted list across the lanes
-    int id = -1;
+    // list across the lanes, descending: (key, ~expert), 0 for none
+    uint32_t mine = 0, low = 0;
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
         uint64_t hit = __ballot(key[v] >= bound);
@@ -90,21 +102,22 @@ __device__ inline void select_topk(const RouteCall& C, int t, int lane, uint32_t
             const int l = __builtin_ctzll(hit);
             hit &= hit - 1;
             const uint32_t k = __builtin_amdgcn_readlane(key[v], l);
-            const int e = v * kWave + l;
-            // lanes that come after (k, e) take their neighbour's entry, the
-            // first of them the new one
-            const bool after = mine < k || (mine == k && id > e);
+            const uint32_t ne = ~uint32_t(v * kWave + l);
+            // lanes that come after it move up by one, the first takes it
+            const bool after = (uint64_t(mine) << 32 | low) < (uint64_t(k) << 32 | ne);
             const uint64_t mask = __ballot(after);
             if (mask == 0) continue;
             const int first = __builtin_ctzll(mask);
-            const uint32_t mk = __builtin_amdgcn_update_dpp(0, int(mine), 0x138, 0xF, 0xF, false);
-            const int mi = __builtin_amdgcn_update_dpp(0, id, 0x138, 0xF, 0xF, false);
-            mine = after ? (lane == first ? k : mk) : mine;
-            id = after ? (lane == first ? e : mi) : id;
+            if (after) {
+                mine = __builtin_amdgcn_update_dpp(int(mine), int(mine), 0x138, 0xF, 0xF, false);
+                low = __builtin_amdgcn_update_dpp(int(low), int(low), 0x138, 0xF, 0xF, false);
+            }
+            mine = lane == first ? k : mine;
+            low = lane == first ? ne : low;
         }
     }
     *key_out = lane < C.top_k ? mine : 0;
-    *id_out = lane < C.top_k && mine ? id : -1;
+    *id_out = lane < C.top_k && mine ? int(~low) : -1;
 }
 
 // ids and weights of tokens t0, t0 + step, .. of one wave; f(u, id) for each
@@ -113,13 +126,18 @@ template <int VPT, int TYPE, class F>
 __device__ inline void route_tokens(const RouteCall& C, int t0, int t1, int step, int lane, F&& f) {
     // up to 4 tokens share one softmax where 16 lanes hold a token's slots
     const int group = C.top_k <= 16 ? 4 : 1;
+    if (t0 >= t1) return;
+    Logits<VPT> next = load_logits<VPT, TYPE>(C, t0, lane);
     for (int t = t0; t < t1; t += group * step) {
         uint32_t key = 0, top = 0;
         int id = -1, tok = 0, slot = kWave;
         for (int s = 0; s < group && t + s * step < t1; ++s) {
             uint32_t k;
             int i;
-            select_topk<VPT, TYPE>(C, t + s * step, lane, &k, &i);
+            const Logits<VPT> now = next;
+            // the next token's logits are on their way meanwhile
+            next = load_logits<VPT, TYPE>(C, min(t + (s + 1) * step, t1 - 1), lane);
+            select_topk<VPT>(C, now, lane, &k, &i);
             const uint32_t first = __builtin_amdgcn_readlane(k, 0);
             if (group == 1) {
                 key = k;
@@ -169,8 +187,8 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(const RouteCall C)
     if (sort) {
         __syncthreads();
         uint16_t* row = C.hist + size_t(blockIdx.x) * C.hist_stride;
-        for (int e = threadIdx.x; e < C.n_experts; e += blockDim.x) row[e] = uint16_t(hist[e]);
-        if (threadIdx.x == 0 && C.hist_stride > C.n_experts) row[C.n_experts] = 0;
+        for (int e = threadIdx.x; e < C.hist_stride; e += blockDim.x)
+            row[e] = e < C.n_experts ? uint16_t(hist[e]) : uint16_t(0);
     }
 }
 
@@ -259,41 +277,58 @@ __global__ __launch_bounds__(kRouteThreads) void scatter_kernel(const RouteCall 
     __syncthreads();
     const int nb = subs / spb;
     const int b0 = blockIdx.x * nb;
-    // the columns, two experts per load, over slices of the blocks
-    const int pairs = C.hist_stride / 2;
-    int width = kWave;
-    while (width < pairs && width < kRouteThreads) width *= 2;
-    const int slices = kRouteThreads / width, slice = threadIdx.x / width;
-    const int len = (C.n_blocks + slices - 1) / slices;
-    const int first = slice * len, last = min(first + len, C.n_blocks);
-    const uint32_t* table = reinterpret_cast<const uint32_t*>(C.hist);
-    for (int c = threadIdx.x & (width - 1); c < pairs; c += width) {
-        uint32_t all[2] = {0, 0}, old[2] = {0, 0};
-#pragma unroll 16
-        for (int b = first; b < last; ++b) {
-            const uint32_t h = table[size_t(b) * pairs + c];
-            all[0] += h & 0xFFFFu;
-            all[1] += h >> 16;
-            old[0] += b < b0 ? h & 0xFFFFu : 0u;
-            old[1] += b < b0 ? h >> 16 : 0u;
+    // the columns: 8 experts per lane and load, the blocks over the waves, 8
+    // loads on their way
+    const int octs = C.hist_stride / 8;
+    const u32x4* table = reinterpret_cast<const u32x4*>(C.hist);
+    for (int c = lane; c - lane < octs; c += kWave) {
+        uint32_t all[8] = {}, old[8] = {};
+        for (int b = wv; b < C.n_blocks; b += 8 * kRouteWaves) {
+            u32x4 h[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                h[k] = table[size_t(min(b + k * kRouteWaves, C.n_blocks - 1)) * octs +
+                             min(c, octs - 1)];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const int at = b + k * kRouteWaves;
+                if (at >= C.n_blocks) break;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    all[2 * i] += h[k][i] & 0xFFFFu;
+                    all[2 * i + 1] += h[k][i] >> 16;
+                }
+                if (at < b0) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        old[2 * i] += h[k][i] & 0xFFFFu;
+                        old[2 * i + 1] += h[k][i] >> 16;
+                    }
+                }
+            }
         }
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
-            if (2 * c + k < E) {
-                atomicAdd(&total[2 * c + k], all[k]);
-                atomicAdd(&earlier[2 * c + k], old[k]);
+        for (int k = 0; k < 8; ++k)
+            if (8 * c + k < E) {
+                atomicAdd(&total[8 * c + k], all[k]);
+                atomicAdd(&earlier[8 * c + k], old[k]);
             }
     }
     // this wave's uses: a part of its block
-    const int b = b0 + wv / spb;
-    const int64_t block_uses = int64_t(C.block_tokens) * C.top_k;
-    const int64_t all_uses = int64_t(C.n_tokens) * C.top_k;
-    const int64_t part = ((block_uses + spb - 1) / spb + kWave - 1) / kWave * kWave;
-    int64_t u0 = b * block_uses + (wv % spb) * part;
-    int64_t u1 = min(min(u0 + part, (b + 1) * block_uses), all_uses);
-    if (wv >= subs) u1 = u0;
-    uint32_t* mine = next + size_t(min(wv, subs - 1)) * E;
-    for (int64_t u = u0 + lane; u < u1; u += kWave) {
+    const int b = b0 + (wv >> (31 - __builtin_clz(spb)));
+    // (all uses are below 2^31, sums of two below 2^32)
+    const uint32_t block_uses = uint32_t(C.block_tokens) * C.top_k;
+    const uint32_t all_uses = uint32_t(C.n_tokens) * C.top_k;
+    const uint32_t start = min(uint32_t(min(b, C.n_blocks)) * block_uses, all_uses);
+    const uint32_t stop = min(start + block_uses, all_uses);
+    const uint32_t part = ((block_uses + kWave * spb - 1) / (kWave * spb)) * kWave;
+    const uint32_t u0 = min(start + (wv & (spb - 1)) * part, stop);
+    const uint32_t u1 = wv < subs ? min(u0 + part, stop) : u0;
+    uint32_t* mine = next + min(wv, subs - 1) * E;
+    // the first round's ids stay in a register
+    const int id0 = u0 + lane < u1 ? C.ids[u0 + lane] : -1;
+    if (id0 >= 0) atomicAdd(&mine[id0], 1u);
+    for (uint32_t u = u0 + kWave + lane; u < u1; u += kWave) {
         const int id = C.ids[u];
         if (id >= 0) atomicAdd(&mine[id], 1u);
     }
@@ -308,17 +343,24 @@ __global__ __launch_bounds__(kRouteThreads) void scatter_kernel(const RouteCall 
             if (e == E - 1) C.offsets[E] = int32_t(at + n);
         }
         uint32_t place = at + earlier[e];
-        for (int w = 0; w < subs; ++w) {
-            const uint32_t k = next[size_t(w) * E + e];
-            next[size_t(w) * E + e] = place;
-            place += k;
+        for (int w0 = 0; w0 < subs; w0 += 4) {
+            uint32_t k[4];
+#pragma unroll
+            for (int w = 0; w < 4; ++w) k[w] = w0 + w < subs ? next[(w0 + w) * E + e] : 0u;
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                if (w0 + w < subs) next[(w0 + w) * E + e] = place;
+                place += k[w];
+            }
         }
         at += n;
     }
     __syncthreads();
     const int bits = 32 - __builtin_clz(E);
-    for (int64_t u = u0; u < u1; u += kWave)
-        place_uses(C.order, mine, u + lane < u1 ? C.ids[u + lane] : -1, u + lane, bits);
+    for (uint32_t u = u0; u < u1; u += kWave) {
+        const int id = u == u0 ? id0 : u + lane < u1 ? C.ids[u + lane] : -1;
+        place_uses(C.order, mine, id, u + lane, bits);
+    }
 }
 
 __global__ void route_nothing_kernel(const RouteCall C) {
@@ -341,7 +383,7 @@ hipError_t launch_select_typed(const RouteCall& C, hipStream_t st) {
     // as many waves as 60 KiB of LDS serve (E <= 4096: at least 1)
     const int fit = 15360 / C.n_experts - 2;
     const int subs = fit >= 16 ? 16 : fit >= 8 ? 8 : fit >= 4 ? 4 : fit >= 2 ? 2 : 1;
-    const int spb = subs >= 16 ? 4 : subs >= 8 ? 2 : 1;
+    const int spb = subs >= 16 ? 8 : subs >= 8 ? 4 : 1;
     const int nb = subs / spb;
     hipLaunchKernelGGL(scatter_kernel, dim3(unsigned((C.n_blocks + nb - 1) / nb)),
                        dim3(kRouteThreads), size_t(subs + 2) * C.n_experts * 4, st, C, subs, spb);

@@ -85,7 +85,7 @@ extern "C" size_t pm_route_workspace_bytes(int n_tokens, int n_experts, int top_
     if (!route_sizes_ok(n_tokens, n_experts, top_k)) return 0;
     int bt, nb;
     route_blocks(n_tokens, &bt, &nb);
-    return (size_t(nb) * ((n_experts + 1) & ~1) * sizeof(uint16_t) + 15) & ~size_t(15);
+    return (size_t(nb) * ((n_experts + 7) & ~7) * sizeof(uint16_t) + 15) & ~size_t(15);
 }
 
 extern "C" pm_status pm_route_topk_device(int n_tokens, int n_experts, int top_k,
@@ -137,7 +137,7 @@ extern "C" pm_status pm_route_topk_device(int n_tokens, int n_experts, int top_k
     C.offsets = d_offsets;
     C.order = d_order;
     C.hist = static_cast<uint16_t*>(d_ws);
-    C.hist_stride = (n_experts + 1) & ~1;
+    C.hist_stride = (n_experts + 7) & ~7;
     C.n_tokens = n_tokens;
     C.n_experts = n_experts;
     C.top_k = top_k;

@@ -22,7 +22,7 @@ struct RouteCall {
     int32_t* offsets;              // null: no sorting
     int32_t* order;
     uint16_t* hist;                // workspace [blocks][hist_stride]
-    int32_t hist_stride;           // n_experts, or one more to be even
+    int32_t hist_stride;           // n_experts, rounded up to 8
     int32_t n_tokens, n_experts, top_k, type;
     int32_t block_tokens, n_blocks;   // tokens per histogram block, blocks
 };
