@@ -340,43 +340,63 @@ def pm_allocate_bits(ids, w, err_profiles, budget):
 
 
 # ---------------------------------------------------------------- routed experts on the device
-# These take torch tensors only: types, sizes and strides come from them.
-_TYPES = {"torch.float32": PM_F32, "torch.float16": PM_F16, "torch.bfloat16": PM_BF16}
+# These take torch tensors only: types, sizes and strides come from them.  The
+# checks are written for a short call: a decode step's kernel takes 3 to 10 us.
+_types = {}
+_device = None
+
+
+def _load_types():
+    """Fills the tables that need torch."""
+    global _device
+    import torch
+    _device = torch.cuda.current_device
+    _types.update({torch.float32: PM_F32, torch.float16: PM_F16, torch.bfloat16: PM_BF16,
+                   torch.int32: "int32", torch.uint8: "uint8"})
 
 
 def _on_device(*tensors):
     """Every tensor (None allowed) is on the current HIP device, where the
     call's kernels run."""
-    import torch
-    cur = torch.cuda.current_device() if torch.cuda.is_initialized() else 0
+    if not _types:
+        _load_types()
+    dev = tensors[0].get_device()
     for t in tensors:
-        if t is not None and not (t.is_cuda and t.get_device() == cur):
-            raise ValueError(f"a tensor on {t.device}, not on the current device cuda:{cur}")
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"tensors on device {tensors[0].device} and {t.device}")
+    if dev < 0 or dev != _device():
+        raise ValueError(f"tensors on {tensors[0].device}, not on the current device")
 
 
 def _type(t, what):
-    try:
-        return _TYPES[str(t.dtype)]
-    except KeyError:
-        raise ValueError(f"{what}: float32, float16 or bfloat16, not {t.dtype}") from None
+    if not _types:
+        _load_types()
+    k = _types.get(t.dtype)
+    if k.__class__ is not int:
+        raise ValueError(f"{what}: float32, float16 or bfloat16, not {t.dtype}")
+    return k
 
 
-def _vec(t, dtype, n, what):
-    """A contiguous tensor of `dtype` (its name) with at least n elements (None passes)."""
-    if t is None:
-        return
-    if str(t.dtype) != dtype or not t.is_contiguous() or t.numel() < n:
-        raise ValueError(f"{what}: contiguous {dtype} of at least {n} elements")
+def _vec(t, kind, n, what):
+    """The address of a contiguous tensor of type `kind` with at least n elements."""
+    if not _types:
+        _load_types()
+    if _types.get(t.dtype) != kind or t.numel() < n or not t.is_contiguous():
+        name = {PM_F32: "float32", PM_F16: "float16"}.get(kind, kind)
+        raise ValueError(f"{what}: contiguous {name} of at least {n} elements, not {t.numel()} "
+                         f"of {t.dtype}")
+    return t.data_ptr()
 
 
 def _rows2d(t, n, cols, what):
     """A 2-D tensor of at least n rows of `cols` adjacent elements: its row
     distance in elements."""
-    if t.dim() != 2 or t.shape[0] < n or t.shape[1] != cols or (cols > 1 and t.stride(1) != 1):
+    shape, strides = t.shape, t.stride()
+    if len(shape) != 2 or shape[0] < n or shape[1] != cols or (cols > 1 and strides[1] != 1):
         raise ValueError(f"{what}: at least {n} rows of {cols} adjacent elements, not "
-                         f"{tuple(t.shape)} with strides {t.stride()}")
+                         f"{tuple(shape)} with strides {strides}")
     # one row, or none, has no distance to the next
-    return t.stride(0) if t.shape[0] > 1 else cols
+    return strides[0] if shape[0] > 1 else cols
 
 
 def pm_route_workspace_bytes(n_tokens, n_experts, top_k):
@@ -395,47 +415,52 @@ def pm_route_topk_device(d_logits, top_k, d_ids, d_w, d_offsets=None, d_order=No
     ld = _rows2d(d_logits, n, e, "logits")
     _on_device(d_logits, d_ids, d_w, d_offsets, d_order, d_ws)
     uses = n * top_k
-    _vec(d_ids, "torch.int32", uses, "ids")
-    _vec(d_w, "torch.float32", uses, "w")
-    _vec(d_offsets, "torch.int32", e + 1, "offsets")
-    _vec(d_order, "torch.int32", uses, "order")
+    ids = _vec(d_ids, "int32", uses, "ids")
+    w = _vec(d_w, PM_F32, uses, "w")
+    offsets = order = ws = None
     ws_bytes = 0
+    if d_offsets is not None:
+        offsets = _vec(d_offsets, "int32", e + 1, "offsets")
+    if d_order is not None:
+        order = _vec(d_order, "int32", uses, "order")
     if d_ws is not None:
         if not d_ws.is_contiguous():
             raise ValueError("workspace: contiguous")
+        ws = d_ws.data_ptr()
         ws_bytes = d_ws.numel() * d_ws.element_size()
-    return _check(lib().pm_route_topk_device(
-        n, e, top_k, d_logits.data_ptr(), _type(d_logits, "logits"), ld, _dptr(d_ids),
-        _dptr(d_w), _dptr(d_offsets), _dptr(d_order), _dptr(d_ws), ws_bytes, _stream(stream)))
+    return _check(lib().pm_route_topk_device(n, e, top_k, d_logits.data_ptr(),
+                                             _type(d_logits, "logits"), ld, ids, w, offsets,
+                                             order, ws, ws_bytes, _stream(stream)))
 
 
 def _grouped_args(n_experts, rows, cols, d_x, d_y, d_offsets, d_order, top_k, flags):
     """The shape, the rows and the row distances of x and y of a grouped product."""
-    if d_x.dim() != 2 or d_y.dim() != 2:
-        raise ValueError("x and y are 2-D")
     if top_k < 1:
         raise ValueError("top_k: at least 1")
-    n = d_y.shape[0] if d_order is None else d_order.numel()
-    _vec(d_offsets, "torch.int32", n_experts + 1, "offsets")
-    _vec(d_order, "torch.int32", n, "order")
+    offsets = _vec(d_offsets, "int32", n_experts + 1, "offsets")
+    if d_order is None:
+        n, order = d_y.shape[0], None
+    else:
+        n = d_order.numel()
+        order = _vec(d_order, "int32", n, "order")
     nx = (n + top_k - 1) // top_k if flags & PM_GROUPED_GATHER else n
     ldx = _rows2d(d_x, nx, cols, "x")
     ldy = _rows2d(d_y, n, rows // 2 if flags & PM_GROUPED_SWIGLU else rows, "y")
-    return (pm_grouped_shape(n_experts, rows, cols),
-            pm_grouped_rows(n, top_k, _dptr(d_offsets), _dptr(d_order)), ldx, ldy)
+    return (pm_grouped_shape(n_experts, rows, cols), pm_grouped_rows(n, top_k, offsets, order),
+            ldx, ldy)
 
 
 def pm_grouped_gemm(d_w, d_x, d_y, d_offsets, d_order=None, top_k=1, flags=0, stream=None):
     """d_w [n_experts][rows][cols] float16 or bfloat16, contiguous; d_x rows
     of cols of the same type; d_y rows of that type or float32."""
-    if d_w.dim() != 3 or not d_w.is_contiguous():
+    shape = d_w.shape
+    if len(shape) != 3 or not d_w.is_contiguous():
         raise ValueError("w: contiguous [n_experts][rows][cols]")
     t = _type(d_w, "w")
     if d_x.dtype != d_w.dtype:
         raise ValueError(f"x of {d_x.dtype} with weights of {d_w.dtype}")
     _on_device(d_w, d_x, d_y, d_offsets, d_order)
-    e, rows, cols = d_w.shape
-    s, r, ldx, ldy = _grouped_args(e, rows, cols, d_x, d_y, d_offsets, d_order, top_k, flags)
+    s, r, ldx, ldy = _grouped_args(*shape, d_x, d_y, d_offsets, d_order, top_k, flags)
     return _check(lib().pm_grouped_gemm(s, t, d_w.data_ptr(), r, d_x.data_ptr(), ldx,
                                         d_y.data_ptr(), _type(d_y, "y"), ldy, flags,
                                         _stream(stream)))
@@ -446,19 +471,19 @@ def pm_grouped_gemm_w4(d_q, d_scales, d_zeros, group, d_x, d_y, d_offsets, d_ord
     """d_q uint8 [n_experts][rows][cols/2], d_scales float16 and d_zeros uint8
     (or None) [n_experts][rows][cols/group]; d_x rows of cols, d_y rows of x's
     type or float32."""
-    if d_q.dim() != 3 or not d_q.is_contiguous() or str(d_q.dtype) != "torch.uint8":
+    if d_q.dim() != 3:
         raise ValueError("q: contiguous uint8 [n_experts][rows][cols/2]")
     e, rows, half = d_q.shape
     cols = 2 * half
     n_groups = e * rows * (cols // group) if group > 0 else 0
+    q = _vec(d_q, "uint8", 0, "q")
     _on_device(d_q, d_scales, d_zeros, d_x, d_y, d_offsets, d_order)
-    _vec(d_scales, "torch.float16", n_groups, "scales")
-    _vec(d_zeros, "torch.uint8", n_groups, "zeros")
+    scales = _vec(d_scales, PM_F16, n_groups, "scales")
+    zeros = None if d_zeros is None else _vec(d_zeros, "uint8", n_groups, "zeros")
     s, r, ldx, ldy = _grouped_args(e, rows, cols, d_x, d_y, d_offsets, d_order, top_k, flags)
-    return _check(lib().pm_grouped_gemm_w4(s, group, d_q.data_ptr(), _dptr(d_scales),
-                                           _dptr(d_zeros), r, d_x.data_ptr(), _type(d_x, "x"),
-                                           ldx, d_y.data_ptr(), _type(d_y, "y"), ldy, flags,
-                                           _stream(stream)))
+    return _check(lib().pm_grouped_gemm_w4(s, group, q, scales, zeros, r, d_x.data_ptr(),
+                                           _type(d_x, "x"), ldx, d_y.data_ptr(), _type(d_y, "y"),
+                                           ldy, flags, _stream(stream)))
 
 
 def pm_encode_w4_device(d_w, group, d_q, d_scales, d_zeros=None, stream=None):
@@ -469,28 +494,27 @@ def pm_encode_w4_device(d_w, group, d_q, d_scales, d_zeros=None, stream=None):
     rows, cols = d_w.shape
     n_groups = rows * (cols // group) if group > 0 else 0
     _on_device(d_w, d_q, d_scales, d_zeros)
-    _vec(d_q, "torch.uint8", rows * cols // 2, "q")
-    _vec(d_scales, "torch.float16", n_groups, "scales")
-    _vec(d_zeros, "torch.uint8", n_groups, "zeros")
+    q = _vec(d_q, "uint8", rows * cols // 2, "q")
+    scales = _vec(d_scales, PM_F16, n_groups, "scales")
+    zeros = None if d_zeros is None else _vec(d_zeros, "uint8", n_groups, "zeros")
     return _check(lib().pm_encode_w4_device(pm_matrix_shape(rows, cols, group), d_w.data_ptr(),
-                                            _type(d_w, "w"), _dptr(d_q), _dptr(d_scales),
-                                            _dptr(d_zeros), _stream(stream)))
+                                            _type(d_w, "w"), q, scales, zeros, _stream(stream)))
 
 
 def pm_combine_uses(d_z, d_w, d_y, stream=None):
     """d_y[t] = sum_j d_w[t][j] * d_z[t * top_k + j]: d_w float32
     [n_tokens][top_k], d_z rows of hidden, d_y rows of z's type or float32."""
-    if d_w.dim() != 2 or d_z.dim() != 2 or d_y.dim() != 2:
+    shape = d_w.shape
+    if len(shape) != 2 or d_z.dim() != 2 or d_y.dim() != 2:
         raise ValueError("z, w and y are 2-D")
-    n, top_k = d_w.shape
+    n, top_k = shape
     hidden = d_y.shape[1]
-    _vec(d_w, "torch.float32", n * top_k, "w")
     _on_device(d_z, d_w, d_y)
+    w = _vec(d_w, PM_F32, n * top_k, "w")
     ldz = _rows2d(d_z, n * top_k, hidden, "z")
     ldy = _rows2d(d_y, n, hidden, "y")
-    return _check(lib().pm_combine_uses(n, top_k, hidden, d_z.data_ptr(), _type(d_z, "z"), ldz,
-                                        d_w.data_ptr(), d_y.data_ptr(), _type(d_y, "y"), ldy,
-                                        _stream(stream)))
+    return _check(lib().pm_combine_uses(n, top_k, hidden, d_z.data_ptr(), _type(d_z, "z"), ldz, w,
+                                        d_y.data_ptr(), _type(d_y, "y"), ldy, _stream(stream)))
 
 
 # ---------------------------------------------------------------- handles
