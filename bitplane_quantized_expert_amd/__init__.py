@@ -340,63 +340,45 @@ def pm_allocate_bits(ids, w, err_profiles, budget):
 
 
 # ---------------------------------------------------------------- routed experts on the device
-# These take torch tensors only: types, sizes and strides come from them.  The
-# checks are written for a short call: a decode step's kernel takes 3 to 10 us.
+# These take torch tensors only: types, sizes and strides come from them.  A
+# decode step's kernel takes 3 to 10 us, so the checks of the calls that a step
+# makes are written out in line, each property of a tensor read once.
 _types = {}
-_device = None
+_int32 = _uint8 = None
 
 
-def _load_types():
-    """Fills the tables that need torch."""
-    global _device
+def _current_device():
+    """The current HIP device, which the kernels run on (loads torch at the
+    first call and puts its device query in place of this function)."""
+    global _current_device, _int32, _uint8
     import torch
-    _device = torch.cuda.current_device
-    _types.update({torch.float32: PM_F32, torch.float16: PM_F16, torch.bfloat16: PM_BF16,
-                   torch.int32: "int32", torch.uint8: "uint8"})
+    _types.update({torch.float32: PM_F32, torch.float16: PM_F16, torch.bfloat16: PM_BF16})
+    _int32, _uint8 = torch.int32, torch.uint8
+    _current_device = torch.cuda.current_device if torch.cuda.is_available() else lambda: -2
+    return _current_device()
 
 
 def _on_device(*tensors):
-    """Every tensor (None allowed) is on the current HIP device, where the
-    call's kernels run."""
-    if not _types:
-        _load_types()
     dev = tensors[0].get_device()
     for t in tensors:
         if t is not None and t.get_device() != dev:
             raise ValueError(f"tensors on device {tensors[0].device} and {t.device}")
-    if dev < 0 or dev != _device():
+    if dev < 0 or dev != _current_device():
         raise ValueError(f"tensors on {tensors[0].device}, not on the current device")
 
 
-def _type(t, what):
-    if not _types:
-        _load_types()
-    k = _types.get(t.dtype)
-    if k.__class__ is not int:
-        raise ValueError(f"{what}: float32, float16 or bfloat16, not {t.dtype}")
-    return k
+def _bad_type(t, what):
+    raise ValueError(f"{what}: float32, float16 or bfloat16, not {t.dtype}")
 
 
-def _vec(t, kind, n, what):
-    """The address of a contiguous tensor of type `kind` with at least n elements."""
-    if not _types:
-        _load_types()
-    if _types.get(t.dtype) != kind or t.numel() < n or not t.is_contiguous():
-        name = {PM_F32: "float32", PM_F16: "float16"}.get(kind, kind)
-        raise ValueError(f"{what}: contiguous {name} of at least {n} elements, not {t.numel()} "
-                         f"of {t.dtype}")
-    return t.data_ptr()
+def _bad_vec(t, name, n, what):
+    raise ValueError(f"{what}: contiguous {name} of at least {n} elements, not {t.numel()} of "
+                     f"{t.dtype}, strides {t.stride()}")
 
 
-def _rows2d(t, n, cols, what):
-    """A 2-D tensor of at least n rows of `cols` adjacent elements: its row
-    distance in elements."""
-    shape, strides = t.shape, t.stride()
-    if len(shape) != 2 or shape[0] < n or shape[1] != cols or (cols > 1 and strides[1] != 1):
-        raise ValueError(f"{what}: at least {n} rows of {cols} adjacent elements, not "
-                         f"{tuple(shape)} with strides {strides}")
-    # one row, or none, has no distance to the next
-    return strides[0] if shape[0] > 1 else cols
+def _bad_rows(t, n, cols, what):
+    raise ValueError(f"{what}: at least {n} rows of {cols} adjacent elements, not "
+                     f"{tuple(t.shape)} with strides {t.stride()}")
 
 
 def pm_route_workspace_bytes(n_tokens, n_experts, top_k):
@@ -409,45 +391,77 @@ def pm_route_topk_device(d_logits, top_k, d_ids, d_w, d_offsets=None, d_order=No
     distance) -> d_ids int32, d_w float32 [n_tokens][top_k], and the uses
     sorted by expert: d_offsets int32 [n_experts + 1], d_order int32
     [n_tokens * top_k], with d_ws of pm_route_workspace_bytes bytes."""
-    if d_logits.dim() != 2:
-        raise ValueError("logits: [n_tokens][n_experts]")
-    n, e = d_logits.shape
-    ld = _rows2d(d_logits, n, e, "logits")
-    _on_device(d_logits, d_ids, d_w, d_offsets, d_order, d_ws)
+    shape, strides = d_logits.shape, d_logits.stride()
+    if len(shape) != 2 or (shape[1] > 1 and strides[1] != 1):
+        raise ValueError(f"logits: rows of adjacent elements, not {tuple(shape)} with strides "
+                         f"{strides}")
+    n, e = shape
+    dev = _current_device()
+    if d_logits.get_device() != dev or d_ids.get_device() != dev or d_w.get_device() != dev or \
+            (d_offsets is not None and d_offsets.get_device() != dev) or \
+            (d_order is not None and d_order.get_device() != dev) or \
+            (d_ws is not None and d_ws.get_device() != dev):
+        _on_device(d_logits, d_ids, d_w, d_offsets, d_order, d_ws)
     uses = n * top_k
-    ids = _vec(d_ids, "int32", uses, "ids")
-    w = _vec(d_w, PM_F32, uses, "w")
+    t = _types.get(d_logits.dtype)
+    if t is None:
+        _bad_type(d_logits, "logits")
+    if d_ids.dtype is not _int32 or d_ids.numel() < uses or not d_ids.is_contiguous():
+        _bad_vec(d_ids, "int32", uses, "ids")
+    if _types.get(d_w.dtype) != PM_F32 or d_w.numel() < uses or not d_w.is_contiguous():
+        _bad_vec(d_w, "float32", uses, "w")
     offsets = order = ws = None
     ws_bytes = 0
     if d_offsets is not None:
-        offsets = _vec(d_offsets, "int32", e + 1, "offsets")
+        if d_offsets.dtype is not _int32 or d_offsets.numel() <= e or \
+                not d_offsets.is_contiguous():
+            _bad_vec(d_offsets, "int32", e + 1, "offsets")
+        offsets = d_offsets.data_ptr()
     if d_order is not None:
-        order = _vec(d_order, "int32", uses, "order")
+        if d_order.dtype is not _int32 or d_order.numel() < uses or not d_order.is_contiguous():
+            _bad_vec(d_order, "int32", uses, "order")
+        order = d_order.data_ptr()
     if d_ws is not None:
         if not d_ws.is_contiguous():
             raise ValueError("workspace: contiguous")
         ws = d_ws.data_ptr()
-        ws_bytes = d_ws.numel() * d_ws.element_size()
-    return _check(lib().pm_route_topk_device(n, e, top_k, d_logits.data_ptr(),
-                                             _type(d_logits, "logits"), ld, ids, w, offsets,
-                                             order, ws, ws_bytes, _stream(stream)))
+        ws_bytes = d_ws.nbytes
+    # (one row, or none, has no distance to the next)
+    return _check(lib().pm_route_topk_device(
+        n, e, top_k, d_logits.data_ptr(), t, strides[0] if n > 1 else e, d_ids.data_ptr(),
+        d_w.data_ptr(), offsets, order, ws, ws_bytes, _stream(stream)))
 
 
-def _grouped_args(n_experts, rows, cols, d_x, d_y, d_offsets, d_order, top_k, flags):
-    """The shape, the rows and the row distances of x and y of a grouped product."""
+def _grouped_args(dev, d_w, n_experts, rows, cols, d_x, d_y, d_offsets, d_order, top_k, flags):
+    """The shape, the rows and the row distances of x and y of a grouped
+    product on device `dev`."""
+    if d_w.get_device() != dev or d_x.get_device() != dev or d_y.get_device() != dev or \
+            d_offsets.get_device() != dev or \
+            (d_order is not None and d_order.get_device() != dev):
+        _on_device(d_w, d_x, d_y, d_offsets, d_order)
     if top_k < 1:
         raise ValueError("top_k: at least 1")
-    offsets = _vec(d_offsets, "int32", n_experts + 1, "offsets")
+    if d_offsets.dtype is not _int32 or d_offsets.numel() <= n_experts or \
+            not d_offsets.is_contiguous():
+        _bad_vec(d_offsets, "int32", n_experts + 1, "offsets")
+    xs, ys, ldx, ldy = d_x.shape, d_y.shape, d_x.stride(), d_y.stride()
     if d_order is None:
-        n, order = d_y.shape[0], None
+        n, order = ys[0], None
     else:
         n = d_order.numel()
-        order = _vec(d_order, "int32", n, "order")
+        if d_order.dtype is not _int32 or not d_order.is_contiguous():
+            _bad_vec(d_order, "int32", n, "order")
+        order = d_order.data_ptr()
     nx = (n + top_k - 1) // top_k if flags & PM_GROUPED_GATHER else n
-    ldx = _rows2d(d_x, nx, cols, "x")
-    ldy = _rows2d(d_y, n, rows // 2 if flags & PM_GROUPED_SWIGLU else rows, "y")
-    return (pm_grouped_shape(n_experts, rows, cols), pm_grouped_rows(n, top_k, offsets, order),
-            ldx, ldy)
+    out = rows // 2 if flags & PM_GROUPED_SWIGLU else rows
+    if len(xs) != 2 or xs[0] < nx or xs[1] != cols or (cols > 1 and ldx[1] != 1):
+        _bad_rows(d_x, nx, cols, "x")
+    if len(ys) != 2 or ys[0] < n or ys[1] != out or (out > 1 and ldy[1] != 1):
+        _bad_rows(d_y, n, out, "y")
+    # (one row, or none, has no distance to the next)
+    return (pm_grouped_shape(n_experts, rows, cols),
+            pm_grouped_rows(n, top_k, d_offsets.data_ptr(), order),
+            ldx[0] if xs[0] > 1 else cols, ldy[0] if ys[0] > 1 else out)
 
 
 def pm_grouped_gemm(d_w, d_x, d_y, d_offsets, d_order=None, top_k=1, flags=0, stream=None):
@@ -456,14 +470,15 @@ def pm_grouped_gemm(d_w, d_x, d_y, d_offsets, d_order=None, top_k=1, flags=0, st
     shape = d_w.shape
     if len(shape) != 3 or not d_w.is_contiguous():
         raise ValueError("w: contiguous [n_experts][rows][cols]")
-    t = _type(d_w, "w")
-    if d_x.dtype != d_w.dtype:
+    dev = _current_device()
+    t, yt = _types.get(d_w.dtype), _types.get(d_y.dtype)
+    if t is None or yt is None:
+        _bad_type(d_w if t is None else d_y, "w and y")
+    if d_x.dtype is not d_w.dtype:
         raise ValueError(f"x of {d_x.dtype} with weights of {d_w.dtype}")
-    _on_device(d_w, d_x, d_y, d_offsets, d_order)
-    s, r, ldx, ldy = _grouped_args(*shape, d_x, d_y, d_offsets, d_order, top_k, flags)
+    s, r, ldx, ldy = _grouped_args(dev, d_w, *shape, d_x, d_y, d_offsets, d_order, top_k, flags)
     return _check(lib().pm_grouped_gemm(s, t, d_w.data_ptr(), r, d_x.data_ptr(), ldx,
-                                        d_y.data_ptr(), _type(d_y, "y"), ldy, flags,
-                                        _stream(stream)))
+                                        d_y.data_ptr(), yt, ldy, flags, _stream(stream)))
 
 
 def pm_grouped_gemm_w4(d_q, d_scales, d_zeros, group, d_x, d_y, d_offsets, d_order=None,
@@ -471,19 +486,34 @@ def pm_grouped_gemm_w4(d_q, d_scales, d_zeros, group, d_x, d_y, d_offsets, d_ord
     """d_q uint8 [n_experts][rows][cols/2], d_scales float16 and d_zeros uint8
     (or None) [n_experts][rows][cols/group]; d_x rows of cols, d_y rows of x's
     type or float32."""
-    if d_q.dim() != 3:
+    shape = d_q.shape
+    if len(shape) != 3:
         raise ValueError("q: contiguous uint8 [n_experts][rows][cols/2]")
-    e, rows, half = d_q.shape
+    e, rows, half = shape
     cols = 2 * half
+    dev = _current_device()
+    if d_q.dtype is not _uint8 or not d_q.is_contiguous():
+        _bad_vec(d_q, "uint8", 0, "q")
+    s, r, ldx, ldy = _grouped_args(dev, d_q, e, rows, cols, d_x, d_y, d_offsets, d_order, top_k,
+                                   flags)
     n_groups = e * rows * (cols // group) if group > 0 else 0
-    q = _vec(d_q, "uint8", 0, "q")
-    _on_device(d_q, d_scales, d_zeros, d_x, d_y, d_offsets, d_order)
-    scales = _vec(d_scales, PM_F16, n_groups, "scales")
-    zeros = None if d_zeros is None else _vec(d_zeros, "uint8", n_groups, "zeros")
-    s, r, ldx, ldy = _grouped_args(e, rows, cols, d_x, d_y, d_offsets, d_order, top_k, flags)
-    return _check(lib().pm_grouped_gemm_w4(s, group, q, scales, zeros, r, d_x.data_ptr(),
-                                           _type(d_x, "x"), ldx, d_y.data_ptr(), _type(d_y, "y"),
-                                           ldy, flags, _stream(stream)))
+    if _types.get(d_scales.dtype) != PM_F16 or d_scales.numel() < n_groups or \
+            not d_scales.is_contiguous():
+        _bad_vec(d_scales, "float16", n_groups, "scales")
+    zeros = None
+    if d_zeros is not None:
+        if d_zeros.dtype is not _uint8 or d_zeros.numel() < n_groups or \
+                not d_zeros.is_contiguous():
+            _bad_vec(d_zeros, "uint8", n_groups, "zeros")
+        zeros = d_zeros.data_ptr()
+    if d_scales.get_device() != dev or (d_zeros is not None and d_zeros.get_device() != dev):
+        _on_device(d_q, d_scales, d_zeros)
+    xt, yt = _types.get(d_x.dtype), _types.get(d_y.dtype)
+    if xt is None or yt is None:
+        _bad_type(d_x if xt is None else d_y, "x and y")
+    return _check(lib().pm_grouped_gemm_w4(s, group, d_q.data_ptr(), d_scales.data_ptr(), zeros, r,
+                                           d_x.data_ptr(), xt, ldx, d_y.data_ptr(), yt, ldy,
+                                           flags, _stream(stream)))
 
 
 def pm_encode_w4_device(d_w, group, d_q, d_scales, d_zeros=None, stream=None):
@@ -494,27 +524,46 @@ def pm_encode_w4_device(d_w, group, d_q, d_scales, d_zeros=None, stream=None):
     rows, cols = d_w.shape
     n_groups = rows * (cols // group) if group > 0 else 0
     _on_device(d_w, d_q, d_scales, d_zeros)
-    q = _vec(d_q, "uint8", rows * cols // 2, "q")
-    scales = _vec(d_scales, PM_F16, n_groups, "scales")
-    zeros = None if d_zeros is None else _vec(d_zeros, "uint8", n_groups, "zeros")
-    return _check(lib().pm_encode_w4_device(pm_matrix_shape(rows, cols, group), d_w.data_ptr(),
-                                            _type(d_w, "w"), q, scales, zeros, _stream(stream)))
+    t = _types.get(d_w.dtype)
+    if t is None:
+        _bad_type(d_w, "w")
+    if d_q.dtype is not _uint8 or d_q.numel() < rows * cols // 2 or not d_q.is_contiguous():
+        _bad_vec(d_q, "uint8", rows * cols // 2, "q")
+    if _types.get(d_scales.dtype) != PM_F16 or d_scales.numel() < n_groups or \
+            not d_scales.is_contiguous():
+        _bad_vec(d_scales, "float16", n_groups, "scales")
+    if d_zeros is not None and (d_zeros.dtype is not _uint8 or d_zeros.numel() < n_groups or
+                                not d_zeros.is_contiguous()):
+        _bad_vec(d_zeros, "uint8", n_groups, "zeros")
+    return _check(lib().pm_encode_w4_device(pm_matrix_shape(rows, cols, group), d_w.data_ptr(), t,
+                                            d_q.data_ptr(), d_scales.data_ptr(), _dptr(d_zeros),
+                                            _stream(stream)))
 
 
 def pm_combine_uses(d_z, d_w, d_y, stream=None):
     """d_y[t] = sum_j d_w[t][j] * d_z[t * top_k + j]: d_w float32
     [n_tokens][top_k], d_z rows of hidden, d_y rows of z's type or float32."""
-    shape = d_w.shape
-    if len(shape) != 2 or d_z.dim() != 2 or d_y.dim() != 2:
+    shape, zs, ys, ldz, ldy = d_w.shape, d_z.shape, d_y.shape, d_z.stride(), d_y.stride()
+    if len(shape) != 2 or len(zs) != 2 or len(ys) != 2:
         raise ValueError("z, w and y are 2-D")
+    dev = _current_device()
+    if d_z.get_device() != dev or d_w.get_device() != dev or d_y.get_device() != dev:
+        _on_device(d_z, d_w, d_y)
     n, top_k = shape
-    hidden = d_y.shape[1]
-    _on_device(d_z, d_w, d_y)
-    w = _vec(d_w, PM_F32, n * top_k, "w")
-    ldz = _rows2d(d_z, n * top_k, hidden, "z")
-    ldy = _rows2d(d_y, n, hidden, "y")
-    return _check(lib().pm_combine_uses(n, top_k, hidden, d_z.data_ptr(), _type(d_z, "z"), ldz, w,
-                                        d_y.data_ptr(), _type(d_y, "y"), ldy, _stream(stream)))
+    uses, hidden = n * top_k, ys[1]
+    if _types.get(d_w.dtype) != PM_F32 or not d_w.is_contiguous():
+        _bad_vec(d_w, "float32", uses, "w")
+    if zs[0] < uses or zs[1] != hidden or (hidden > 1 and ldz[1] != 1):
+        _bad_rows(d_z, uses, hidden, "z")
+    if ys[0] < n or (hidden > 1 and ldy[1] != 1):
+        _bad_rows(d_y, n, hidden, "y")
+    zt, yt = _types.get(d_z.dtype), _types.get(d_y.dtype)
+    if zt is None or yt is None:
+        _bad_type(d_z if zt is None else d_y, "z and y")
+    # (one row, or none, has no distance to the next)
+    return _check(lib().pm_combine_uses(
+        n, top_k, hidden, d_z.data_ptr(), zt, ldz[0] if zs[0] > 1 else hidden, d_w.data_ptr(),
+        d_y.data_ptr(), yt, ldy[0] if ys[0] > 1 else hidden, _stream(stream)))
 
 
 # ---------------------------------------------------------------- handles
