@@ -12,7 +12,7 @@ hipError_t launch_grouped(const GroupedCall& C, int kind, hipStream_t st) {
     if (kind == kW16) {
         const int64_t xrows = C.flags & PM_GROUPED_GATHER ? (C.n_rows - 1) / C.top_k + 1 : 256;
         if (C.n_rows >= 48 * groups && (xrows * C.ldx + C.cols) * 2 < 0xFFFFFFF0ll)
-            return launch_grouped_tiles(C, st);
+            return launch_grouped_tiles(C, C.n_rows < 160 * groups ? 128 : 256, st);
         return launch_grouped_stream16(C, C.n_rows <= 8 * groups ? 1 : 2, st);
     }
     // an fp32 row takes two columns

@@ -41,9 +41,8 @@ namespace pm {
 
 namespace {
 
-constexpr int kTileM = 256, kTileN = 256, kTileK = 64;
+constexpr int kTileN = 256, kTileK = 64;
 constexpr int kTileThreads = 512, kTileWaves = 8;
-constexpr int kStageBytes = (kTileM + kTileN) * kTileK * 2;
 constexpr uint32_t kOutside = 0xFFFFFFF0u;      // an offset beyond any buffer
 constexpr int kBufferFlags = 0x00020000;        // raw buffer, 32-bit data format
 
@@ -61,16 +60,21 @@ __device__ inline f32x4 mfma16(const u32x4& a, const u32x4& b, const f32x4& c) {
                                                        __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
 }
 
-template <int WT, int YT, bool GLU>
+// BM rows by 256 weight rows, S stages of 64 inputs in LDS.
+template <int WT, int YT, bool GLU, int BM, int S>
 __global__ __launch_bounds__(kTileThreads, 2) void tile_kernel(const GroupedCall C, int nt,
                                                                bool vec) {
 #ifdef __HIP_DEVICE_COMPILE__
+    constexpr int kStageA = BM * kTileK * 2, kStage = kStageA + kTileN * kTileK * 2;
+    constexpr int LA = BM / 64, LB = kTileN / 64, L = LA + LB;   // a wave's loads per stage
+    constexpr int WM = BM / 2;                    // rows of a wave: 2 x 4 waves
+    constexpr int MB = WM / 16, NB = 4, NP = MB * NB, NR = MB + NB;
     extern __shared__ __attribute__((aligned(1024))) char smem[];
-    int* const ymap = reinterpret_cast<int*>(smem + 2 * kStageBytes);     // [2][256]
-    int* const before = ymap + 2 * kTileM;                                // [E + 1]
+    int* const ymap = reinterpret_cast<int*>(smem + S * kStage);          // [2][BM]
+    int* const before = ymap + 2 * BM;                                    // [E + 1]
     const int lane = threadIdx.x & 63, wv = uni(threadIdx.x >> 6);
     const int out = GLU ? C.rows / 2 : C.rows;
-    const int n_tiles = tile_table(C, kTileM, before) * nt;
+    const int n_tiles = tile_table(C, BM, before) * nt;
     __syncthreads();
 
     const int wm = wv >> 2, wn = wv & 3;
@@ -90,34 +94,38 @@ __global__ __launch_bounds__(kTileThreads, 2) void tile_kernel(const GroupedCall
             const int mt = i / nt;
             const int e = tile_expert(C, before, mt);
             const RowRange g = group_rows(C, e);
-            const int64_t skip = int64_t(mt - before[e]) * kTileM;
+            const int64_t skip = int64_t(mt - before[e]) * BM;
             const bool ok = skip >= 0 && skip < g.n;      // (not so only for bad offsets)
             w.e = uni(e);
             w.row0 = uni(ok ? g.row0 + int(skip) : 0);
-            w.n = uni(ok ? min(g.n - int(skip), kTileM) : 0);
+            w.n = uni(ok ? min(g.n - int(skip), BM) : 0);
             w.o0 = uni((i - mt * nt) * (GLU ? kTileN / 2 : kTileN));
         }
         return w;
     };
-    // offsets of this lane's rows, 4 of x and 4 of W per stage, and the buffers
+    // offsets of this lane's rows of x and of W per stage, and the buffers
     const bool gather = C.flags & PM_GROUPED_GATHER;
     const size_t wbytes = size_t(C.rows) * C.cols * 2;
     auto use_rows = [&](const Where& w, int* u) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < LA; ++i) {
             const int r = (i * kTileWaves + wv) * 8 + r8;
             u[i] = r < w.n ? use_of(C, w.row0 + r) : -1;
         }
     };
     auto set_rows = [&](const Where& w, const int* u, int parity, uint32_t* pa, uint32_t* pb) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < LA; ++i) {
             const int r = (i * kTileWaves + wv) * 8 + r8;
             const uint32_t xr = gather ? uint32_t(u[i]) / uint32_t(C.top_k) : uint32_t(r);
             pa[i] = u[i] >= 0 ? uint32_t(xr * uint64_t(C.ldx) * 2) + piece * 16 : kOutside;
             if ((lane & 7) == 0)
-                ymap[parity * kTileM + r] =
+                ymap[parity * BM + r] =
                     u[i] < 0 ? -1 : (C.flags & PM_GROUPED_SCATTER ? u[i] : w.row0 + r);
+        }
+#pragma unroll
+        for (int i = 0; i < LB; ++i) {
+            const int r = (i * kTileWaves + wv) * 8 + r8;
             // LDS slot (block j, row m) of the wave's 64 holds the weight row
             // that gives a lane adjacent outputs: 16 (8 with gate and up)
             const int s = r & 63, j = s >> 4, m = s & 15;
@@ -149,9 +157,10 @@ __global__ __launch_bounds__(kTileThreads, 2) void tile_kernel(const GroupedCall
                                                  kBufferFlags);
     };
 
-    const int T = max(2, (C.cols + kTileK - 1) / kTileK);
-    uint32_t pa[4], pb[4];
-    int u[4];
+    // (stages past the last input hold zeros; a tile has at least S)
+    const int T = max(S, (C.cols + kTileK - 1) / kTileK);
+    uint32_t pa[LA], pb[LB];
+    int u[LA];
     Where cur = locate(place), nxt;
     if (cur.n == 0) return;
     use_rows(cur, u);
@@ -159,43 +168,46 @@ __global__ __launch_bounds__(kTileThreads, 2) void tile_kernel(const GroupedCall
     auto ra = x_buffer(cur), rb = w_buffer(cur);
     int kk = 0;
     auto issue = [&](int stage) {
-        char* base = smem + stage * kStageBytes + wv * 1024;
+        char* base = smem + stage * kStage + wv * 1024;
         const bool in = kk * kTileK + piece * 8 < C.cols;
         const int ko = kk * kTileK * 2;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < LA; ++i)
             __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void*)(base + i * 8192), 16,
                                                      in ? pa[i] : kOutside, ko, 0, 0);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_void*)(base + 32768 + i * 8192), 16,
+        for (int i = 0; i < LB; ++i)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_void*)(base + kStageA + i * 8192), 16,
                                                      in ? pb[i] : kOutside, ko, 0, 0);
     };
-    issue(0);
-    kk = 1;
-    asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
-    issue(1);
+#pragma unroll
+    for (int i = 0; i < S; ++i) {
+        issue(i);
+        ++kk;
+    }
+    // stage 0 is needed now; three stages: and stage 1 in the first step
+    asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"((S > 2 ? S - 2 : S - 1) * L) : "memory");
 
     const int off0 = i16 * 128 + ((q ^ (i16 & 7)) * 16);
     const int off1 = i16 * 128 + (((4 + q) ^ (i16 & 7)) * 16);
-    const int ao = wm * 128 * 128, bo = 32768 + wn * 64 * 128;
-    u32x4 fa[2][8], fb[2][4];
-    f32x4 acc[8][4];
+    const int ao = wm * WM * 128, bo = kStageA + wn * 64 * 128;
+    u32x4 fa[2][MB], fb[2][NB];
+    f32x4 acc[MB][NB];
     int st = 0, parity = 0;
     auto read_half = [&](int stage, int h) {
-        const char* base = smem + stage * kStageBytes + (h ? off1 : off0);
+        const char* base = smem + stage * kStage + (h ? off1 : off0);
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < NB; ++j)
             fb[h][j] = *reinterpret_cast<const u32x4*>(base + bo + j * 2048);
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < MB; ++i)
             fa[h][i] = *reinterpret_cast<const u32x4*>(base + ao + i * 2048);
     };
     auto products = [&](int h) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < MB; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) acc[i][j] = mfma16<WT>(fb[h][j], fa[h][i], acc[i][j]);
+            for (int j = 0; j < NB; ++j) acc[i][j] = mfma16<WT>(fb[h][j], fa[h][i], acc[i][j]);
     };
     read_half(0, 0);
 
@@ -203,67 +215,76 @@ __global__ __launch_bounds__(kTileThreads, 2) void tile_kernel(const GroupedCall
         // the next tile's place and uses, long before its first loads
         nxt = locate(tile + gridDim.x);
         use_rows(nxt, u);
-        const bool act = cur.n > wm * 128;
+        const bool act = cur.n > wm * WM;
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < MB; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+            for (int j = 0; j < NB; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
         auto steps = [&](auto active) {
             constexpr bool ACT = decltype(active)::value;
             for (int t = 0; t < T; ++t) {
+                const int after = st + 1 == S ? 0 : st + 1;
                 __builtin_amdgcn_sched_barrier(0);
                 if constexpr (ACT) {
                     read_half(st, 1);
                     products(0);
+                    constexpr int R = (NP - 4) / NR;
                     __builtin_amdgcn_sched_group_barrier(0x8, 4, 0);
 #pragma unroll
-                    for (int g = 0; g < 12; ++g) {
+                    for (int g = 0; g < NR; ++g) {
                         __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-                        __builtin_amdgcn_sched_group_barrier(0x8, 2, 0);
+                        __builtin_amdgcn_sched_group_barrier(0x8, R, 0);
                     }
-                    __builtin_amdgcn_sched_group_barrier(0x8, 4, 0);
+                    __builtin_amdgcn_sched_group_barrier(0x8, NP - 4 - NR * R, 0);
                 }
                 __builtin_amdgcn_sched_barrier(0);
-                // the next stage has arrived, and every wave is done with this one
-                asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+                // the next stage has arrived, and every wave is done with this
+                // one.  With three stages the first step's has been waited for
+                // before the last tile's stores went out: loads and stores
+                // complete in order
+                if (S > 2 && t == 0)
+                    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+                else
+                    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((S - 2) * L)
+                                 : "memory");
                 __builtin_amdgcn_sched_barrier(0);
-                if (t == T - 2) {
+                if (t == T - S) {
                     set_rows(nxt, u, parity ^ 1, pa, pb);
                     ra = x_buffer(nxt);
                     rb = w_buffer(nxt);
                     kk = 0;
-                } else {
-                    ++kk;
                 }
                 __builtin_amdgcn_sched_barrier(0);
                 issue(st);
+                ++kk;
                 if constexpr (ACT) {
-                    read_half(st ^ 1, 0);
+                    read_half(after, 0);
                     products(1);
                     __builtin_amdgcn_sched_group_barrier(0x8, 2, 0);
 #pragma unroll
-                    for (int g = 0; g < 8; ++g) {
+                    for (int g = 0; g < L; ++g) {
                         __builtin_amdgcn_sched_group_barrier(0x10, 1, 0);
                         __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
                     }
 #pragma unroll
-                    for (int g = 0; g < 12; ++g) {
+                    for (int g = 0; g < NR; ++g) {
                         __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
                         __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
                     }
-                    __builtin_amdgcn_sched_group_barrier(0x8, 10, 0);
+                    __builtin_amdgcn_sched_group_barrier(0x8, NP - 2 - L - NR, 0);
                 } else if (t == T - 1) {
-                    read_half(st ^ 1, 0);         // the next tile may need this wave
+                    read_half(after, 0);          // the next tile may need this wave
                 }
                 __builtin_amdgcn_sched_barrier(0);
-                st ^= 1;
+                st = after;
             }
+            if (S > 2) asm volatile("s_waitcnt vmcnt(%0)" ::"n"((S - 2) * L) : "memory");
         };
         if (act) {
             steps(std::true_type{});
-            const int* rows = ymap + parity * kTileM + wm * 128 + i16;
+            const int* rows = ymap + parity * BM + wm * WM + i16;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
+            for (int i = 0; i < MB; ++i) {
                 const int yr = rows[i * 16];
                 if (yr < 0) continue;
                 const int64_t at = int64_t(yr) * C.ldy;
@@ -295,35 +316,43 @@ __global__ __launch_bounds__(kTileThreads, 2) void tile_kernel(const GroupedCall
 #endif
 }
 
-template <int WT, int YT, bool GLU>
+template <int WT, int YT, bool GLU, int BM, int S>
 hipError_t run_tiles(const GroupedCall& C, hipStream_t st) {
     const int out = GLU ? C.rows / 2 : C.rows;
     const int per = GLU ? kTileN / 2 : kTileN;
     const int nt = (out + per - 1) / per;
-    const size_t lds = 2 * kStageBytes + (2 * kTileM + C.n_experts + 1) * sizeof(int);
-    auto* f = tile_kernel<WT, YT, GLU>;
+    const size_t lds =
+        S * (BM + kTileN) * kTileK * 2 + (2 * BM + C.n_experts + 1) * sizeof(int);
+    auto* f = tile_kernel<WT, YT, GLU, BM, S>;
     hipError_t e = allow_lds(reinterpret_cast<const void*>(f), kTileMaxLds);
     if (e != hipSuccess) return e;
-    const bool vec = stores_by_4(C);
-    const int64_t tiles = (int64_t(std::min(C.n_rows, C.n_experts)) + C.n_rows / kTileM) * nt;
+    const int64_t tiles = (int64_t(std::min(C.n_rows, C.n_experts)) + C.n_rows / BM) * nt;
     const unsigned grid = unsigned(std::min<int64_t>(tiles, compute_units()));
-    hipLaunchKernelGGL(f, dim3(grid), dim3(kTileThreads), lds, st, C, nt, vec);
+    hipLaunchKernelGGL(f, dim3(grid), dim3(kTileThreads), lds, st, C, nt, stores_by_4(C));
     return hipGetLastError();
 }
 
-template <int WT, int YT>
-hipError_t run_tiles_glu(const GroupedCall& C, hipStream_t st) {
-    return C.flags & PM_GROUPED_SWIGLU ? run_tiles<WT, YT, true>(C, st)
-                                       : run_tiles<WT, YT, false>(C, st);
+template <int BM, int S>
+hipError_t run_tiles_typed(const GroupedCall& C, hipStream_t st) {
+    const bool f32 = C.y_type == PM_F32;
+    if (C.flags & PM_GROUPED_SWIGLU) {
+        if (C.w_type == PM_F16)
+            return f32 ? run_tiles<PM_F16, PM_F32, true, BM, S>(C, st)
+                       : run_tiles<PM_F16, PM_F16, true, BM, S>(C, st);
+        return f32 ? run_tiles<PM_BF16, PM_F32, true, BM, S>(C, st)
+                   : run_tiles<PM_BF16, PM_BF16, true, BM, S>(C, st);
+    }
+    if (C.w_type == PM_F16)
+        return f32 ? run_tiles<PM_F16, PM_F32, false, BM, S>(C, st)
+                   : run_tiles<PM_F16, PM_F16, false, BM, S>(C, st);
+    return f32 ? run_tiles<PM_BF16, PM_F32, false, BM, S>(C, st)
+               : run_tiles<PM_BF16, PM_BF16, false, BM, S>(C, st);
 }
 
 }  // namespace
 
-hipError_t launch_grouped_tiles(const GroupedCall& C, hipStream_t st) {
-    const bool f32 = C.y_type == PM_F32;
-    if (C.w_type == PM_F16)
-        return f32 ? run_tiles_glu<PM_F16, PM_F32>(C, st) : run_tiles_glu<PM_F16, PM_F16>(C, st);
-    return f32 ? run_tiles_glu<PM_BF16, PM_F32>(C, st) : run_tiles_glu<PM_BF16, PM_BF16>(C, st);
+hipError_t launch_grouped_tiles(const GroupedCall& C, int rows, hipStream_t st) {
+    return rows == 128 ? run_tiles_typed<128, 3>(C, st) : run_tiles_typed<256, 2>(C, st);
 }
 
 }  // namespace pm

@@ -49,9 +49,9 @@ struct GroupedCall {
 // Experts of one call (the kernels keep a table of them in LDS).
 constexpr int kMaxGroupedExperts = PM_GROUPED_MAX_EXPERTS;
 hipError_t launch_grouped(const GroupedCall& C, int kind, hipStream_t st);
-// 256 x 256 tiles (pm_grouped_tile.hip), 16-bit weights; the offsets of a
-// tile's rows in x must fit 32 bits.
-hipError_t launch_grouped_tiles(const GroupedCall& C, hipStream_t st);
+// Tiles of `rows` (128 or 256) x 256 (pm_grouped_tile.hip), 16-bit weights; the
+// offsets of a tile's rows in x must fit 32 bits.
+hipError_t launch_grouped_tiles(const GroupedCall& C, int rows, hipStream_t st);
 // Weights streamed past 16 * mt columns of activations, mt 1 or 2
 // (pm_grouped_stream.h); any sizes.
 hipError_t launch_grouped_stream16(const GroupedCall& C, int mt, hipStream_t st);
