@@ -5,19 +5,26 @@
 
 namespace pm {
 
+// 4-bit weights are always streamed.  16-bit weights are streamed while a group
+// has few rows: measured on 128 experts, us of the streamed kernel against
+// 128-row tiles at 4, 8, 12 rows per group: 329/377, 406/413, 451/419 with 4096
+// inputs (2048 outputs); 16 experts, 2048 inputs, 1536 outputs: 28/34, 29/34,
+// 33/34; with 1024 inputs (4096 outputs) 160/148 already at 2 rows.  Tiles of
+// 256 rows instead of 128 from 224 rows per group on, where there are two for
+// each compute unit: 353/359 us at 192 rows, 438/427 at 256, 760/726 at 512 (128
+// experts, 1024 inputs, 4096 outputs).  The groups' sizes are on the device;
+// these are rows per group if every expert had some.
 hipError_t launch_grouped(const GroupedCall& C, int kind, hipStream_t st) {
-    // rows per group if every expert had some: the groups' sizes are on the
-    // device
+    if (kind == kW4)
+        return C.x_type == PM_F32 ? launch_grouped_stream4f(C, st) : launch_grouped_stream4(C, st);
     const int64_t groups = std::min(C.n_experts, C.n_rows);
-    if (kind == kW16) {
-        const int64_t xrows = C.flags & PM_GROUPED_GATHER ? (C.n_rows - 1) / C.top_k + 1 : 256;
-        if (C.n_rows >= 48 * groups && (xrows * C.ldx + C.cols) * 2 < 0xFFFFFFF0ll)
-            return launch_grouped_tiles(C, C.n_rows < 160 * groups ? 128 : 256, st);
-        return launch_grouped_stream16(C, C.n_rows <= 8 * groups ? 1 : 2, st);
-    }
-    // an fp32 row takes two columns
-    if (C.x_type == PM_F32) return launch_grouped_stream4f(C, C.n_rows <= 4 * groups ? 1 : 2, st);
-    return launch_grouped_stream4(C, C.n_rows <= 8 * groups ? 1 : 2, st);
+    const int64_t x_rows = C.flags & PM_GROUPED_GATHER ? (C.n_rows - 1) / C.top_k + 1 : 256;
+    if (int64_t(C.n_rows) * 512 <= C.cols * groups ||
+        (x_rows * C.ldx + C.cols) * 2 >= 0xFFFFFFF0ll)
+        return launch_grouped_stream16(C, st);
+    const int64_t tiles256 = (C.n_rows / 256) * int64_t((C.rows + 255) / 256);
+    const bool big = C.n_rows >= 224 * groups && tiles256 >= 2 * compute_units();
+    return launch_grouped_tiles(C, big ? 256 : 128, st);
 }
 
 }  // namespace pm

@@ -7,15 +7,17 @@
 // Bound by reading the weights, so they go from memory to the matrix cores
 // through registers, once, and everything else stays out of the way.
 //
-// A workgroup of 8 waves works on row tiles, 16 rows of one expert's matrix
-// (8 gate and 8 up rows under PM_GROUPED_SWIGLU), for up to 16 * MT columns v
-// of activations.  KW waves split the inputs, the other factor of 8 splits the
+// A workgroup of NW waves works on row tiles, 16 rows of one expert's matrix
+// (8 gate and 8 up rows under PM_GROUPED_SWIGLU), for up to 16 columns v of
+// activations.  KW waves split the inputs, the other factor of NW splits the
 // row tiles.  A wave's share of the inputs, KB blocks of 128, stays in
 // registers as matrix operands while the row tiles pass: a row tile costs the
-// wave one 16-byte load per lane and 1 KiB, MT products each (4-bit: 4 MT) and
-// nothing from LDS.  The loads of the next row tile are in flight while one is
-// multiplied.  After kChunk row tiles the waves' sums meet in LDS (one
-// barrier) and are added in the order of the waves.
+// wave one 16-byte load per lane and 1 KiB, one product each (4-bit: 4) and
+// nothing from LDS.  The loads of the next row tiles are in flight while one
+// is multiplied.  The waves' sums meet in LDS after a chunk of 4 to 16 row
+// tiles per wave, as many as LDS holds (one barrier), and are added in a fixed
+// order.  The code that runs once per group of rows is kept small: a call that
+// lasts 15 us fetches every instruction from memory once.
 //
 // The row tiles of all groups form one sequence, of which every workgroup
 // takes an equal, contiguous part.
@@ -57,7 +59,6 @@ struct StreamPlan {
 
 namespace {
 
-constexpr int kStreamThreads = 512, kStreamWaves = 8;
 constexpr int kSteps = 4;                       // row tiles of an unrolled group
 // An offset beyond any buffer (all are below 2 GiB), with any immediate added.
 constexpr uint32_t kNowhere = 0x80000000u;
@@ -283,9 +284,9 @@ __device__ inline void steps_to(F&& f) {
     }
 }
 
-template <int KIND, bool BF16, bool X32, int KB, int MT, int GM, bool ZEROS>
-__global__ __launch_bounds__(kStreamThreads, 2) void stream_kernel(const GroupedCall C,
-                                                                   const StreamPlan P) {
+template <int KIND, bool BF16, bool X32, int NW, int KB, int GM, bool ZEROS>
+__global__ __launch_bounds__(NW * kWave, 2) void stream_kernel(const GroupedCall C,
+                                                               const StreamPlan P) {
 #ifdef __HIP_DEVICE_COMPILE__
     // 16-byte loads of a row tile per lane, and scales: one per block where a
     // group covers it, else one per 32 inputs
@@ -294,18 +295,18 @@ __global__ __launch_bounds__(kStreamThreads, 2) void stream_kernel(const Grouped
     constexpr bool kWhole = GM == kGroup128;
     // row tiles held in registers: one at work, the others on their way
     // (as many as 256 registers hold beside the activations)
-    constexpr int kSlots =
-        GM == kAnyGroup || (GM == kGroup32 && KB == 4) || kLoads * MT > 8 ? 2 : 4;
+    constexpr int kSlots = GM == kAnyGroup || (GM == kGroup32 && KB == 4) || kLoads > 8 ? 2 : 4;
+    constexpr int kThreads = NW * kWave, kLogNW = NW == 8 ? 3 : 2;
     // sums of a chunk: [buffer][wave][row tile][column of x][16], room
     // for 4 row tiles of all columns; the buffer to be filled next holds the
     // converted activations before
-    constexpr int kPart = kSteps * MT * 256;
-    __shared__ __attribute__((aligned(16))) float part[2][kStreamWaves][kPart];
-    __shared__ float xscale[16 * MT][kStreamWaves];
-    __shared__ int use_row[2][16 * MT];
+    constexpr int kPart = kSteps * 256;
+    __shared__ __attribute__((aligned(16))) float part[2][NW][kPart];
+    __shared__ float xscale[16][NW];
+    __shared__ int use_row[2][16];
     const int lane = threadIdx.x & 63, wv = uni(threadIdx.x >> 6);
     const int i16 = lane & 15, q = lane >> 4;
-    const int kw = 1 << P.kw_log, rw = kStreamWaves >> P.kw_log;
+    const int kw = 1 << P.kw_log, rw = NW >> P.kw_log;
     const int ks = wv & (kw - 1), rg = wv >> P.kw_log;
     const bool glu = C.flags & PM_GROUPED_SWIGLU, gather = C.flags & PM_GROUPED_GATHER;
     const int out = glu ? C.rows / 2 : C.rows;
@@ -313,7 +314,7 @@ __global__ __launch_bounds__(kStreamThreads, 2) void stream_kernel(const Grouped
 
     Eight eight;
     // sorted rows of a tile: an fp32 row takes two columns
-    constexpr int kTileRows = 16 * MT / (X32 ? 2 : 1);
+    constexpr int kTileRows = X32 ? 8 : 16;
     const TileScan scan = scan_tiles<kTileRows>(C, &eight);
     // Few groups: a whole number of workgroups each, which costs up to 1 part
     // in 8 of the workgroups but no workgroup prepares two groups' rows
@@ -459,8 +460,8 @@ __global__ __launch_bounds__(kStreamThreads, 2) void stream_kernel(const Grouped
         if (wv == 0 && lane < g.n)
             use_row[seg][lane] =
                 u_lane < 0 ? -1 : (C.flags & PM_GROUPED_SCATTER ? u_lane : g.row0 + lane);
-        u32x4 xf[KB * 4][MT];
-        float xs[MT][4];                                   // of columns 4q + r
+        u32x4 xf[KB * 4];
+        float xs[4];                                       // of columns 4q + r
         // row r of x (any row where r is not a row of the group)
         auto x_row = [&](int u, int r) {
             const int64_t xr = u < 0 ? 0 : gather ? u / C.top_k : g.row0 + r;
@@ -488,25 +489,22 @@ __global__ __launch_bounds__(kStreamThreads, 2) void stream_kernel(const Grouped
         auto load_x = [&](int panel, bool first) {
             const int c0 = first_block(panel) * 128;       // the wave's inputs
             if constexpr (KIND != kW4) {
+                const int u = __shfl(u_lane, i16);
+                const char* p = x_row(u, i16);
+                int c = c0 + q * 8;
+                asm volatile("" : "+v"(c));                // (addresses are not kept)
 #pragma unroll
-                for (int m = 0; m < MT; ++m) {
-                    const int u = __shfl(u_lane, m * 16 + i16);
-                    const char* p = x_row(u, m * 16 + i16);
-                    int c = c0 + q * 8;
-                    asm volatile("" : "+v"(c));            // (addresses are not kept)
-#pragma unroll
-                    for (int f = 0; f < KB * 4; ++f) {
-                        const bool ok = u >= 0 && c + f * 32 < C.cols;
-                        const u32x4 d = *reinterpret_cast<const u32x4*>(
-                            p + size_t(max(min(c + f * 32, C.cols - 8), 0)) * 2);
-                        xf[f][m] = ok ? d : u32x4{0, 0, 0, 0};
-                    }
+                for (int f = 0; f < KB * 4; ++f) {
+                    const bool ok = u >= 0 && c + f * 32 < C.cols;
+                    const u32x4 d = *reinterpret_cast<const u32x4*>(
+                        p + size_t(max(min(c + f * 32, C.cols - 8), 0)) * 2);
+                    xf[f] = ok ? d : u32x4{0, 0, 0, 0};
                 }
             } else {
                 // vper columns at a time: halves [column][inputs of the panel]
                 char* const stage = reinterpret_cast<char*>(&part[buf][0][0]);
                 const int width = KB * 128 << P.kw_log;
-                const int vper = min(1 << vlog, kStreamWaves * kPart * 2 / width);
+                const int vper = min(1 << vlog, NW * kPart * 2 / width);
                 const int rper = X32 ? vper >> 1 : vper;
                 const bool bf16 = C.x_type == PM_BF16;
                 const bool scaled = X32 || bf16;
@@ -556,22 +554,19 @@ __global__ __launch_bounds__(kStreamThreads, 2) void stream_kernel(const Grouped
                         }
                     }
                     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+                    // (a column without a row takes another's operands; its sums
+                    // are not used)
+                    const int v = i16 - v0;
+                    const char* p = stage + (size_t(v & (vper - 1)) * width + ks * KB * 128 +
+                                             (kWhole ? q * 32 : q * 8)) * 2;
+                    if (v0 == 0 || (v >= 0 && v < vper)) {
 #pragma unroll
-                    for (int m = 0; m < MT; ++m) {
-                        // (a column without a row takes another's operands; its
-                        // sums are not used)
-                        const int v = m * 16 + i16 - v0;
-                        const char* p = stage + (size_t(v & (vper - 1)) * width + ks * KB * 128 +
-                                                 (kWhole ? q * 32 : q * 8)) * 2;
-                        if (v0 == 0 || (v >= 0 && v < vper)) {
-#pragma unroll
-                            for (int f = 0; f < KB * 4; ++f)
-                                xf[f][m] = *reinterpret_cast<const u32x4*>(
-                                    p + ((f >> 2) * 128 + (f & 3) * (kWhole ? 8 : 32)) * 2);
-                        }
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) xs[m][r] = xscale[m * 16 + 4 * q + r][ks];
+                        for (int f = 0; f < KB * 4; ++f)
+                            xf[f] = *reinterpret_cast<const u32x4*>(
+                                p + ((f >> 2) * 128 + (f & 3) * (kWhole ? 8 : 32)) * 2);
                     }
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) xs[r] = xscale[4 * q + r][ks];
                     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
                 }
             }
@@ -583,18 +578,16 @@ __global__ __launch_bounds__(kStreamThreads, 2) void stream_kernel(const Grouped
             issue(std::integral_constant<int, c + 1>{}, rt0 + (c + 1) * rw + rg, 0);
         });
 
-        auto multiply = [&](auto slot, int panel, f32x4* a) {
+        auto multiply = [&](auto slot, int panel, f32x4& a) {
             constexpr int S = decltype(slot)::value;
-            f32x4 sum[MT];
-#pragma unroll
-            for (int m = 0; m < MT; ++m) sum[m] = f32x4{0.f, 0.f, 0.f, 0.f};
+            f32x4 sum = {0.f, 0.f, 0.f, 0.f};
             if constexpr (KIND == kW4) {
                 const int c0 = first_block(panel) * 128;
 #pragma unroll
                 for (int b = 0; b < KB; ++b) {
                     __builtin_amdgcn_sched_barrier(0);
                     const u32x4 c = kWhole ? w[S][b] : exchange(w[S][b]);
-                    f32x4 d[MT];
+                    f32x4 d = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         constexpr int kPer = kWhole ? 4 : GM == kGroup64 ? 2 : 1;
@@ -607,21 +600,15 @@ __global__ __launch_bounds__(kStreamThreads, 2) void stream_kernel(const Grouped
                             zb = za - f16x2{_Float16(960.0f), _Float16(960.0f)};
                         }
                         const u32x4 wf = codes_to_f16(bits, c[j], za, zb);
-#pragma unroll
-                        for (int m = 0; m < MT; ++m)
-                            d[m] = mfma_x_w<false>(
-                                xf[b * 4 + j][m], wf,
-                                j % kPer == 0 ? f32x4{0.f, 0.f, 0.f, 0.f} : d[m]);
+                        d = mfma_x_w<false>(xf[b * 4 + j], wf,
+                                            j % kPer == 0 ? f32x4{0.f, 0.f, 0.f, 0.f} : d);
                         if (j % kPer == kPer - 1) {
                             // past the last input there is no scale of this row
                             const bool in = c0 + b * 128 + (kWhole ? 0 : j / kPer * kPer * 32) < C.cols;
                             const float sf =
                                 in ? half_bits(sc[S][unit / 2] >> (16 * (unit & 1))) : 0.0f;
 #pragma unroll
-                            for (int m = 0; m < MT; ++m)
-#pragma unroll
-                                for (int r = 0; r < 4; ++r)
-                                    sum[m][r] = fmaf(d[m][r], sf, sum[m][r]);
+                            for (int r = 0; r < 4; ++r) sum[r] = fmaf(d[r], sf, sum[r]);
                         }
                     }
                 }
@@ -635,24 +622,19 @@ __global__ __launch_bounds__(kStreamThreads, 2) void stream_kernel(const Grouped
                         if (c0 + f * 32 + q * 8 >= C.cols) w[S][f] = u32x4{0, 0, 0, 0};
                 }
 #pragma unroll
-                for (int f = 0; f < kLoads; ++f)
-#pragma unroll
-                    for (int m = 0; m < MT; ++m)
-                        sum[m] = mfma_x_w<BF16>(xf[f][m], w[S][f], sum[m]);
+                for (int f = 0; f < kLoads; ++f) sum = mfma_x_w<BF16>(xf[f], w[S][f], sum);
             }
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    a[m][r] = KIND == kW4 ? fmaf(sum[m][r], xs[m][r], a[m][r]) : a[m][r] + sum[m][r];
+            for (int r = 0; r < 4; ++r)
+                a[r] = KIND == kW4 ? fmaf(sum[r], xs[r], a[r]) : a[r] + sum[r];
         };
 
-        f32x4 acc[kSteps][MT];
+        f32x4 acc[kSteps];
         int nlog = 0;
         while ((1 << nlog) < g.n) ++nlog;
         const int plog = glu ? 3 : 4;
         // row tiles of a wave per chunk, and floats of one
-        const int clog = P.panels > 1 ? 2 : min(4, 6 + MT - 1 - vlog);
+        const int clog = P.panels > 1 ? 2 : min(4, 6 - vlog);
         const int tile_floats = 16 << vlog;
         if (C.cols > 0) load_x(0, true);
         bool first = true;
@@ -660,9 +642,7 @@ __global__ __launch_bounds__(kStreamThreads, 2) void stream_kernel(const Grouped
             int here = 0;                                  // row tiles of the chunk so far
             do {
 #pragma unroll
-                for (int c = 0; c < kSteps; ++c)
-#pragma unroll
-                    for (int m = 0; m < MT; ++m) acc[c][m] = f32x4{0.f, 0.f, 0.f, 0.f};
+                for (int c = 0; c < kSteps; ++c) acc[c] = f32x4{0.f, 0.f, 0.f, 0.f};
                 for (int panel = 0; panel < P.panels; ++panel) {
                     if (P.panels > 1 && !first) load_x(panel, false);
                     first = false;
@@ -676,16 +656,14 @@ __global__ __launch_bounds__(kStreamThreads, 2) void stream_kernel(const Grouped
                         __builtin_amdgcn_sched_barrier(0);
                     });
                 }
+                if (4 * q < 1 << vlog) {
 #pragma unroll
-                for (int c = 0; c < kSteps; ++c)
+                    for (int c = 0; c < kSteps; ++c)
 #pragma unroll
-                    for (int m = 0; m < MT; ++m)
-                        if (m * 16 + 4 * q < 1 << vlog) {
-#pragma unroll
-                            for (int r = 0; r < 4; ++r)
-                                part[buf][wv][(here + c) * tile_floats + sum_at(m * 16 + 4 * q + r) +
-                                              i16] = acc[c][m][r];
-                        }
+                        for (int r = 0; r < 4; ++r)
+                            part[buf][wv][(here + c) * tile_floats + sum_at(4 * q + r) + i16] =
+                                acc[c][r];
+                }
                 here += kSteps;
                 step += kSteps;
             } while (here < 1 << clog && rtb + here * rw < rt1);
@@ -694,7 +672,7 @@ __global__ __launch_bounds__(kStreamThreads, 2) void stream_kernel(const Grouped
             // 4 adjacent outputs of a row per thread
             const int items = (rw << clog) << (nlog + plog - 2);
 #pragma unroll 1
-            for (int it = threadIdx.x; it < items; it += kStreamThreads) {
+            for (int it = threadIdx.x; it < items; it += kThreads) {
                 const int col = (it & ((1 << plog) / 4 - 1)) * 4;
                 const int r = (it >> (plog - 2)) & ((1 << nlog) - 1), t = it >> (plog - 2 + nlog);
                 const int rt = rtb + t, o = rt * per_tile + col;
@@ -703,7 +681,7 @@ __global__ __launch_bounds__(kStreamThreads, 2) void stream_kernel(const Grouped
                 if (yr < 0) continue;
                 const int v = X32 ? 2 * r : r;
                 const float* p = &part[buf][(t & (rw - 1)) << P.kw_log]
-                                      [(t >> (3 - P.kw_log)) * tile_floats + col];
+                                      [(t >> (kLogNW - P.kw_log)) * tile_floats + col];
                 const int a0 = sum_at(v), a1 = sum_at(v + 1);
                 f32x4 p0 = {0.f, 0.f, 0.f, 0.f}, p1 = p0;
 #pragma unroll 2
@@ -733,25 +711,27 @@ __global__ __launch_bounds__(kStreamThreads, 2) void stream_kernel(const Grouped
 #endif
 }
 
-template <int KIND, bool BF16, bool X32, int KB, int MT, int GM, bool ZEROS>
+template <int KIND, bool BF16, bool X32, int NW, int KB, int GM, bool ZEROS>
 hipError_t run_stream(const GroupedCall& C, const StreamPlan& P, hipStream_t st) {
-    const int64_t tiles =
-        int64_t(std::min(C.n_rows, C.n_experts)) + C.n_rows / (16 * MT / (X32 ? 2 : 1));
-    const unsigned grid = unsigned(std::min<int64_t>(tiles * P.row_tiles, compute_units()));
-    hipLaunchKernelGGL((stream_kernel<KIND, BF16, X32, KB, MT, GM, ZEROS>), dim3(grid),
-                       dim3(kStreamThreads), 0, st, C, P);
+    const int64_t tiles = int64_t(std::min(C.n_rows, C.n_experts)) + C.n_rows / (X32 ? 8 : 16);
+    const int64_t most = int64_t(compute_units()) * (8 / NW);
+    hipLaunchKernelGGL((stream_kernel<KIND, BF16, X32, NW, KB, GM, ZEROS>),
+                       dim3(unsigned(std::min<int64_t>(tiles * P.row_tiles, most))),
+                       dim3(NW * kWave), 0, st, C, P);
     return hipGetLastError();
 }
 
-// The split of the inputs: 4 blocks of 128 per wave where there are as many,
-// over up to 8 waves, then panels.
-inline StreamPlan plan_stream(const GroupedCall& C, int mt, int* kb) {
+// The split of the inputs: 4 blocks of 128 per wave where there are as many.
+// Up to 4 waves cover 2048 inputs: then workgroups have 4 waves and a compute
+// unit holds two, of which one streams while the other prepares a group's
+// rows.  Else 8 waves, and panels past 4096 inputs.
+inline StreamPlan plan_stream(const GroupedCall& C, int* nw, int* kb) {
     StreamPlan P{};
     const int blocks = std::max(1, (C.cols + 127) / 128);
     while (P.kw_log < 3 && (4 << P.kw_log) < blocks) ++P.kw_log;
+    *nw = P.kw_log == 3 ? 8 : 4;
     const int per = (blocks + (1 << P.kw_log) - 1) >> P.kw_log;
-    // (32 columns: registers for 2 blocks)
-    *kb = per >= 3 && mt == 1 ? 4 : std::min(per, 2);
+    *kb = per >= 3 ? 4 : per;
     P.panels = (blocks + (*kb << P.kw_log) - 1) / (*kb << P.kw_log);
     const int out = C.flags & PM_GROUPED_SWIGLU ? C.rows / 2 : C.rows;
     const int per_tile = C.flags & PM_GROUPED_SWIGLU ? 8 : 16;

@@ -8,7 +8,7 @@
 namespace pm {
 namespace {
 
-template <bool X32, int KB, int MT, bool ZEROS>
+template <bool X32, int NW, int KB, bool ZEROS>
 hipError_t run4_group(const GroupedCall& C, const StreamPlan& P, hipStream_t st) {
     // groups are read as aligned vectors of up to 4 scales
     auto vector_ok = [&](int group) {
@@ -17,29 +17,22 @@ hipError_t run4_group(const GroupedCall& C, const StreamPlan& P, hipStream_t st)
                reinterpret_cast<uintptr_t>(C.scales) % (2 * n) == 0 &&
                reinterpret_cast<uintptr_t>(C.zeros) % n == 0;
     };
-    if (vector_ok(128)) return run_stream<kW4, false, X32, KB, MT, kGroup128, ZEROS>(C, P, st);
-    if (vector_ok(64)) return run_stream<kW4, false, X32, KB, MT, kGroup64, ZEROS>(C, P, st);
-    if (vector_ok(32)) return run_stream<kW4, false, X32, KB, MT, kGroup32, ZEROS>(C, P, st);
-    return run_stream<kW4, false, X32, KB, MT, kAnyGroup, ZEROS>(C, P, st);
+    if (vector_ok(128)) return run_stream<kW4, false, X32, NW, KB, kGroup128, ZEROS>(C, P, st);
+    if (vector_ok(64)) return run_stream<kW4, false, X32, NW, KB, kGroup64, ZEROS>(C, P, st);
+    if (vector_ok(32)) return run_stream<kW4, false, X32, NW, KB, kGroup32, ZEROS>(C, P, st);
+    return run_stream<kW4, false, X32, NW, KB, kAnyGroup, ZEROS>(C, P, st);
 }
 
-template <bool X32, int MT, bool ZEROS>
+template <bool X32, bool ZEROS>
 hipError_t run4(const GroupedCall& C, hipStream_t st) {
-    int kb;
-    const StreamPlan P = plan_stream(C, MT, &kb);
+    int nw, kb;
+    const StreamPlan P = plan_stream(C, &nw, &kb);
+    if (nw == 8) return run4_group<X32, 8, 4, ZEROS>(C, P, st);
     switch (kb) {
-    case 1: return run4_group<X32, 1, MT, ZEROS>(C, P, st);
-    case 2: return run4_group<X32, 2, MT, ZEROS>(C, P, st);
-    default:
-        if constexpr (MT == 1) return run4_group<X32, 4, 1, ZEROS>(C, P, st);
-        return hipErrorInvalidValue;                      // plan_stream gives no such plan
+    case 1: return run4_group<X32, 4, 1, ZEROS>(C, P, st);
+    case 2: return run4_group<X32, 4, 2, ZEROS>(C, P, st);
+    default: return run4_group<X32, 4, 4, ZEROS>(C, P, st);
     }
-}
-
-template <bool X32>
-hipError_t run4_any(const GroupedCall& C, int mt, hipStream_t st) {
-    if (C.zeros) return mt == 1 ? run4<X32, 1, true>(C, st) : run4<X32, 2, true>(C, st);
-    return mt == 1 ? run4<X32, 1, false>(C, st) : run4<X32, 2, false>(C, st);
 }
 
 }  // namespace

@@ -3,8 +3,8 @@
 
 namespace pm {
 
-hipError_t launch_grouped_stream4(const GroupedCall& C, int mt, hipStream_t st) {
-    return run4_any<false>(C, mt, st);
+hipError_t launch_grouped_stream4(const GroupedCall& C, hipStream_t st) {
+    return C.zeros ? run4<false, true>(C, st) : run4<false, false>(C, st);
 }
 
 }  // namespace pm

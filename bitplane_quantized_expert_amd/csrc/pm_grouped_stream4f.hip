@@ -3,8 +3,8 @@
 
 namespace pm {
 
-hipError_t launch_grouped_stream4f(const GroupedCall& C, int mt, hipStream_t st) {
-    return run4_any<true>(C, mt, st);
+hipError_t launch_grouped_stream4f(const GroupedCall& C, hipStream_t st) {
+    return C.zeros ? run4<true, true>(C, st) : run4<true, false>(C, st);
 }
 
 }  // namespace pm

@@ -52,11 +52,11 @@ hipError_t launch_grouped(const GroupedCall& C, int kind, hipStream_t st);
 // Tiles of `rows` (128 or 256) x 256 (pm_grouped_tile.hip), 16-bit weights; the
 // offsets of a tile's rows in x must fit 32 bits.
 hipError_t launch_grouped_tiles(const GroupedCall& C, int rows, hipStream_t st);
-// Weights streamed past 16 * mt columns of activations, mt 1 or 2
-// (pm_grouped_stream.h); any sizes.
-hipError_t launch_grouped_stream16(const GroupedCall& C, int mt, hipStream_t st);
-hipError_t launch_grouped_stream4(const GroupedCall& C, int mt, hipStream_t st);
-hipError_t launch_grouped_stream4f(const GroupedCall& C, int mt, hipStream_t st);
+// Weights streamed past 16 columns of activations (pm_grouped_stream.h): 16-bit
+// weights, 4-bit weights with 16-bit and with fp32 activations; any sizes.
+hipError_t launch_grouped_stream16(const GroupedCall& C, hipStream_t st);
+hipError_t launch_grouped_stream4(const GroupedCall& C, hipStream_t st);
+hipError_t launch_grouped_stream4f(const GroupedCall& C, hipStream_t st);
 
 // Compute units of the current device.
 int compute_units();
