@@ -312,6 +312,9 @@ __global__ __launch_bounds__(NW * kWave, 2) void stream_kernel(const GroupedCall
     const int out = glu ? C.rows / 2 : C.rows;
     const int per_tile = glu ? 8 : 16;
 
+    // a short call's uses are loaded along with the offsets
+    const bool few = C.n_rows <= kWave;
+    const int u_few = few && lane < C.n_rows ? use_of(C, lane) : -1;
     Eight eight;
     // sorted rows of a tile: an fp32 row takes two columns
     constexpr int kTileRows = X32 ? 8 : 16;
@@ -358,7 +361,9 @@ __global__ __launch_bounds__(NW * kWave, 2) void stream_kernel(const GroupedCall
         const int rt1 = min(P.row_tiles, rt0 + left);
         left -= rt1 - rt0;
         // loads return in order: the uses come before any weights
-        const int u_lane = lane < g.n ? use_of(C, g.row0 + lane) : -1;
+        int u_lane = __shfl(u_few, (g.row0 + lane) & 63);
+        if (!few && lane < g.n) u_lane = use_of(C, g.row0 + lane);
+        u_lane = lane < g.n ? u_lane : -1;
 
         const auto wbuf = __builtin_amdgcn_make_buffer_rsrc(
             uni_ptr(const_cast<char*>(static_cast<const char*>(C.w)) + size_t(g.e) * w_bytes), 0,

@@ -88,8 +88,18 @@ __global__ __launch_bounds__(kTileThreads, 2) void tile_kernel(const GroupedCall
     struct Where {
         int e, row0, n, o0;                       // expert, rows, first output; n 0: no tile
     };
+    // A last round of at most half the workgroups is shared out by halves of
+    // 128 rows, which take half the time.  (128-row tiles wait for their
+    // weights, which halves would read twice.)
+    const int full = n_tiles / int(gridDim.x) * int(gridDim.x), rest = n_tiles - full;
+    const bool halves = BM == 256 && full > 0 && 2 * rest <= int(gridDim.x);
     auto locate = [&](int i) {
         Where w{0, 0, 0, 0};
+        int half = -1;
+        if (halves && i >= full) {
+            half = (i - full) & 1;
+            i = full + ((i - full) >> 1);
+        }
         if (i < n_tiles) {
             const int mt = i / nt;
             const int e = tile_expert(C, before, mt);
@@ -99,6 +109,11 @@ __global__ __launch_bounds__(kTileThreads, 2) void tile_kernel(const GroupedCall
             w.e = uni(e);
             w.row0 = uni(ok ? g.row0 + int(skip) : 0);
             w.n = uni(ok ? min(g.n - int(skip), BM) : 0);
+            if (half == 0) w.n = min(w.n, BM / 2);
+            if (half == 1) {
+                w.row0 += BM / 2;
+                w.n = max(w.n - BM / 2, 0);
+            }
             w.o0 = uni((i - mt * nt) * (GLU ? kTileN / 2 : kTileN));
         }
         return w;
