@@ -43,6 +43,7 @@ PM_GROUPED_SWIGLU = 4
 PM_ROUTE_MAX_EXPERTS = 4096
 PM_ROUTE_MAX_TOPK = 64
 PM_GROUPED_MAX_EXPERTS = 4096
+PM_ROUTED_MAX_USES = 0x7FFF0000
 
 _STATUS = {0: "PM_OK", -1: "PM_ERR_ARG", -2: "PM_ERR_SHAPE", -3: "PM_ERR_PREFIX",
            -4: "PM_ERR_NOT_RESIDENT", -5: "PM_ERR_OOM", -6: "PM_ERR_HIP", -7: "PM_ERR_STATE"}

@@ -3,6 +3,8 @@
 #include <hip/hip_fp16.h>
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
+
 #include "pm_convert.h"
 #include "pm_device.h"
 #include "pm_routed.h"
@@ -17,15 +19,12 @@ namespace {
 // element's: the hardware splits the accesses that cross a line).  U rows are
 // on their way together.
 template <int ZT, int YT, int U>
-__global__ __launch_bounds__(256) void combine_uses_kernel(int n_tokens, int top_k, int hidden,
-                                                           int chunks, const void* z, int64_t ldz,
-                                                           const float* w, void* y, int64_t ldy) {
+__device__ __forceinline__ void combine_chunk(int64_t t, int chunk, int top_k, int hidden,
+                                              const void* z, int64_t ldz, const float* w, void* y,
+                                              int64_t ldy) {
     constexpr int V = ZT == PM_F32 ? 4 : 8, ZB = ZT == PM_F32 ? 4 : 2, YB = YT == PM_F32 ? 4 : 2;
-    const int64_t id = int64_t(blockIdx.x) * 4 + uni(threadIdx.x >> 6);
-    const int64_t t = id / chunks;
-    if (t >= n_tokens) return;
     // (lanes past the row stay: each holds one weight)
-    const int c = min((int(id - t * chunks) * kWave + int(threadIdx.x & 63)) * V, hidden - 1);
+    const int c = int(min((int64_t(chunk) * kWave + (threadIdx.x & 63)) * V, int64_t(hidden) - 1));
     // the last columns of a row are taken as a whole vector that ends there;
     // rows of fewer columns element by element
     const bool whole = hidden >= V;
@@ -62,6 +61,20 @@ __global__ __launch_bounds__(256) void combine_uses_kernel(int n_tokens, int top
         for (int j = 0; j < top_k; ++j)
             if (wp[j] != 0.0f) v = fmaf(wp[j], load_f32<ZT>(zp + j * ldz * ZB, i), v);
         store_f32<YT>(y, t * ldy + c0 + i, v);
+    }
+}
+
+// A wave goes on by the waves of the grid, which is held below the 2^32 threads
+// of a launch; up to 2^20 workgroups every wave has one chunk at most.
+template <int ZT, int YT, int U>
+__global__ __launch_bounds__(256) void combine_uses_kernel(int n_tokens, int top_k, int hidden,
+                                                           int chunks, const void* z, int64_t ldz,
+                                                           const float* w, void* y, int64_t ldy) {
+    const int64_t all = int64_t(n_tokens) * chunks;
+    for (int64_t id = int64_t(blockIdx.x) * 4 + uni(threadIdx.x >> 6); id < all;
+         id += int64_t(gridDim.x) * 4) {
+        const int64_t t = id / chunks;
+        combine_chunk<ZT, YT, U>(t, int(id - t * chunks), top_k, hidden, z, ldz, w, y, ldy);
     }
 }
 
@@ -124,8 +137,8 @@ template <int ZT, int YT>
 static hipError_t combine_typed(int n_tokens, int top_k, int hidden, const void* z, int64_t ldz,
                                 const float* w, void* y, int64_t ldy, hipStream_t st) {
     const int per_wave = kWave * (ZT == PM_F32 ? 4 : 8);
-    const int chunks = (hidden + per_wave - 1) / per_wave;
-    const dim3 grid(unsigned((int64_t(n_tokens) * chunks + 3) / 4));
+    const int chunks = hidden / per_wave + (hidden % per_wave != 0);
+    const dim3 grid(unsigned(std::min<int64_t>((int64_t(n_tokens) * chunks + 3) / 4, 1 << 20)));
     // all rows of a token together where they are 10 at most
     auto* f = &combine_uses_kernel<ZT, YT, 8>;
     if (top_k <= 2) f = &combine_uses_kernel<ZT, YT, 2>;

@@ -12,7 +12,8 @@ namespace pm {
 // 33/34; with 1024 inputs (4096 outputs) 160/148 already at 2 rows.  Tiles of
 // 256 rows instead of 128 from 224 rows per group on, where there are two for
 // each compute unit: 353/359 us at 192 rows, 438/427 at 256, 760/726 at 512 (128
-// experts, 1024 inputs, 4096 outputs).  The groups' sizes are on the device;
+// experts, 1024 inputs, 4096 outputs), or where 128-row tiles' three stages leave
+// no room in LDS for the table of experts (above some 3500).  The groups' sizes are on the device;
 // these are rows per group if every expert had some.
 hipError_t launch_grouped(const GroupedCall& C, int kind, hipStream_t st) {
     if (kind == kW4)
@@ -23,7 +24,8 @@ hipError_t launch_grouped(const GroupedCall& C, int kind, hipStream_t st) {
         (x_rows * C.ldx + C.cols) * 2 >= 0xFFFFFFF0ll)
         return launch_grouped_stream16(C, st);
     const int64_t tiles256 = (C.n_rows / 256) * int64_t((C.rows + 255) / 256);
-    const bool big = C.n_rows >= 224 * groups && tiles256 >= 2 * compute_units();
+    const bool big =
+        (C.n_rows >= 224 * groups && tiles256 >= 2 * compute_units()) || !tiles128_fit(C);
     return launch_grouped_tiles(C, big ? 256 : 128, st);
 }
 

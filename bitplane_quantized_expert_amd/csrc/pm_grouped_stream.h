@@ -31,10 +31,10 @@
 // v_permlane swaps) makes them 32 adjacent inputs.
 //
 // Activations meet 4-bit weights as fp16; bf16 and fp32 are scaled by a power
-// of two per row and wave so that the largest lies in [2^14, 2^15): what is
-// lost is below 2^-39 of the largest.  An fp32 row takes two columns, its
-// value rounded to fp16 and the rest (times 2^11) rounded again, together
-// 2^-24 of the value.  The waves convert a few columns at a time into LDS and
+// of two per row and wave so that the largest lies in [2^14, 2^15): a bf16
+// value loses at most 2^-39 of the largest, below fp16's normal range.  An fp32
+// row takes two columns, its value rounded to fp16 and the rest (times 2^11)
+// rounded again: off by 2^-23 of the value, or 2^-50 of the largest.  The waves convert a few columns at a time into LDS and
 // take their operands from there.
 #pragma once
 

@@ -331,13 +331,17 @@ __global__ __launch_bounds__(kTileThreads, 2) void tile_kernel(const GroupedCall
 #endif
 }
 
+// LDS of a workgroup: the stages, the rows of y, the table of experts.
+inline size_t tile_lds(const GroupedCall& C, int bm, int stages) {
+    return size_t(stages) * (bm + kTileN) * kTileK * 2 + (2 * bm + C.n_experts + 1) * sizeof(int);
+}
+
 template <int WT, int YT, bool GLU, int BM, int S>
 hipError_t run_tiles(const GroupedCall& C, hipStream_t st) {
     const int out = GLU ? C.rows / 2 : C.rows;
     const int per = GLU ? kTileN / 2 : kTileN;
     const int nt = (out + per - 1) / per;
-    const size_t lds =
-        S * (BM + kTileN) * kTileK * 2 + (2 * BM + C.n_experts + 1) * sizeof(int);
+    const size_t lds = tile_lds(C, BM, S);
     auto* f = tile_kernel<WT, YT, GLU, BM, S>;
     hipError_t e = allow_lds(reinterpret_cast<const void*>(f), kTileMaxLds);
     if (e != hipSuccess) return e;
@@ -365,6 +369,8 @@ hipError_t run_tiles_typed(const GroupedCall& C, hipStream_t st) {
 }
 
 }  // namespace
+
+bool tiles128_fit(const GroupedCall& C) { return tile_lds(C, 128, 3) <= kTileMaxLds; }
 
 hipError_t launch_grouped_tiles(const GroupedCall& C, int rows, hipStream_t st) {
     return rows == 128 ? run_tiles_typed<128, 3>(C, st) : run_tiles_typed<256, 2>(C, st);

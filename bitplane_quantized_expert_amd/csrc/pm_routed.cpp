@@ -36,6 +36,10 @@ static size_t span(size_t n, int64_t ld, size_t cols, int type) {
 // addresses of a valid call never wrap.
 static constexpr int64_t kMaxLd = int64_t(1) << 31;
 
+// Uses of a call: rounding their number up to a tile, or going on by a few
+// waves' tokens, stays within 32 bits.
+static bool uses_ok(int64_t n) { return n <= PM_ROUTED_MAX_USES; }
+
 // ---------------------------------------------------------------- device properties
 static constexpr int kMaxDevices = 64;
 
@@ -78,7 +82,7 @@ void pm::route_blocks(int n_tokens, int* block_tokens, int* n_blocks) {
 static bool route_sizes_ok(int n_tokens, int n_experts, int top_k) {
     return n_tokens >= 0 && n_experts >= 1 && n_experts <= PM_ROUTE_MAX_EXPERTS && top_k >= 1 &&
            top_k <= PM_ROUTE_MAX_TOPK && top_k <= n_experts &&
-           int64_t(n_tokens) * top_k < (int64_t(1) << 31);
+           uses_ok(int64_t(n_tokens) * top_k);
 }
 
 extern "C" size_t pm_route_workspace_bytes(int n_tokens, int n_experts, int top_k) {
@@ -155,14 +159,14 @@ static pm_status check_grouped(pm_grouped_shape s, pm_grouped_rows r, const void
     if (s.n_experts > kMaxGroupedExperts)
         return failf(PM_ERR_SHAPE, "grouped: %d experts, above %d", s.n_experts,
                      kMaxGroupedExperts);
-    if (int64_t(s.rows) * s.cols >= (int64_t(1) << 30))
+    if (int64_t(s.rows) * std::max(s.cols, 1) >= (int64_t(1) << 30))
         return failf(PM_ERR_SHAPE, "grouped: a matrix of %d x %d holds 2^30 weights or more",
                      s.rows, s.cols);
     if (flags & ~uint32_t(PM_GROUPED_GATHER | PM_GROUPED_SCATTER | PM_GROUPED_SWIGLU))
         return failf(PM_ERR_ARG, "grouped: flags 0x%x", flags);
     if ((flags & PM_GROUPED_SWIGLU) && s.rows % 2)
         return failf(PM_ERR_SHAPE, "grouped: gate and up of %d rows together", s.rows);
-    if (r.n_rows < 0 || r.top_k < 1)
+    if (r.n_rows < 0 || r.top_k < 1 || !uses_ok(r.n_rows))
         return failf(PM_ERR_ARG, "grouped: n_rows=%d top_k=%d", r.n_rows, r.top_k);
     if (y_type != PM_F32 && y_type != x_type)
         return failf(PM_ERR_ARG, "grouped: x of type %d, y of type %d", x_type, y_type);
@@ -274,7 +278,7 @@ extern "C" pm_status pm_encode_w4_device(pm_matrix_shape s, const void* d_w, int
 extern "C" pm_status pm_combine_uses(int n_tokens, int top_k, int hidden, const void* d_z,
                                      int z_type, int64_t ldz, const float* d_w, void* d_y,
                                      int y_type, int64_t ldy, void* stream) {
-    if (n_tokens < 0 || top_k < 1 || hidden < 0 || int64_t(n_tokens) * top_k >= (int64_t(1) << 31))
+    if (n_tokens < 0 || top_k < 1 || hidden < 0 || !uses_ok(int64_t(n_tokens) * top_k))
         return failf(PM_ERR_ARG, "combine: n_tokens=%d top_k=%d hidden=%d", n_tokens, top_k,
                      hidden);
     if (!type_ok(z_type) || (y_type != PM_F32 && y_type != z_type))

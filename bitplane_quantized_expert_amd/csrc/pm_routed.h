@@ -52,6 +52,9 @@ hipError_t launch_grouped(const GroupedCall& C, int kind, hipStream_t st);
 // Tiles of `rows` (128 or 256) x 256 (pm_grouped_tile.hip), 16-bit weights; the
 // offsets of a tile's rows in x must fit 32 bits.
 hipError_t launch_grouped_tiles(const GroupedCall& C, int rows, hipStream_t st);
+// Whether the table of experts lies in LDS beside the stages of 128-row tiles
+// (beside those of 256 rows it always does).
+bool tiles128_fit(const GroupedCall& C);
 // Weights streamed past 16 columns of activations (pm_grouped_stream.h): 16-bit
 // weights, 4-bit weights with 16-bit and with fp32 activations; any sizes.
 hipError_t launch_grouped_stream16(const GroupedCall& C, hipStream_t st);

@@ -372,7 +372,9 @@ pm_status pm_moe_token_forward(pm_store* s, int layer, int n_tokens, int top_k,
  *   pm_combine_uses        y[t] = sum_j w[t][j] * row (t, j).
  * pm_grouped_gemm_w4 takes the place of pm_grouped_gemm for 4-bit experts.
  * Sums run in fp32 in a fixed order (no atomics); each output is rounded
- * once, to nearest even, to its type.  Element types: */
+ * once, to nearest even, to its type.  A call has at most PM_ROUTED_MAX_USES
+ * uses (else PM_ERR_ARG).  Element types: */
+#define PM_ROUTED_MAX_USES 0x7FFF0000
 enum { PM_F32 = 0, PM_F16 = 1, PM_BF16 = 2 };
 
 /* Router [T c4], the selection of pm_route_topk on the device.
@@ -384,14 +386,15 @@ enum { PM_F32 = 0, PM_F16 = 1, PM_BF16 = 2 };
  * top_k others has id -1 and weight 0 in its last slots, and one with none
  * (padding) is routed nowhere.  Several +inf share the weight equally.
  *   d_offsets int32 [n_experts + 1], d_order int32 [n_tokens * top_k], both
- *   null (no sorting) or neither (d_order may be null without tokens): the uses of expert e are d_order[d_offsets[e] ..
- *   d_offsets[e+1]), in ascending order.  Entries of d_order from
+ *   null (no sorting) or neither (d_order may be null without tokens): the
+ *   uses of expert e are d_order[d_offsets[e] .. d_offsets[e+1]), in ascending
+ *   order.  Entries of d_order from
  *   d_offsets[n_experts] on are left as they were.
  *   d_ws: pm_route_workspace_bytes(...) bytes of workspace, 16-byte aligned
  *   (null when that is 0 or d_order is null); its contents need not be kept
  *   or cleared, and calls that may overlap need one each.
  * n_experts <= PM_ROUTE_MAX_EXPERTS and top_k <= PM_ROUTE_MAX_TOPK (else
- * PM_ERR_SHAPE), top_k <= n_experts, n_tokens * top_k < 2^31 (PM_ERR_ARG).
+ * PM_ERR_SHAPE), top_k <= n_experts (PM_ERR_ARG).
  * The outputs may not overlap the logits. */
 #define PM_ROUTE_MAX_EXPERTS 4096
 #define PM_ROUTE_MAX_TOPK 64
@@ -409,8 +412,8 @@ pm_status pm_route_topk_device(int n_tokens, int n_experts, int top_k, const voi
  * otherwise.  Under PM_GROUPED_SWIGLU the first rows/2 rows of W[e] are the
  * gate and the others the up matrix, y has rows/2 columns and
  *     y[yr] = SiLU(p[0 .. rows/2)) * p[rows/2 .. rows),  SiLU(g) = g / (1 + e^-g).
- *   s.n_experts in 1 .. PM_GROUPED_MAX_EXPERTS (else PM_ERR_SHAPE); n_rows is the number of entries of d_order, at least
- *   d_offsets[n_experts]; d_offsets[0] = 0 and they do not decrease (other
+ *   s.n_experts in 1 .. PM_GROUPED_MAX_EXPERTS (else PM_ERR_SHAPE); n_rows is
+ *   the number of entries of d_order, at least d_offsets[n_experts]; d_offsets[0] = 0 and they do not decrease (other
  *   offsets read and write nothing out of bounds, but give unspecified
  *   rows).  Rows of y that no i maps to are left as they were, and an
  *   i whose u is outside 0 .. n_rows-1 is left out.  A u that occurs twice under
@@ -421,7 +424,7 @@ pm_status pm_route_topk_device(int n_tokens, int n_experts, int top_k, const voi
  *   to reach no output.
  * Alignment: weights, d_x and each row of x 16 bytes (ldx a multiple of 16
  * bytes), d_y its element.  x and y may not overlap (PM_ERR_ARG).  One
- * matrix holds fewer than 2^30 weights (PM_ERR_SHAPE).  cols == 0 gives
+ * matrix has fewer than 2^30 rows and weights (PM_ERR_SHAPE).  cols == 0 gives
  * zeros. */
 #define PM_GROUPED_MAX_EXPERTS 4096
 typedef struct { int32_t n_experts, rows, cols; } pm_grouped_shape;
@@ -442,7 +445,11 @@ pm_status pm_grouped_gemm(pm_grouped_shape s, int type, const void* d_w, pm_grou
  *   d_scales fp16, d_zeros uint8 [n_experts][rows][cols/group]: one scale and
  *   zero point per `group` inputs of one row; d_zeros null: z = 8.
  *   group % 32 == 0, cols % group == 0 (PM_ERR_SHAPE).
- * x and y are fp32, fp16 or bf16, y fp32 or of x's type. */
+ * x and y are fp32, fp16 or bf16, y fp32 or of x's type.  The products take
+ * fp16 values: x in fp16 enters as it is, bf16 and fp32 times a power of two
+ * per row and share of 128 to 512 inputs.  What bf16 loses thereby is at most
+ * 2^-39 of the share's largest; fp32 enters as the sum of two halves, off by
+ * at most 2^-23 of its value or 2^-50 of the share's largest. */
 pm_status pm_grouped_gemm_w4(pm_grouped_shape s, int group, const uint8_t* d_q,
                              const uint16_t* d_scales, const uint8_t* d_zeros,
                              pm_grouped_rows r, const void* d_x, int x_type, int64_t ldx,

@@ -103,6 +103,23 @@ def test_route_without_sorting_and_without_tokens():
     assert not off.any()
 
 
+def test_route_many_tokens():
+    """More tokens than 256 blocks of the sorting hold."""
+    report("route 17 000 000 tokens")
+    T = 17_000_000
+    l = torch.randn(T, 2, generator=rc.gen(2), device="cuda")
+    l[12345:23456] = -float("inf")
+    ids, w, off, order = run_route(l, 1)
+    want = torch.where(l[:, 0] >= l[:, 1], 0, 1)
+    want[12345:23456] = -1
+    assert torch.equal(ids[:, 0].long(), want)
+    assert torch.equal(w[:, 0], (want >= 0).float())
+    n0, n1 = int((want == 0).sum()), int((want == 1).sum())
+    assert off.tolist() == [0, n0, n0 + n1]
+    assert torch.equal(order[:n0].long(), (want == 0).nonzero()[:, 0])
+    assert torch.equal(order[n0:n0 + n1].long(), (want == 1).nonzero()[:, 0])
+
+
 # ---------------------------------------------------------------- grouped products
 def make_w16(E, R, C, dt, seed):
     w = torch.empty(E, R, C, dtype=dt, device="cuda")
@@ -270,6 +287,75 @@ def test_grouped16_repeats_bit_for_bit_and_on_two_streams():
         assert torch.equal(y, ys[0])
 
 
+@pytest.mark.parametrize("counts,R", [([2100, 2000], 8192),      # 544 tiles: a short last round
+                                      ([1800, 0, 2900, 3], 8190),  # outputs off the tile
+                                      ([256, 4000], 8448)])
+def test_grouped16_large_tiles(counts, R):
+    """Enough 256-row tiles for several rounds of the device, the last of them
+    short or long."""
+    report(f"grouped large tiles {counts} {R}")
+    run_grouped16(counts, R, 136, "bf16", "f32", 1, SCATTER, seed=11)
+    run_grouped16(counts, R, 64, "f16", "f16", 2, GATHER | SWIGLU, seed=12)
+
+
+@pytest.mark.parametrize("n", [63, 64, 65, 128, 129])
+def test_grouped16_short_calls(n):
+    """Around the number of rows up to which the uses are loaded at the start."""
+    report(f"grouped {n} rows")
+    counts = [1] * (n - 20) + [0, 13, 7]
+    run_grouped16(counts, 40, 2048, "bf16", "f32", 3, GATHER, seed=13)
+    run_grouped16(counts, 40, 4096, "f16", "f32", 1, SCATTER, seed=13)
+
+
+def test_grouped16_offsets_beyond_32_bits():
+    """Rows of x and y so far apart that their byte offsets pass 2^32, through
+    the kernels of few and of many rows."""
+    report("grouped: offsets beyond 32 bits")
+    C, R, ld = 64, 48, 1 << 30
+    xbuf = torch.empty(2 * ld + C, dtype=torch.bfloat16, device="cuda")
+    x = xbuf.as_strided((3, C), (ld, 1))
+    x.copy_(torch.randn(3, C, generator=rc.gen(1), device="cuda"))
+    w = make_w16(2, R, C, torch.bfloat16, 2)
+    for counts, top_k in (([3, 3], 2), ([400, 300], 234)):
+        off, order = rc.groups(counts, 3)
+        n = sum(counts)
+        y = torch.full((n, R), 3.0, device="cuda")
+        pm.pm_grouped_gemm(w, x, y, off, order, top_k, GATHER | SCATTER)
+        want = rc.grouped_plain(lambda e: w[e].double(), x, off, order, n, top_k, True, True, False)
+        rc.check_grouped(y, 3.0, want, f"x, {n} rows")
+    del xbuf, x
+    ybuf = torch.empty(2 * ld + R, dtype=torch.bfloat16, device="cuda")
+    y = ybuf.as_strided((3, R), (ld, 1))
+    y.fill_(3.0)
+    x = torch.randn(3, C, generator=rc.gen(1), device="cuda").bfloat16()
+    off, order = rc.groups([2, 1], 4)
+    pm.pm_grouped_gemm(w, x, y, off, order, 1, SCATTER)
+    want = rc.grouped_plain(lambda e: w[e].double(), x, off, order, 3, 1, False, True, False)
+    rc.check_grouped(y, 3.0, want, "y")
+    del ybuf, y
+    # tiles whose rows lie beyond 2^32 bytes of x and y
+    ld, counts = 1 << 22, [400, 300]
+    x = torch.empty(700 * ld, dtype=torch.bfloat16, device="cuda").as_strided((700, C), (ld, 1))
+    x.copy_(torch.randn(700, C, generator=rc.gen(5), device="cuda"))
+    y = torch.empty(700 * ld, dtype=torch.bfloat16, device="cuda").as_strided((700, R), (ld, 1))
+    off, order = rc.groups(counts, 6)
+    for flags in (0, SCATTER):
+        y.fill_(3.0)
+        pm.pm_grouped_gemm(w, x, y, off, order, 1, flags)
+        want = rc.grouped_plain(lambda e: w[e].double(), x, off, order, 700, 1, False, bool(flags),
+                                False)
+        rc.check_grouped(y, 3.0, want, f"tiles, flags {flags}")
+
+
+def test_grouped16_most_experts():
+    report("grouped: 4096 experts")
+    counts = np.zeros(4096, np.int64)
+    counts[[0, 1, 63, 64, 2047, 4094, 4095]] = [1, 2, 3, 20, 1, 5, 1]
+    run_grouped16(counts.tolist(), 16, 64, "bf16", "f32", 1, 0, seed=14)
+    counts[[5, 4000]] = [90000, 120000]
+    run_grouped16(counts.tolist(), 16, 64, "bf16", "f32", 1, 0, seed=14)
+
+
 # ---------------------------------------------------------------- 4-bit weights
 def make_w4(E, R, C, group, zeros, seed):
     g = rc.gen(seed)
@@ -346,6 +432,40 @@ def test_w4_odd_rows(R):
     if R % 2 == 0:
         run_w4([2, 0, 9, 1], R, 384, 128, False, "bf16", "f32", 3, GATHER | SWIGLU, seed=4,
                order=False)
+
+
+@pytest.mark.parametrize("group,C", [(128, 4224), (64, 8320), (32, 4128), (96, 4896), (256, 8192),
+                                     (128, 12288), (2176, 4352)])
+def test_w4_many_inputs(group, C):
+    """More inputs than the waves hold at once."""
+    report(f"w4 group {group} cols {C}")
+    for ty in ("f32", "bf16"):
+        run_w4([1, 0, 3, 17], 34, C, group, True, ty, "f32", 1, SCATTER, seed=6)
+    run_w4([9, 2], 40, C, group, False, "f16", "f16", 2, GATHER | SWIGLU, seed=7)
+
+
+def test_w4_many_rows_and_experts():
+    report("w4: 512 experts, ragged")
+    counts = np.random.default_rng(1).integers(0, 4, 512)
+    counts[[0, 200, 511]] = [70, 33, 129]
+    run_w4(counts.tolist(), 48, 256, 128, True, "bf16", "bf16", 4, GATHER | SWIGLU, seed=8)
+    run_w4(counts.tolist(), 33, 384, 64, False, "f32", "f32", 1, SCATTER, seed=9)
+
+
+def test_w4_strides_and_rows_outside():
+    report("w4 strides, untouched rows, order entries out of range")
+    run_w4([2, 5, 0, 9], 50, 96, 32, True, "f16", "f32", 2, GATHER, seed=6, pad=3, n_rows=70)
+    run_w4([2, 5, 0, 9], 50, 96, 32, False, "f32", "f32", 1, 0, seed=6, pad=1, order=False)
+    off, order = rc.groups([4, 9, 3], 1)
+    order[2], order[7], order[11] = -1, 16, 2 ** 31 - 1
+    q, sc, z = make_w4(3, 40, 64, 32, True, 1)
+    x = torch.randn(16, 64, generator=rc.gen(2), device="cuda")
+    for flags in (SCATTER, 0, GATHER):
+        y = torch.full((16, 40), 3.0, device="cuda")
+        pm.pm_grouped_gemm_w4(q, sc, z, 32, x, y, off, order, 1, flags)
+        want = rc.grouped_plain(lambda e: rc.decode_w4(q[e], sc[e], z[e], 32), x, off, order, 16,
+                                1, bool(flags & GATHER), bool(flags & SCATTER), False)
+        rc.check_grouped(y, 3.0, want, f"flags {flags}")
 
 
 @pytest.mark.parametrize("ty", ["f32", "f16", "bf16"])
@@ -471,6 +591,18 @@ def test_combine(T, K, H, z_ty, y_ty, pad):
     tol = tol + half * (want.abs() + tol) + torch.finfo(y.dtype).smallest_normal * half
     assert torch.all((y.double() - want).abs() <= tol)
     assert torch.all(yb[:, H:] == 3.0)
+
+
+@pytest.mark.parametrize("H", [4, 8])
+def test_combine_many_tokens(H):
+    """More tokens than one grid's waves."""
+    report(f"combine 5 000 000 x {H}")
+    T = 5_000_000
+    z = torch.randn(T, H, generator=rc.gen(H), device="cuda").bfloat16()
+    w = torch.full((T, 1), 0.5, device="cuda")
+    y = torch.full((T, H), 3.0, dtype=torch.bfloat16, device="cuda")
+    pm.pm_combine_uses(z, w, y)
+    assert torch.equal(y, z * 0.5)
 
 
 # ---------------------------------------------------------------- whole layers
@@ -605,6 +737,29 @@ def test_captured_layer_serves_new_tokens(bits, dt):
             L.run()
             torch.cuda.synchronize()
             assert torch.equal(L.y, got), rep
+
+
+def test_layers_on_two_streams_at_once():
+    """Two layers, each with its own buffers, issued in turn on two streams
+    give what each gives alone."""
+    report("two layers on two streams")
+    Ls = [Layer(40, 32, 4, 512, 256, 16, torch.bfloat16), Layer(6, 32, 4, 512, 256, 4, torch.float32)]
+    for i, L in enumerate(Ls):
+        L.new_tokens(20 + i)
+        L.run()
+    torch.cuda.synchronize()
+    alone = [L.y.clone() for L in Ls]
+    streams = [torch.cuda.Stream() for _ in Ls]
+    for rep in range(5):
+        for L in Ls:
+            L.y.zero_()
+        torch.cuda.synchronize()
+        for _ in range(3):
+            for L, st in zip(Ls, streams):
+                L.run(st)
+        torch.cuda.synchronize()
+        for L, want in zip(Ls, alone):
+            assert torch.equal(L.y, want), rep
 
 
 def test_grouped_on_materialized_prefixes():

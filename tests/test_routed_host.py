@@ -36,6 +36,7 @@ def test_route_refusals():
     refused(route(E=4097, ld=4097), pm.PM_ERR_SHAPE)
     refused(route(E=100, ld=100, K=65), pm.PM_ERR_SHAPE)
     refused(route(T=1 << 30, K=2), pm.PM_ERR_ARG)
+    refused(route(T=pm.PM_ROUTED_MAX_USES + 1, K=1), pm.PM_ERR_ARG)
     refused(route(ty=3), pm.PM_ERR_ARG, "type")
     refused(route(ld=15), pm.PM_ERR_ARG, "distance")
     refused(route(order=None), pm.PM_ERR_ARG, "together")
@@ -90,6 +91,8 @@ def test_grouped_refusals(call):
     refused(call(s=shape(e=pm.PM_GROUPED_MAX_EXPERTS + 1)), pm.PM_ERR_SHAPE, "experts")
     refused(call(s=shape(r=-1)), pm.PM_ERR_SHAPE)
     refused(call(s=shape(r=1 << 15, c=1 << 15)), pm.PM_ERR_SHAPE, "2^30")
+    refused(call(s=shape(r=1 << 30, c=0)), pm.PM_ERR_SHAPE, "2^30")
+    refused(call(r=rows(n=pm.PM_ROUTED_MAX_USES + 1)), pm.PM_ERR_ARG, "n_rows")
     refused(call(s=shape(r=63), flags=pm.PM_GROUPED_SWIGLU), pm.PM_ERR_SHAPE, "gate")
     refused(call(flags=8), pm.PM_ERR_ARG, "flags")
     refused(call(r=rows(n=-1)), pm.PM_ERR_ARG)
@@ -149,6 +152,7 @@ def test_combine_refusals():
     refused(comb(K=0), pm.PM_ERR_ARG)
     refused(comb(H=-1), pm.PM_ERR_ARG)
     refused(comb(T=1 << 30), pm.PM_ERR_ARG)
+    refused(comb(T=pm.PM_ROUTED_MAX_USES + 1, K=1), pm.PM_ERR_ARG)
     refused(comb(zt=3), pm.PM_ERR_ARG, "type")
     refused(comb(yt=pm.PM_F16), pm.PM_ERR_ARG, "type")
     refused(comb(ldz=15), pm.PM_ERR_ARG, "distance")
