@@ -1,6 +1,6 @@
 // Products grouped by expert for groups of few rows: the kernel's template,
 // instantiated for 16-bit weights in pm_grouped_stream16.hip and for 4-bit
-// weights in pm_grouped_stream4.hip.
+// weights in pm_grouped_stream4.hip and pm_grouped_stream4f.hip.
 //
 //   D[v][o] = sum_k x[v][k] W[o][k]   (v_mfma_f32_16x16x32, fp32 sums)
 //
@@ -36,6 +36,15 @@
 // row takes two columns, its value rounded to fp16 and the rest (times 2^11)
 // rounded again: off by 2^-23 of the value, or 2^-50 of the largest.  The waves convert a few columns at a time into LDS and
 // take their operands from there.
+//
+// Measured: 80 rows over 512 experts, 2048 x 4096 fp16 with gate and up: 212 to
+// 230 us, 5.4 to 5.9 TB/s (a large copy reaches 4.8).  4-bit: 640 rows over 512
+// experts, 4096 x 1024 with zero points, bf16: 163 to 170 us, 4.9 TB/s; 10 rows
+// of fp32, 2048 x 4096 with gate and up: 20 us for 43 MB, of which the stream
+// takes 9 and finding the groups, converting x and the last sums the rest.
+// Above some 64 rows per expert the decoding, repeated for every 16 columns,
+// bounds the 4-bit kernel: 64 experts of 4096 x 4096 with 32, 64, 128 bf16 rows
+// each take 261, 500, 997 us.
 #pragma once
 
 #include <hip/hip_runtime.h>

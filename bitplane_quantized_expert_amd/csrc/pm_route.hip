@@ -16,6 +16,12 @@
 // sum over lower experts and earlier blocks, plus its rank among the uses of
 // its block with the same expert.  Counts are integers and ranks come from
 // ballots, so the order never depends on timing.
+//
+// Measured (kernel time): 1 token, 512 experts, top-10: 5.6 us in one launch,
+// bound by the chain of dependent steps of one wave.  1003 tokens, 60 experts,
+// top-4: 4.8 + 6.0 us.  16384 tokens, 512 experts, top-10: 15.5 us (33.6 MB of
+// logits, 2.2 TB/s; the selection's instructions bound it) + 11.1 us of sorting,
+// of which adding up the table's columns in every workgroup is the most.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
