@@ -26,6 +26,7 @@ TARGETS = [
       os.path.join(PKG, "csrc", "pm_mfma.hip"), os.path.join(PKG, "csrc", "pm_routed.cpp"),
       os.path.join(PKG, "csrc", "pm_route.hip"), os.path.join(PKG, "csrc", "pm_grouped.hip"),
       os.path.join(PKG, "csrc", "pm_grouped_tile.hip"),
+      os.path.join(PKG, "csrc", "pm_grouped_tile4.hip"),
       os.path.join(PKG, "csrc", "pm_grouped_stream16.hip"),
       os.path.join(PKG, "csrc", "pm_grouped_stream4.hip"),
       os.path.join(PKG, "csrc", "pm_grouped_stream4f.hip"), os.path.join(PKG, "csrc", "pm_combine.hip")]),

@@ -16,12 +16,15 @@ namespace pm {
 // no room in LDS for the table of experts (above some 3500).  The groups' sizes are on the device;
 // these are rows per group if every expert had some.
 hipError_t launch_grouped(const GroupedCall& C, int kind, hipStream_t st) {
-    if (kind == kW4)
-        return C.x_type == PM_F32 ? launch_grouped_stream4f(C, st) : launch_grouped_stream4(C, st);
     const int64_t groups = std::min(C.n_experts, C.n_rows);
     const int64_t x_rows = C.flags & PM_GROUPED_GATHER ? (C.n_rows - 1) / C.top_k + 1 : 256;
-    if (int64_t(C.n_rows) * 512 <= C.cols * groups ||
-        (x_rows * C.ldx + C.cols) * 2 >= 0xFFFFFFF0ll)
+    const bool far = (x_rows * C.ldx + C.cols) * 2 >= 0xFFFFFFF0ll;
+    if (kind == kW4) {
+        if (C.x_type == PM_F32) return launch_grouped_stream4f(C, st);
+        if (C.n_rows < 48 * groups || far) return launch_grouped_stream4(C, st);
+        return launch_grouped_tiles4(C, st);
+    }
+    if (int64_t(C.n_rows) * 512 <= C.cols * groups || far)
         return launch_grouped_stream16(C, st);
     const int64_t tiles256 = (C.n_rows / 256) * int64_t((C.rows + 255) / 256);
     const bool big =

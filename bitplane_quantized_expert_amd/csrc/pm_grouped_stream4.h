@@ -10,16 +10,9 @@ namespace {
 
 template <bool X32, int NW, int KB, bool ZEROS>
 hipError_t run4_group(const GroupedCall& C, const StreamPlan& P, hipStream_t st) {
-    // groups are read as aligned vectors of up to 4 scales
-    auto vector_ok = [&](int group) {
-        const int n = std::min(4, KB * 128 / group);
-        return C.group == group && (C.cols / group) % n == 0 &&
-               reinterpret_cast<uintptr_t>(C.scales) % (2 * n) == 0 &&
-               reinterpret_cast<uintptr_t>(C.zeros) % n == 0;
-    };
-    if (vector_ok(128)) return run_stream<kW4, false, X32, NW, KB, kGroup128, ZEROS>(C, P, st);
-    if (vector_ok(64)) return run_stream<kW4, false, X32, NW, KB, kGroup64, ZEROS>(C, P, st);
-    if (vector_ok(32)) return run_stream<kW4, false, X32, NW, KB, kGroup32, ZEROS>(C, P, st);
+    if (reads_scales_by(C, 128, KB)) return run_stream<kW4, false, X32, NW, KB, kGroup128, ZEROS>(C, P, st);
+    if (reads_scales_by(C, 64, KB)) return run_stream<kW4, false, X32, NW, KB, kGroup64, ZEROS>(C, P, st);
+    if (reads_scales_by(C, 32, KB)) return run_stream<kW4, false, X32, NW, KB, kGroup32, ZEROS>(C, P, st);
     return run_stream<kW4, false, X32, NW, KB, kAnyGroup, ZEROS>(C, P, st);
 }
 

@@ -1,0 +1,420 @@
+// Products grouped by expert with 4-bit weights for groups of many rows: tiles
+// of 128 rows of 16-bit activations by 256 weight rows.
+//
+//   D[m][o] = sum_g scale[o][g] sum_{k in g} x[m][k] (q - z)[o][k]
+//
+// (v_mfma_f32_16x16x32; q - z is exact in fp16 and bf16, sums are fp32.)
+// Streamed past 16 columns at a time, the weights are decoded once per 16 rows
+// of x, which bounds groups of more than some 64 rows; here once per 128.
+//
+// 8 waves, each with 32 weight rows and all 128 rows of x.  The codes go from
+// memory to registers, 16 bytes per lane and 128 inputs (as in the streamed
+// kernel), two blocks of 128 inputs ahead, and are decoded to matrix operands
+// there: no wave needs another's.  x goes straight to LDS, three blocks of 128
+// inputs x 128 rows (32 KiB), two ahead; one barrier per block.  A wave reads
+// 16 rows of a block at a time, the next 16 while these are multiplied.
+//
+// Bound by LDS: every 1 KiB read of x feeds two products.  A wave of 64 x 64
+// would halve that, but decode every code twice.
+//
+// LDS holds rows of 128 inputs (256 bytes = 16 pieces); piece c of row r lies
+// at place c ^ (r % 16), so that the 16-byte reads of 16 rows fall in distinct
+// banks.  Rows past the group and inputs past `cols` read as zero.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+
+#include "pm_convert.h"
+#include "pm_device.h"
+#include "pm_grouped_codes.h"
+#include "pm_grouped_rows.h"
+#include "pm_routed.h"
+
+namespace pm {
+
+namespace {
+
+constexpr int kRows = 128, kOuts = 256, kBlockK = 128, kStages = 3;
+constexpr int kStageBytes = kRows * kBlockK * 2;
+constexpr int kThreads4 = 512;
+constexpr uint32_t kOutside = 0xFFFFFFF0u;      // an offset beyond any buffer
+
+typedef __attribute__((address_space(3))) void lds_void;
+
+// The 8 codes of word w minus the zero point, as 16-bit operands in order.
+template <bool BF16>
+__device__ inline u32x4 codes_in_order(const CodeBits& k, uint32_t w, f16x2 za, f16x2 zb) {
+    const u32x4 c = codes_to_f16(k, w, za, zb);          // 0 4 | 1 5 | 2 6 | 3 7
+    if constexpr (!BF16) {
+        return u32x4{__builtin_amdgcn_perm(c[1], c[0], 0x05040100u),
+                     __builtin_amdgcn_perm(c[3], c[2], 0x05040100u),
+                     __builtin_amdgcn_perm(c[1], c[0], 0x07060302u),
+                     __builtin_amdgcn_perm(c[3], c[2], 0x07060302u)};
+    } else {
+        // (integers of 8 bits: the upper half of the fp32 value is exact)
+        uint32_t lo[4], hi[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t pair = c[i];                  // (a bit_cast of c[i] takes c[0])
+            const f16x2 h = __builtin_bit_cast(f16x2, pair);
+            lo[i] = __float_as_uint(float(h[0]));
+            hi[i] = __float_as_uint(float(h[1]));
+        }
+        return u32x4{__builtin_amdgcn_perm(lo[1], lo[0], 0x07060302u),
+                     __builtin_amdgcn_perm(lo[3], lo[2], 0x07060302u),
+                     __builtin_amdgcn_perm(hi[1], hi[0], 0x07060302u),
+                     __builtin_amdgcn_perm(hi[3], hi[2], 0x07060302u)};
+    }
+}
+
+template <bool BF16, int GM, bool ZEROS>
+__global__ __launch_bounds__(kThreads4, 2) void tile4_kernel(const GroupedCall C, int nt) {
+#ifdef __HIP_DEVICE_COMPILE__
+    constexpr bool kWhole = GM == kGroup128;
+    // products between two scales, scales of a block
+    constexpr int kPer = kWhole ? 4 : GM == kGroup64 ? 2 : 1, kUnits = 4 / kPer;
+    constexpr int kScaleLoads = GM == kAnyGroup ? 4 : 1;
+    constexpr int LX = 4, LW = 2 * (1 + kScaleLoads * (ZEROS ? 2 : 1));   // loads per block
+    extern __shared__ __attribute__((aligned(1024))) char smem[];
+    int* const ymap = reinterpret_cast<int*>(smem + kStages * kStageBytes);   // [2][kRows]
+    int* const before = ymap + 2 * kRows;                                     // [E + 1]
+    const int lane = threadIdx.x & 63, wv = uni(threadIdx.x >> 6);
+    const int i16 = lane & 15, q = lane >> 4;
+    const bool glu = C.flags & PM_GROUPED_SWIGLU, gather = C.flags & PM_GROUPED_GATHER;
+    const int out = glu ? C.rows / 2 : C.rows;
+    const int n_tiles = tile_table(C, kRows, before) * nt;
+    __syncthreads();
+
+    // place of this workgroup in a round of tiles: the 32 of one XCD are
+    // consecutive, so that they share weight rows and x rows in its L2
+    const int per_xcd = gridDim.x >> 3;
+    const int place = gridDim.x & 7 ? blockIdx.x : (blockIdx.x & 7) * per_xcd + (blockIdx.x >> 3);
+    struct Where {
+        int e, row0, n, o0;                       // expert, rows, first output; n 0: no tile
+    };
+    auto locate = [&](int i) {
+        Where w{0, 0, 0, 0};
+        if (i < n_tiles) {
+            const int mt = i / nt;
+            const int e = tile_expert(C, before, mt);
+            const RowRange g = group_rows(C, e);
+            const int64_t skip = int64_t(mt - before[e]) * kRows;
+            const bool ok = skip >= 0 && skip < g.n;      // (not so only for bad offsets)
+            w.e = uni(e);
+            w.row0 = uni(ok ? g.row0 + int(skip) : 0);
+            w.n = uni(ok ? min(g.n - int(skip), kRows) : 0);
+            w.o0 = uni((i - mt * nt) * (glu ? kOuts / 2 : kOuts));
+        }
+        return w;
+    };
+
+    // ---- x: this lane's rows of a block, 4 loads of 4 rows per wave
+    const int xrow = wv * 4 + q, piece = i16 ^ (xrow & 15);
+    auto use_rows = [&](const Where& w, int* u) {
+#pragma unroll
+        for (int i = 0; i < LX; ++i)
+            u[i] = i * 32 + xrow < w.n ? use_of(C, w.row0 + i * 32 + xrow) : -1;
+    };
+    uint32_t pa[LX];
+    auto set_rows = [&](const Where& w, const int* u, int parity) {
+#pragma unroll
+        for (int i = 0; i < LX; ++i) {
+            const int r = i * 32 + xrow;
+            const uint32_t xr = gather ? uint32_t(u[i]) / uint32_t(C.top_k) : uint32_t(r);
+            pa[i] = u[i] >= 0 ? uint32_t(xr * uint64_t(C.ldx) * 2) + piece * 16 : kOutside;
+            if (i16 == 0)
+                ymap[parity * kRows + r] =
+                    u[i] < 0 ? -1 : (C.flags & PM_GROUPED_SCATTER ? u[i] : w.row0 + r);
+        }
+    };
+    auto x_buffer = [&](const Where& w) {
+        const char* p = static_cast<const char*>(C.x) + (gather ? 0 : size_t(w.row0) * C.ldx * 2);
+        const size_t n = w.n == 0 ? 0
+                                  : (size_t(gather ? (C.n_rows - 1) / C.top_k : w.n - 1) * C.ldx +
+                                     C.cols) * 2;
+        return __builtin_amdgcn_make_buffer_rsrc(
+            uni_ptr(const_cast<char*>(p)), 0, uni(int(uint32_t(min(n, size_t(kOutside))))),
+            kRawBuffer);
+    };
+
+    // ---- weights: this lane's two rows (gate and up under SWIGLU)
+    const uint32_t row_bytes = uint32_t(C.cols) / 2;
+    const size_t w_bytes = size_t(C.rows) * row_bytes;
+    const int ng = C.cols / C.group;
+    int wrow[2];
+    auto set_weights = [&](const Where& w) {
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            const int o = w.o0 + (glu ? wv * 16 : wv * 32 + b * 16) + i16;
+            wrow[b] = w.n > 0 && o < out ? (glu && b ? out + o : o) : -1;
+        }
+    };
+    auto w_buffer = [&](const Where& w) {
+        return __builtin_amdgcn_make_buffer_rsrc(
+            uni_ptr(const_cast<char*>(static_cast<const char*>(C.w)) + size_t(w.e) * w_bytes), 0,
+            uni(int(uint32_t(w_bytes))), kRawBuffer);
+    };
+    auto s_buffer = [&](const Where& w) {
+        return __builtin_amdgcn_make_buffer_rsrc(
+            uni_ptr(const_cast<uint16_t*>(C.scales) + size_t(w.e) * C.rows * ng), 0,
+            uni(int(uint32_t(C.rows) * uint32_t(ng) * 2)), kRawBuffer);
+    };
+    auto z_buffer = [&](const Where& w) {
+        return __builtin_amdgcn_make_buffer_rsrc(
+            uni_ptr(const_cast<uint8_t*>(C.zeros) + size_t(w.e) * C.rows * ng), 0,
+            uni(int(uint32_t(C.rows) * uint32_t(ng))), kRawBuffer);
+    };
+
+    // (blocks past the last input hold zeros; a tile has an even number)
+    const int T = max(2, ((C.cols + kBlockK - 1) / kBlockK + 1) & ~1);
+    int u[LX];
+    Where cur = locate(place), nxt;
+    if (cur.n == 0) return;
+    use_rows(cur, u);
+    set_rows(cur, u, 0);
+    set_weights(cur);
+    auto xb = x_buffer(cur);
+    auto wb = w_buffer(cur), sb = s_buffer(cur), zb = z_buffer(cur);
+    int kx = 0, kw = 0;
+    auto issue_x = [&](int stage) {
+        char* base = smem + stage * kStageBytes + wv * 1024;
+        const bool in = kx * kBlockK + piece * 8 < C.cols;
+#pragma unroll
+        for (int i = 0; i < LX; ++i)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(xb, (lds_void*)(base + i * 8192), 16,
+                                                     in ? pa[i] : kOutside, kx * kBlockK * 2, 0, 0);
+        ++kx;
+    };
+    u32x4 w[2][2];
+    uint32_t sc[2][2][2], zp[2][2];               // [slot][weight row]
+    auto issue_w = [&](auto slot) {
+        constexpr int S = decltype(slot)::value;
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            const bool some = wrow[b] >= 0 && kw * kBlockK < C.cols;
+            const uint32_t at = chosen(some, uint32_t(wrow[b]) * row_bytes + kw * 64 + q * 16);
+            w[S][b] = __builtin_bit_cast(u32x4,
+                                         __builtin_amdgcn_raw_buffer_load_b128(wb, at, 0, 0));
+            if constexpr (GM == kAnyGroup) {
+                uint32_t z = 0;
+#pragma unroll
+                for (int s = 0; s < 4; ++s) {
+                    const int c = kw * kBlockK + s * 32;
+                    const uint32_t g = uint32_t(wrow[b]) * ng + c / C.group;
+                    const bool in = wrow[b] >= 0 && c < C.cols;
+                    const uint32_t v =
+                        uint16_t(__builtin_amdgcn_raw_buffer_load_b16(sb, chosen(in, g * 2), 0, 0));
+                    sc[S][b][s / 2] = s & 1 ? sc[S][b][s / 2] | v << 16 : v;
+                    if constexpr (ZEROS)
+                        z |= uint32_t(uint8_t(__builtin_amdgcn_raw_buffer_load_b8(
+                                 zb, chosen(in, g), 0, 0))) << (8 * s);
+                }
+                if constexpr (ZEROS) zp[S][b] = z;
+            } else {
+                const uint32_t g = uint32_t(wrow[b]) * ng + uint32_t(kw) * kUnits;
+                const uint32_t so = chosen(some, g * 2), zo = chosen(some, g);
+                if constexpr (kUnits == 1) {
+                    sc[S][b][0] = uint16_t(__builtin_amdgcn_raw_buffer_load_b16(sb, so, 0, 0));
+                    if constexpr (ZEROS)
+                        zp[S][b] = uint8_t(__builtin_amdgcn_raw_buffer_load_b8(zb, zo, 0, 0));
+                } else if constexpr (kUnits == 2) {
+                    sc[S][b][0] = __builtin_amdgcn_raw_buffer_load_b32(sb, so, 0, 0);
+                    if constexpr (ZEROS)
+                        zp[S][b] = uint16_t(__builtin_amdgcn_raw_buffer_load_b16(zb, zo, 0, 0));
+                } else {
+                    const u32x2 v = __builtin_bit_cast(
+                        u32x2, __builtin_amdgcn_raw_buffer_load_b64(sb, so, 0, 0));
+                    sc[S][b][0] = v[0];
+                    sc[S][b][1] = v[1];
+                    if constexpr (ZEROS) zp[S][b] = __builtin_amdgcn_raw_buffer_load_b32(zb, zo, 0, 0);
+                }
+            }
+        }
+        ++kw;
+    };
+    const CodeBits bits = code_bits();
+    issue_x(0);
+    __builtin_amdgcn_sched_barrier(0);
+    issue_w(std::integral_constant<int, 0>{});
+    __builtin_amdgcn_sched_barrier(0);
+    issue_x(1);
+    __builtin_amdgcn_sched_barrier(0);
+    issue_w(std::integral_constant<int, 1>{});
+
+    // place in a row of x of this lane's 8 inputs of each product
+    int place_of[4];
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+        place_of[s] = i16 * 256 + (((kWhole ? q * 4 + s : s * 4 + q) ^ i16) * 16);
+    f32x4 acc[kRows / 16][2];
+    int xs = 0, parity = 0, arrived = 0;
+    auto step = [&](auto slot, int t) {
+        constexpr int S = decltype(slot)::value;
+        __builtin_amdgcn_sched_barrier(0);
+        // this block of x has arrived, and every wave is done with the last.
+        // (Loads and stores complete in order: the two blocks that were under
+        // way at a tile's end were waited for before its stores.)
+        if (arrived > 0) {
+            asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+            --arrived;
+        } else {
+            asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(2 * LW + LX)
+                         : "memory");
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        const bool last = S == 0 && t == T - 2;
+        if (last) {
+            set_rows(nxt, u, parity ^ 1);
+            xb = x_buffer(nxt);
+            kx = 0;
+        }
+        issue_x(xs == 0 ? 2 : xs - 1);
+        __builtin_amdgcn_sched_barrier(0);
+        u32x4 wf[2][4];
+        float sf[2][kUnits];
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            const u32x4 c = kWhole ? w[S][b] : exchange(w[S][b]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                f16x2 za = {_Float16(1032.0f), _Float16(1032.0f)};
+                f16x2 zc = {_Float16(72.0f), _Float16(72.0f)};
+                if constexpr (ZEROS) {
+                    const uint32_t z = zp[S][b] >> (8 * (j / kPer)) & 255u;
+                    za = __builtin_bit_cast(f16x2, 0x64006400u | z | z << 16);
+                    zc = za - f16x2{_Float16(960.0f), _Float16(960.0f)};
+                }
+                wf[b][j] = codes_in_order<BF16>(bits, c[j], za, zc);
+            }
+#pragma unroll
+            for (int k = 0; k < kUnits; ++k)
+                sf[b][k] = half_bits(sc[S][b][k / 2] >> (16 * (k & 1)));
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        if (last) {
+            set_weights(nxt);
+            wb = w_buffer(nxt);
+            sb = s_buffer(nxt);
+            zb = z_buffer(nxt);
+            kw = 0;
+        }
+        issue_w(slot);
+        __builtin_amdgcn_sched_barrier(0);
+
+        const char* xt = smem + xs * kStageBytes;
+        u32x4 fa[2][4];
+        auto read = [&](int m) {
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+                fa[m & 1][s] = *reinterpret_cast<const u32x4*>(xt + m * 16 * 256 + place_of[s]);
+        };
+        read(0);
+#pragma unroll
+        for (int m = 0; m < kRows / 16; ++m) {
+            if (m * 16 >= cur.n) break;
+            if (m + 1 < kRows / 16) read(m + 1);
+            // a unit's sums meet their scale after the next unit's first products
+            f32x4 d[2][2];
+            auto scale = [&](int k) {
+#pragma unroll
+                for (int b = 0; b < 2; ++b)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        acc[m][b][r] = fmaf(d[k & 1][b][r], sf[b][k], acc[m][b][r]);
+            };
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                const int k = s / kPer;
+#pragma unroll
+                for (int b = 0; b < 2; ++b)
+                    d[k & 1][b] =
+                        mfma_x_w<BF16>(fa[m & 1][s], wf[b][s],
+                                       s % kPer == 0 ? f32x4{0.f, 0.f, 0.f, 0.f} : d[k & 1][b]);
+                if (s > 0 && s % kPer == 0) scale(k - 1);
+            }
+            scale(kUnits - 1);
+            // here, not where the sums are needed: the products' registers are
+            // free then
+            asm volatile("" : "+v"(acc[m][0]), "+v"(acc[m][1]));
+        }
+        xs = xs == 2 ? 0 : xs + 1;
+    };
+
+    auto store = [&](int64_t at, float v) {
+        if (C.y_type == PM_F32) store_f32<PM_F32>(C.y, at, v);
+        else store_f32<BF16 ? PM_BF16 : PM_F16>(C.y, at, v);
+    };
+    for (int tile = place; cur.n > 0; tile += gridDim.x) {
+        // the next tile's place and uses, long before its first loads
+        nxt = locate(tile + gridDim.x);
+        use_rows(nxt, u);
+#pragma unroll
+        for (int m = 0; m < kRows / 16; ++m)
+#pragma unroll
+            for (int b = 0; b < 2; ++b) acc[m][b] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int t = 0; t < T; t += 2) {
+            step(std::integral_constant<int, 0>{}, t);
+            step(std::integral_constant<int, 1>{}, t + 1);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(LW) : "memory");
+        arrived = 2;
+        const int* rows = ymap + parity * kRows + 4 * q;
+#pragma unroll
+        for (int m = 0; m < kRows / 16; ++m) {
+            if (m * 16 >= cur.n) break;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int yr = rows[m * 16 + r];
+                if (yr < 0) continue;
+                const int64_t at = int64_t(yr) * C.ldy;
+                if (glu) {
+                    const int o = cur.o0 + wv * 16 + i16;
+                    if (o < out) store(at + o, silu_up(acc[m][0][r], acc[m][1][r]));
+                } else {
+                    const int o = cur.o0 + wv * 32 + i16;
+                    if (o < out) store(at + o, acc[m][0][r]);
+                    if (o + 16 < out) store(at + o + 16, acc[m][1][r]);
+                }
+            }
+        }
+        cur = nxt;
+        parity ^= 1;
+    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // the last blocks' loads
+#endif
+}
+
+template <bool BF16, int GM, bool ZEROS>
+hipError_t run_tiles4(const GroupedCall& C, hipStream_t st) {
+    const int out = C.flags & PM_GROUPED_SWIGLU ? C.rows / 2 : C.rows;
+    const int per = C.flags & PM_GROUPED_SWIGLU ? kOuts / 2 : kOuts;
+    const int nt = (out + per - 1) / per;
+    const size_t lds =
+        size_t(kStages) * kStageBytes + (2 * kRows + C.n_experts + 1) * sizeof(int);
+    auto* f = tile4_kernel<BF16, GM, ZEROS>;
+    hipError_t e = allow_lds(reinterpret_cast<const void*>(f), kTileMaxLds);
+    if (e != hipSuccess) return e;
+    const int64_t tiles = (int64_t(std::min(C.n_rows, C.n_experts)) + C.n_rows / kRows) * nt;
+    const unsigned grid = unsigned(std::min<int64_t>(tiles, compute_units()));
+    hipLaunchKernelGGL(f, dim3(grid), dim3(kThreads4), lds, st, C, nt);
+    return hipGetLastError();
+}
+
+template <bool BF16, bool ZEROS>
+hipError_t run_tiles4_group(const GroupedCall& C, hipStream_t st) {
+    if (reads_scales_by(C, 128, 1)) return run_tiles4<BF16, kGroup128, ZEROS>(C, st);
+    if (reads_scales_by(C, 64, 1)) return run_tiles4<BF16, kGroup64, ZEROS>(C, st);
+    if (reads_scales_by(C, 32, 1)) return run_tiles4<BF16, kGroup32, ZEROS>(C, st);
+    return run_tiles4<BF16, kAnyGroup, ZEROS>(C, st);
+}
+
+}  // namespace
+
+hipError_t launch_grouped_tiles4(const GroupedCall& C, hipStream_t st) {
+    if (C.x_type == PM_BF16)
+        return C.zeros ? run_tiles4_group<true, true>(C, st) : run_tiles4_group<true, false>(C, st);
+    return C.zeros ? run_tiles4_group<false, true>(C, st) : run_tiles4_group<false, false>(C, st);
+}
+
+}  // namespace pm

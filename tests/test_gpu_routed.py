@@ -444,6 +444,62 @@ def test_w4_many_inputs(group, C):
     run_w4([9, 2], 40, C, group, False, "f16", "f16", 2, GATHER | SWIGLU, seed=7)
 
 
+@pytest.mark.parametrize("ty,y_ty", [("f16", "f16"), ("bf16", "f32"), ("bf16", "bf16")])
+@pytest.mark.parametrize("flags,top_k", LAYOUTS)
+def test_w4_many_rows_layouts(ty, y_ty, flags, top_k):
+    report(f"w4 tiles {ty}->{y_ty} flags {flags}")
+    counts = [130, 0, 70, 257, 1, 128]
+    run_w4(counts, 96, 256, 64, bool(flags & SCATTER), ty, y_ty, top_k, flags, seed=1)
+    run_w4(counts, 562, 640, 128, not flags & SCATTER, ty, y_ty, top_k, flags, seed=2, n_rows=600)
+
+
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("group,C", [(128, 128), (128, 4224), (64, 384), (32, 256), (32, 32),
+                                     (96, 288), (64, 192), (256, 1024), (160, 800)])
+def test_w4_many_rows_groups(group, C, zeros):
+    report(f"w4 tiles group {group} cols {C} zeros {zeros}")
+    run_w4([60, 48, 100], 258, C, group, zeros, "f16", "f32", 2, GATHER, seed=3)
+    run_w4([200, 16, 129], 130, C, group, zeros, "bf16", "bf16", 1, SCATTER | SWIGLU, seed=4)
+
+
+def test_w4_many_rows_rounds_and_bad_entries():
+    """Several rounds of tiles; rows and order entries left out; a wide x; no
+    order; infinities beside other rows."""
+    report("w4 tiles: rounds, entries out of range, strides")
+    run_w4([1500, 3, 0, 900, 128, 64], 4100, 256, 128, True, "bf16", "bf16", 3, GATHER, seed=5)
+    run_w4([1500, 3, 0, 900, 128, 64], 4096, 128, 32, False, "f16", "f16", 1, SWIGLU, seed=6,
+           pad=2, order=False)
+    off, order = rc.groups([300, 200, 100], 1)
+    order[2], order[7], order[411] = -1, 600, 2 ** 31 - 1
+    q, sc, z = make_w4(3, 72, 320, 64, True, 1)
+    x = torch.randn(600, 320, generator=rc.gen(2), device="cuda").half()
+    for flags in (SCATTER, 0, GATHER):
+        y = torch.full((600, 72), 3.0, device="cuda")
+        pm.pm_grouped_gemm_w4(q, sc, z, 64, x, y, off, order, 1, flags)
+        want = rc.grouped_plain(lambda e: rc.decode_w4(q[e], sc[e], z[e], 64), x, off, order, 600,
+                                1, bool(flags & GATHER), bool(flags & SCATTER), False)
+        rc.check_grouped(y, 3.0, want, f"flags {flags}")
+    off, _ = rc.groups([300, 200, 100], 1)
+    clean = torch.empty(600, 72, device="cuda")
+    pm.pm_grouped_gemm_w4(q, sc, z, 64, x, clean, off, None, 1, 0)
+    bad = x.clone()
+    bad[5], bad[299, 3], bad[450, 319] = float("nan"), float("inf"), -float("inf")
+    y = torch.empty(600, 72, device="cuda")
+    pm.pm_grouped_gemm_w4(q, sc, z, 64, bad, y, off, None, 1, 0)
+    keep = torch.ones(600, dtype=torch.bool, device="cuda")
+    keep[[5, 299, 450]] = False
+    assert torch.equal(y[keep], clean[keep])
+    assert not torch.isfinite(y[5]).any()
+    # offsets that decrease or pass the rows: every access stays in bounds
+    for o in ([0, 400, 100, 600], [-5, 300, 9999, 600], [600, 0, 0, 0]):
+        pm.pm_grouped_gemm_w4(q, sc, z, 64, x, y, torch.tensor(o, dtype=torch.int32, device="cuda"),
+                              order, 1, SCATTER)
+    torch.cuda.synchronize()
+    y.zero_()
+    pm.pm_grouped_gemm_w4(q, sc, z, 64, x, y, off, None, 1, 0)
+    assert torch.equal(y, clean)
+
+
 def test_w4_many_rows_and_experts():
     report("w4: 512 experts, ragged")
     counts = np.random.default_rng(1).integers(0, 4, 512)
