@@ -5,23 +5,36 @@
 
 namespace pm {
 
-// 4-bit weights are always streamed.  16-bit weights are streamed while a group
-// has few rows: measured on 128 experts, us of the streamed kernel against
-// 128-row tiles at 4, 8, 12 rows per group: 329/377, 406/413, 451/419 with 4096
-// inputs (2048 outputs); 16 experts, 2048 inputs, 1536 outputs: 28/34, 29/34,
-// 33/34; with 1024 inputs (4096 outputs) 160/148 already at 2 rows.  Tiles of
-// 256 rows instead of 128 from 224 rows per group on, where there are two for
-// each compute unit: 353/359 us at 192 rows, 438/427 at 256, 760/726 at 512 (128
-// experts, 1024 inputs, 4096 outputs), or where 128-row tiles' three stages leave
-// no room in LDS for the table of experts (above some 3500).  The groups' sizes are on the device;
-// these are rows per group if every expert had some.
+// 16-bit weights are streamed while a group has few rows: measured on 128
+// experts, us of the streamed kernel against 128-row tiles at 4, 8, 12 rows per
+// group: 329/377, 406/413, 451/419 with 4096 inputs (2048 outputs); 16 experts,
+// 2048 inputs, 1536 outputs: 28/34, 29/34, 33/34; with 1024 inputs (4096
+// outputs) 160/148 already at 2 rows.  Tiles of 256 rows instead of 128 from 224
+// rows per group on, where there are two for each compute unit: 353/359 us at
+// 192 rows, 438/427 at 256, 760/726 at 512 (128 experts, 1024 inputs, 4096
+// outputs), or where 128-row tiles' three stages leave no room in LDS for the
+// table of experts (above some 3500).  The groups' sizes are on the device; these
+// are rows per group if every expert had some.
+//
+// 4-bit weights with fp32 activations are always streamed.  With 16-bit
+// activations tiles decode them less often from 20 rows per group on: us of the
+// streamed kernel against tiles at 12, 20, 32 rows: 195/254, 300/274, 404/303
+// (512 experts, 512 inputs, 4096 outputs); 92/128, 132/130, 176/134 (128 experts,
+// 2048 x 2048); 68/72, 85/73, 106/75 (32 experts, 4096 inputs, 2048 outputs); 302/527,
+// 464/550, 640/551 (256 of these).  And where every workgroup has at most 4 blocks
+// of 128 inputs to do, tiles start sooner: 20/16 us at one row (128 experts, 256
+// inputs, 1024 outputs), 18/12 (16 experts, 512 inputs, 1024 outputs); with 8
+// blocks (1024 inputs) 17/18.
 hipError_t launch_grouped(const GroupedCall& C, int kind, hipStream_t st) {
     const int64_t groups = std::min(C.n_experts, C.n_rows);
     const int64_t x_rows = C.flags & PM_GROUPED_GATHER ? (C.n_rows - 1) / C.top_k + 1 : 256;
     const bool far = (x_rows * C.ldx + C.cols) * 2 >= 0xFFFFFFF0ll;
     if (kind == kW4) {
         if (C.x_type == PM_F32) return launch_grouped_stream4f(C, st);
-        if (C.n_rows < 48 * groups || far) return launch_grouped_stream4(C, st);
+        const int64_t blocks = (C.cols + 127) / 128, cus = compute_units();
+        const int64_t rounds = (groups * ((C.rows + 255) / 256) + cus - 1) / cus;
+        if (far || (C.n_rows < 20 * groups && blocks * rounds > 4))
+            return launch_grouped_stream4(C, st);
         return launch_grouped_tiles4(C, st);
     }
     if (int64_t(C.n_rows) * 512 <= C.cols * groups || far)

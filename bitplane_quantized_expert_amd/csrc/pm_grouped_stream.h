@@ -42,9 +42,9 @@
 // experts, 4096 x 1024 with zero points, bf16: 163 to 170 us, 4.9 TB/s; 10 rows
 // of fp32, 2048 x 4096 with gate and up: 20 us for 43 MB, of which the stream
 // takes 9 and finding the groups, converting x and the last sums the rest.
-// Above some 64 rows per expert the decoding, repeated for every 16 columns,
-// bounds the 4-bit kernel: 64 experts of 4096 x 4096 with 32, 64, 128 bf16 rows
-// each take 261, 500, 997 us.
+// The decoding, repeated for every 16 columns, bounds 4-bit calls of more rows:
+// 64 experts of 4096 x 4096 with 32, 64, 128 bf16 rows each take 261, 500, 997
+// us here, which is why tiles take 16-bit activations from some 20 rows on.
 #pragma once
 
 #include <hip/hip_runtime.h>

@@ -444,6 +444,21 @@ def test_w4_many_inputs(group, C):
     run_w4([9, 2], 40, C, group, False, "f16", "f16", 2, GATHER | SWIGLU, seed=7)
 
 
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("E,group,C", [(65, 32, 128), (65, 64, 128), (65, 128, 128), (65, 96, 96),
+                                       (33, 32, 256), (33, 64, 256), (33, 128, 256), (33, 96, 192),
+                                       (33, 128, 384), (33, 32, 512), (33, 64, 512), (33, 96, 480),
+                                       (4, 32, 1024), (4, 128, 1280), (4, 96, 1152)])
+def test_w4_few_rows_16_bit(E, group, C, zeros):
+    """Few rows of 16-bit activations, with many experts where the inputs are
+    few."""
+    report(f"w4 few rows {E} experts group {group} cols {C} zeros {zeros}")
+    counts = np.random.default_rng(E + C).integers(0, 4, E)
+    counts[[0, E // 2, E - 1]] = [17, 5, 1]
+    run_w4(counts.tolist(), 4096, C, group, zeros, "f16", "f32", 1, SCATTER, seed=8)
+    run_w4(counts.tolist(), 4094, C, group, zeros, "bf16", "bf16", 2, GATHER | SWIGLU, seed=9)
+
+
 @pytest.mark.parametrize("ty,y_ty", [("f16", "f16"), ("bf16", "f32"), ("bf16", "bf16")])
 @pytest.mark.parametrize("flags,top_k", LAYOUTS)
 def test_w4_many_rows_layouts(ty, y_ty, flags, top_k):
