@@ -1,5 +1,5 @@
 // Products grouped by expert with 4-bit weights for groups of many rows: tiles
-// of 128 rows of 16-bit activations by 256 weight rows.
+// of 128 rows of 16-bit activations, or 64 of fp32, by 256 weight rows.
 //
 //   D[m][o] = sum_g scale[o][g] sum_{k in g} x[m][k] (q - z)[o][k]
 //
@@ -14,10 +14,16 @@
 // inputs x 128 rows (32 KiB), two ahead; one barrier per block.  A wave reads
 // 16 rows of a block at a time, the next 16 while these are multiplied.
 //
+// An fp32 row takes two of the 128: its values times a power of two per row and
+// block, rounded to fp16, and the rest (times 2^11) rounded again: off by 2^-23
+// of the value, or 2^-50 of the largest.  Every lane holds 16 inputs of a row,
+// loaded a block ahead, and converts them while the last block is multiplied.
+//
 // Bound by LDS: every 1 KiB read of x feeds two products.  A wave of 64 x 64
 // would halve that, but decode every code twice.  Measured: 64 experts of 4096 x
 // 4096 with 128 bf16 rows each 339 us (811 TFLOP/s; the streamed kernel 997), with
-// 64 rows 244 us (500); 8 experts with 256 rows 93 us (223).
+// 64 rows 244 us (500); 8 experts with 256 rows 93 us (223).  With fp32: 809 us (1930), 411 (968), 244 (416): the conversion and the
+// products of a wave follow each other.
 //
 // LDS holds rows of 128 inputs (256 bytes = 16 pieces); piece c of row r lies
 // at place c ^ (r % 16), so that the 16-byte reads of 16 rows fall in distinct
@@ -36,9 +42,12 @@ namespace pm {
 
 namespace {
 
-constexpr int kRows = 128, kOuts = 256, kBlockK = 128, kStages = 3;
-constexpr int kStageBytes = kRows * kBlockK * 2;
+constexpr int kOuts = 256, kBlockK = 128;
+constexpr int kStageBytes = 128 * kBlockK * 2;
 constexpr int kThreads4 = 512;
+// Rows of x per tile, blocks held in LDS.
+constexpr int tile4_rows(bool x32) { return x32 ? 64 : 128; }
+constexpr int tile4_stages(bool x32) { return x32 ? 2 : 3; }
 constexpr uint32_t kOutside = 0xFFFFFFF0u;      // an offset beyond any buffer
 
 typedef __attribute__((address_space(3))) void lds_void;
@@ -69,17 +78,20 @@ __device__ inline u32x4 codes_in_order(const CodeBits& k, uint32_t w, f16x2 za, 
     }
 }
 
-template <bool BF16, int GM, bool ZEROS>
+template <bool BF16, bool X32, int GM, bool ZEROS>
 __global__ __launch_bounds__(kThreads4, 2) void tile4_kernel(const GroupedCall C, int nt) {
 #ifdef __HIP_DEVICE_COMPILE__
+    constexpr int kRows = tile4_rows(X32), kStages = tile4_stages(X32), XB = X32 ? 4 : 2;
     constexpr bool kWhole = GM == kGroup128;
     // products between two scales, scales of a block
     constexpr int kPer = kWhole ? 4 : GM == kGroup64 ? 2 : 1, kUnits = 4 / kPer;
     constexpr int kScaleLoads = GM == kAnyGroup ? 4 : 1;
-    constexpr int LX = 4, LW = 2 * (1 + kScaleLoads * (ZEROS ? 2 : 1));   // loads per block
+    constexpr int LX = 4, XR = X32 ? 1 : 4;       // a lane's loads of x, rows of them
+    constexpr int LW = 2 * (1 + kScaleLoads * (ZEROS ? 2 : 1));   // loads per block
     extern __shared__ __attribute__((aligned(1024))) char smem[];
     int* const ymap = reinterpret_cast<int*>(smem + kStages * kStageBytes);   // [2][kRows]
     int* const before = ymap + 2 * kRows;                                     // [E + 1]
+    __shared__ __attribute__((aligned(16))) float xscale[2][X32 ? kRows : 4];
     const int lane = threadIdx.x & 63, wv = uni(threadIdx.x >> 6);
     const int i16 = lane & 15, q = lane >> 4;
     const bool glu = C.flags & PM_GROUPED_SWIGLU, gather = C.flags & PM_GROUPED_GATHER;
@@ -110,30 +122,33 @@ __global__ __launch_bounds__(kThreads4, 2) void tile4_kernel(const GroupedCall C
         return w;
     };
 
-    // ---- x: this lane's rows of a block, 4 loads of 4 rows per wave
-    const int xrow = wv * 4 + q, piece = i16 ^ (xrow & 15);
+    // ---- x: this lane's rows of a block, 4 loads of 4 rows per wave (fp32: of
+    // one row, 8 lanes each)
+    const int xrow = X32 ? int(threadIdx.x >> 3) : wv * 4 + q, piece = i16 ^ (xrow & 15);
     auto use_rows = [&](const Where& w, int* u) {
 #pragma unroll
-        for (int i = 0; i < LX; ++i)
+        for (int i = 0; i < XR; ++i)
             u[i] = i * 32 + xrow < w.n ? use_of(C, w.row0 + i * 32 + xrow) : -1;
     };
-    uint32_t pa[LX];
+    uint32_t pa[XR];
     auto set_rows = [&](const Where& w, const int* u, int parity) {
 #pragma unroll
-        for (int i = 0; i < LX; ++i) {
+        for (int i = 0; i < XR; ++i) {
             const int r = i * 32 + xrow;
             const uint32_t xr = gather ? uint32_t(u[i]) / uint32_t(C.top_k) : uint32_t(r);
-            pa[i] = u[i] >= 0 ? uint32_t(xr * uint64_t(C.ldx) * 2) + piece * 16 : kOutside;
-            if (i16 == 0)
+            pa[i] = u[i] >= 0 ? uint32_t(xr * uint64_t(C.ldx) * XB) +
+                                    (X32 ? (lane & 7) * 16 : piece * 16)
+                              : kOutside;
+            if ((lane & (X32 ? 7 : 15)) == 0)
                 ymap[parity * kRows + r] =
                     u[i] < 0 ? -1 : (C.flags & PM_GROUPED_SCATTER ? u[i] : w.row0 + r);
         }
     };
     auto x_buffer = [&](const Where& w) {
-        const char* p = static_cast<const char*>(C.x) + (gather ? 0 : size_t(w.row0) * C.ldx * 2);
+        const char* p = static_cast<const char*>(C.x) + (gather ? 0 : size_t(w.row0) * C.ldx * XB);
         const size_t n = w.n == 0 ? 0
                                   : (size_t(gather ? (C.n_rows - 1) / C.top_k : w.n - 1) * C.ldx +
-                                     C.cols) * 2;
+                                     C.cols) * XB;
         return __builtin_amdgcn_make_buffer_rsrc(
             uni_ptr(const_cast<char*>(p)), 0, uni(int(uint32_t(min(n, size_t(kOutside))))),
             kRawBuffer);
@@ -169,7 +184,7 @@ __global__ __launch_bounds__(kThreads4, 2) void tile4_kernel(const GroupedCall C
 
     // (blocks past the last input hold zeros; a tile has an even number)
     const int T = max(2, ((C.cols + kBlockK - 1) / kBlockK + 1) & ~1);
-    int u[LX];
+    int u[XR];
     Where cur = locate(place), nxt;
     if (cur.n == 0) return;
     use_rows(cur, u);
@@ -178,13 +193,70 @@ __global__ __launch_bounds__(kThreads4, 2) void tile4_kernel(const GroupedCall C
     auto xb = x_buffer(cur);
     auto wb = w_buffer(cur), sb = s_buffer(cur), zb = z_buffer(cur);
     int kx = 0, kw = 0;
+    // fp32: to registers, and from there as two halves to LDS
+    u32x4 raw[X32 ? LX : 1];
+    auto load_x = [&]() {
+#pragma unroll
+        for (int j = 0; j < (X32 ? LX : 1); ++j) {
+            const bool in = pa[0] != kOutside && kx * kBlockK + (j * 8 + (lane & 7)) * 4 < C.cols;
+            uint32_t at = in ? pa[0] + uint32_t(j * 128 + kx * kBlockK * 4) : kOutside;
+            asm("" : "+v"(at));                          // (no branches with a load in each)
+            raw[j] =
+                __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(xb, at, 0, 0));
+        }
+        ++kx;
+    };
+    // times a power of two per row and block that brings the largest to [2^14,
+    // 2^15); row r holds the values rounded to fp16, row 64 + r the rest, times
+    // 2^11, rounded again
+    auto split_x = [&](int stage) {
+        float v[4 * LX];
+        float big = 0.0f;
+#pragma unroll
+        for (int j = 0; j < (X32 ? LX : 1); ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t bits = raw[j][i];
+                v[4 * j + i] = __uint_as_float(bits);
+                const float a = fabsf(v[4 * j + i]);
+                big = a < INFINITY ? fmaxf(big, a) : big;
+            }
+        big = fmaxf(big, dpp<0xB1, 0xF>(big));
+        big = fmaxf(big, dpp<0x4E, 0xF>(big));
+        big = fmaxf(big, dpp<0x141, 0xF>(big));
+        const int e = min(max(14 - (int(__float_as_uint(big) >> 23) - 127), -113), 126);
+        const float up = __uint_as_float(uint32_t(127 + e) << 23);
+        char* const base = smem + stage * kStageBytes + xrow * 256;
+#pragma unroll
+        for (int j = 0; j < (X32 ? LX : 1); ++j) {
+            uint16_t hi[4], lo[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float s = v[4 * j + i] * up;
+                const _Float16 h = _Float16(s);
+                const float back = float(h);
+                hi[i] = __builtin_bit_cast(uint16_t, h);
+                const _Float16 l = fabsf(back) < INFINITY ? _Float16((s - back) * 2048.0f)
+                                                          : _Float16(0.0f);
+                lo[i] = __builtin_bit_cast(uint16_t, l);
+            }
+            const int g = j * 8 + (lane & 7);            // these 4 inputs of the block
+            char* at = base + (((g >> 1) ^ (xrow & 15)) * 16) + (g & 1) * 8;
+            *reinterpret_cast<u32x2*>(at) = u32x2{hi[0] | uint32_t(hi[1]) << 16,
+                                                  hi[2] | uint32_t(hi[3]) << 16};
+            *reinterpret_cast<u32x2*>(at + 64 * 256) = u32x2{lo[0] | uint32_t(lo[1]) << 16,
+                                                             lo[2] | uint32_t(lo[3]) << 16};
+        }
+        if ((lane & 7) == 0) xscale[stage][xrow] = __uint_as_float(uint32_t(127 - e) << 23);
+    };
     auto issue_x = [&](int stage) {
         char* base = smem + stage * kStageBytes + wv * 1024;
         const bool in = kx * kBlockK + piece * 8 < C.cols;
 #pragma unroll
         for (int i = 0; i < LX; ++i)
             __builtin_amdgcn_raw_ptr_buffer_load_lds(xb, (lds_void*)(base + i * 8192), 16,
-                                                     in ? pa[i] : kOutside, kx * kBlockK * 2, 0, 0);
+                                                     in ? pa[X32 ? 0 : i] : kOutside,
+                                                     kx * kBlockK * 2, 0, 0);
         ++kx;
     };
     u32x4 w[2][2];
@@ -235,11 +307,17 @@ __global__ __launch_bounds__(kThreads4, 2) void tile4_kernel(const GroupedCall C
         ++kw;
     };
     const CodeBits bits = code_bits();
-    issue_x(0);
+    if constexpr (X32) load_x();
+    else issue_x(0);
     __builtin_amdgcn_sched_barrier(0);
     issue_w(std::integral_constant<int, 0>{});
     __builtin_amdgcn_sched_barrier(0);
-    issue_x(1);
+    if constexpr (X32) {
+        split_x(0);
+        load_x();
+    } else {
+        issue_x(1);
+    }
     __builtin_amdgcn_sched_barrier(0);
     issue_w(std::integral_constant<int, 1>{});
 
@@ -256,7 +334,7 @@ __global__ __launch_bounds__(kThreads4, 2) void tile4_kernel(const GroupedCall C
         // this block of x has arrived, and every wave is done with the last.
         // (Loads and stores complete in order: the two blocks that were under
         // way at a tile's end were waited for before its stores.)
-        if (arrived > 0) {
+        if (X32 || arrived > 0) {
             asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
             --arrived;
         } else {
@@ -265,12 +343,14 @@ __global__ __launch_bounds__(kThreads4, 2) void tile4_kernel(const GroupedCall C
         }
         __builtin_amdgcn_sched_barrier(0);
         const bool last = S == 0 && t == T - 2;
+        if constexpr (X32) split_x(S ^ 1);
         if (last) {
             set_rows(nxt, u, parity ^ 1);
             xb = x_buffer(nxt);
             kx = 0;
         }
-        issue_x(xs == 0 ? 2 : xs - 1);
+        if constexpr (X32) load_x();
+        else issue_x(xs == 0 ? 2 : xs - 1);
         __builtin_amdgcn_sched_barrier(0);
         u32x4 wf[2][4];
         float sf[2][kUnits];
@@ -303,35 +383,51 @@ __global__ __launch_bounds__(kThreads4, 2) void tile4_kernel(const GroupedCall C
         issue_w(slot);
         __builtin_amdgcn_sched_barrier(0);
 
-        const char* xt = smem + xs * kStageBytes;
-        u32x4 fa[2][4];
+        // (fp32: H = 1 is the rest of row m)
+        constexpr int H = X32 ? 2 : 1;
+        const char* xt = smem + (X32 ? S : xs) * kStageBytes;
+        u32x4 fa[2][H][4];
         auto read = [&](int m) {
 #pragma unroll
-            for (int s = 0; s < 4; ++s)
-                fa[m & 1][s] = *reinterpret_cast<const u32x4*>(xt + m * 16 * 256 + place_of[s]);
+            for (int h = 0; h < H; ++h)
+#pragma unroll
+                for (int s = 0; s < 4; ++s)
+                    fa[m & 1][h][s] = *reinterpret_cast<const u32x4*>(
+                        xt + (h * 64 + m * 16) * 256 + place_of[s]);
         };
         read(0);
 #pragma unroll
         for (int m = 0; m < kRows / 16; ++m) {
             if (m * 16 >= cur.n) break;
             if (m + 1 < kRows / 16) read(m + 1);
+            f32x4 xf = {1.f, 1.f, 1.f, 1.f};
+            if constexpr (X32) xf = *reinterpret_cast<const f32x4*>(&xscale[S][m * 16 + 4 * q]);
             // a unit's sums meet their scale after the next unit's first products
-            f32x4 d[2][2];
+            f32x4 d[2][2][H];
             auto scale = [&](int k) {
 #pragma unroll
                 for (int b = 0; b < 2; ++b)
 #pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        acc[m][b][r] = fmaf(d[k & 1][b][r], sf[b][k], acc[m][b][r]);
+                    for (int r = 0; r < 4; ++r) {
+                        const float v = d[k & 1][b][0][r], by = sf[b][k];
+                        if constexpr (X32) {
+                            const float both = fmaf(d[k & 1][b][H - 1][r], 1.0f / 2048.0f, v);
+                            acc[m][b][r] = fmaf(both * by, xf[r], acc[m][b][r]);
+                        } else {
+                            acc[m][b][r] = fmaf(v, by, acc[m][b][r]);
+                        }
+                    }
             };
 #pragma unroll
             for (int s = 0; s < 4; ++s) {
                 const int k = s / kPer;
 #pragma unroll
                 for (int b = 0; b < 2; ++b)
-                    d[k & 1][b] =
-                        mfma_x_w<BF16>(fa[m & 1][s], wf[b][s],
-                                       s % kPer == 0 ? f32x4{0.f, 0.f, 0.f, 0.f} : d[k & 1][b]);
+#pragma unroll
+                    for (int h = 0; h < H; ++h)
+                        d[k & 1][b][h] = mfma_x_w<BF16>(
+                            fa[m & 1][h][s], wf[b][s],
+                            s % kPer == 0 ? f32x4{0.f, 0.f, 0.f, 0.f} : d[k & 1][b][h]);
                 if (s > 0 && s % kPer == 0) scale(k - 1);
             }
             scale(kUnits - 1);
@@ -359,8 +455,10 @@ __global__ __launch_bounds__(kThreads4, 2) void tile4_kernel(const GroupedCall C
             step(std::integral_constant<int, 1>{}, t + 1);
         }
         __builtin_amdgcn_sched_barrier(0);
-        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(LW) : "memory");
-        arrived = 2;
+        if constexpr (!X32) {
+            asm volatile("s_waitcnt vmcnt(%0)" ::"n"(LW) : "memory");
+            arrived = 2;
+        }
         const int* rows = ymap + parity * kRows + 4 * q;
 #pragma unroll
         for (int m = 0; m < kRows / 16; ++m) {
@@ -387,14 +485,15 @@ __global__ __launch_bounds__(kThreads4, 2) void tile4_kernel(const GroupedCall C
 #endif
 }
 
-template <bool BF16, int GM, bool ZEROS>
+template <bool BF16, bool X32, int GM, bool ZEROS>
 hipError_t run_tiles4(const GroupedCall& C, hipStream_t st) {
     const int out = C.flags & PM_GROUPED_SWIGLU ? C.rows / 2 : C.rows;
     const int per = C.flags & PM_GROUPED_SWIGLU ? kOuts / 2 : kOuts;
     const int nt = (out + per - 1) / per;
+    constexpr int kRows = tile4_rows(X32);
     const size_t lds =
-        size_t(kStages) * kStageBytes + (2 * kRows + C.n_experts + 1) * sizeof(int);
-    auto* f = tile4_kernel<BF16, GM, ZEROS>;
+        size_t(tile4_stages(X32)) * kStageBytes + (2 * kRows + C.n_experts + 1) * sizeof(int);
+    auto* f = tile4_kernel<BF16, X32, GM, ZEROS>;
     hipError_t e = allow_lds(reinterpret_cast<const void*>(f), kTileMaxLds);
     if (e != hipSuccess) return e;
     const int64_t tiles = (int64_t(std::min(C.n_rows, C.n_experts)) + C.n_rows / kRows) * nt;
@@ -403,20 +502,26 @@ hipError_t run_tiles4(const GroupedCall& C, hipStream_t st) {
     return hipGetLastError();
 }
 
-template <bool BF16, bool ZEROS>
+template <bool BF16, bool X32, bool ZEROS>
 hipError_t run_tiles4_group(const GroupedCall& C, hipStream_t st) {
-    if (reads_scales_by(C, 128, 1)) return run_tiles4<BF16, kGroup128, ZEROS>(C, st);
-    if (reads_scales_by(C, 64, 1)) return run_tiles4<BF16, kGroup64, ZEROS>(C, st);
-    if (reads_scales_by(C, 32, 1)) return run_tiles4<BF16, kGroup32, ZEROS>(C, st);
-    return run_tiles4<BF16, kAnyGroup, ZEROS>(C, st);
+    if (reads_scales_by(C, 128, 1)) return run_tiles4<BF16, X32, kGroup128, ZEROS>(C, st);
+    if (reads_scales_by(C, 64, 1)) return run_tiles4<BF16, X32, kGroup64, ZEROS>(C, st);
+    if (reads_scales_by(C, 32, 1)) return run_tiles4<BF16, X32, kGroup32, ZEROS>(C, st);
+    return run_tiles4<BF16, X32, kAnyGroup, ZEROS>(C, st);
+}
+
+template <bool BF16, bool X32>
+hipError_t run_tiles4_zeros(const GroupedCall& C, hipStream_t st) {
+    return C.zeros ? run_tiles4_group<BF16, X32, true>(C, st)
+                   : run_tiles4_group<BF16, X32, false>(C, st);
 }
 
 }  // namespace
 
 hipError_t launch_grouped_tiles4(const GroupedCall& C, hipStream_t st) {
-    if (C.x_type == PM_BF16)
-        return C.zeros ? run_tiles4_group<true, true>(C, st) : run_tiles4_group<true, false>(C, st);
-    return C.zeros ? run_tiles4_group<false, true>(C, st) : run_tiles4_group<false, false>(C, st);
+    if (C.x_type == PM_F32) return run_tiles4_zeros<false, true>(C, st);
+    return C.x_type == PM_BF16 ? run_tiles4_zeros<true, false>(C, st)
+                               : run_tiles4_zeros<false, false>(C, st);
 }
 
 }  // namespace pm

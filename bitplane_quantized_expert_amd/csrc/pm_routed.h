@@ -55,7 +55,7 @@ hipError_t launch_grouped_tiles(const GroupedCall& C, int rows, hipStream_t st);
 // Whether the table of experts lies in LDS beside the stages of 128-row tiles
 // (beside those of 256 rows it always does).
 bool tiles128_fit(const GroupedCall& C);
-// Tiles of 128 x 256 with 4-bit weights and 16-bit activations
+// Tiles of 128 (fp32 activations: 64) x 256 with 4-bit weights
 // (pm_grouped_tile4.hip); the same limit.
 hipError_t launch_grouped_tiles4(const GroupedCall& C, hipStream_t st);
 // Weights streamed past 16 columns of activations (pm_grouped_stream.h): 16-bit

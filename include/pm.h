@@ -446,8 +446,8 @@ pm_status pm_grouped_gemm(pm_grouped_shape s, int type, const void* d_w, pm_grou
  *   zero point per `group` inputs of one row; d_zeros null: z = 8.
  *   group % 32 == 0, cols % group == 0 (PM_ERR_SHAPE).
  * x and y are fp32, fp16 or bf16, y fp32 or of x's type.  The products take
- * fp16 values: x in fp16 enters as it is, bf16 and fp32 times a power of two
- * per row and share of 128 to 512 inputs.  What bf16 loses thereby is at most
+ * fp16 values (bf16 ones where a group has many rows): x in fp16 enters as it
+ * is, bf16 and fp32 times a power of two per row and share of 128 to 512 inputs.  What bf16 loses thereby is at most
  * 2^-39 of the share's largest; fp32 enters as the sum of two halves, off by
  * at most 2^-23 of its value or 2^-50 of the share's largest. */
 pm_status pm_grouped_gemm_w4(pm_grouped_shape s, int group, const uint8_t* d_q,

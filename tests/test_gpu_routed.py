@@ -459,7 +459,8 @@ def test_w4_few_rows_16_bit(E, group, C, zeros):
     run_w4(counts.tolist(), 4094, C, group, zeros, "bf16", "bf16", 2, GATHER | SWIGLU, seed=9)
 
 
-@pytest.mark.parametrize("ty,y_ty", [("f16", "f16"), ("bf16", "f32"), ("bf16", "bf16")])
+@pytest.mark.parametrize("ty,y_ty", [("f16", "f16"), ("bf16", "f32"), ("bf16", "bf16"),
+                                     ("f32", "f32")])
 @pytest.mark.parametrize("flags,top_k", LAYOUTS)
 def test_w4_many_rows_layouts(ty, y_ty, flags, top_k):
     report(f"w4 tiles {ty}->{y_ty} flags {flags}")
@@ -475,19 +476,21 @@ def test_w4_many_rows_groups(group, C, zeros):
     report(f"w4 tiles group {group} cols {C} zeros {zeros}")
     run_w4([60, 48, 100], 258, C, group, zeros, "f16", "f32", 2, GATHER, seed=3)
     run_w4([200, 16, 129], 130, C, group, zeros, "bf16", "bf16", 1, SCATTER | SWIGLU, seed=4)
+    run_w4([64, 16, 129], 258, C, group, zeros, "f32", "f32", 1, SCATTER, seed=5)
 
 
-def test_w4_many_rows_rounds_and_bad_entries():
+@pytest.mark.parametrize("ty", ["f16", "bf16", "f32"])
+def test_w4_many_rows_rounds_and_bad_entries(ty):
     """Several rounds of tiles; rows and order entries left out; a wide x; no
     order; infinities beside other rows."""
-    report("w4 tiles: rounds, entries out of range, strides")
-    run_w4([1500, 3, 0, 900, 128, 64], 4100, 256, 128, True, "bf16", "bf16", 3, GATHER, seed=5)
-    run_w4([1500, 3, 0, 900, 128, 64], 4096, 128, 32, False, "f16", "f16", 1, SWIGLU, seed=6,
+    report(f"w4 tiles {ty}: rounds, entries out of range, strides")
+    run_w4([1500, 3, 0, 900, 128, 64], 4100, 256, 128, True, ty, ty, 3, GATHER, seed=5)
+    run_w4([1500, 3, 0, 900, 128, 64], 4096, 128, 32, False, ty, ty, 1, SWIGLU, seed=6,
            pad=2, order=False)
     off, order = rc.groups([300, 200, 100], 1)
     order[2], order[7], order[411] = -1, 600, 2 ** 31 - 1
     q, sc, z = make_w4(3, 72, 320, 64, True, 1)
-    x = torch.randn(600, 320, generator=rc.gen(2), device="cuda").half()
+    x = torch.randn(600, 320, generator=rc.gen(2), device="cuda").to(rc.TYPES[ty])
     for flags in (SCATTER, 0, GATHER):
         y = torch.full((600, 72), 3.0, device="cuda")
         pm.pm_grouped_gemm_w4(q, sc, z, 64, x, y, off, order, 1, flags)
