@@ -16,16 +16,16 @@ namespace pm {
 // table of experts (above some 3500).  The groups' sizes are on the device; these
 // are rows per group if every expert had some.
 //
-// 4-bit weights: tiles decode them less often from 20 rows per group on: us of
-// the streamed kernel against tiles at 12, 20, 32 rows, 16-bit activations:
-// 195/254, 300/274, 404/303 (512 experts, 512 inputs, 4096 outputs); 92/128,
-// 132/130, 176/134 (128 experts, 2048 x 2048); 68/72, 85/73, 106/75 (32 experts,
-// 4096 inputs, 2048 outputs); 302/527, 464/550, 640/551 (256 of these); fp32:
-// 277/334, 421/384, 636/418; 133/159, 190/177, 283/199; 86/86, 116/90, 157/97;
-// 502/641, 745/663, 1127/689.  Where every workgroup has at most 4 blocks of 128
-// inputs to do, tiles start sooner at any number of rows: 20/16 us at one row
-// (128 experts, 256 inputs, 1024 outputs; fp32 19/18), 18/12 (16 experts, 512
-// inputs, 1024 outputs; fp32 16/15); with 8 blocks (1024 inputs) 17/18, 17/23.
+// 4-bit weights: tiles decode them less often from 16 rows per group on: us of
+// the streamed kernel against tiles at 12, 16, 32 rows, 16-bit activations:
+// 193/228, 248/239, 403/276 (512 experts, 512 inputs, 4096 outputs); 92/107,
+// 113/108, 178/119 (128 experts, 2048 x 2048); 74/63, 83/63, 113/66 (32 experts,
+// 4096 inputs, 2048 outputs); 300/439, 387/449, 654/469 (256 of these); fp32:
+// 288/328, 364/332, 661/404; 139/154, 170/164, 307/197; 87/85, 105/86, 162/97;
+// 503/572, 622/619, 1128/692.  Where every workgroup has at most 4 blocks of 128
+// inputs to do, tiles start sooner at any number of rows: 19/15 us at one row
+// (128 experts, 256 inputs, 1024 outputs; fp32 19/18), 16/12 (16 experts, 512
+// inputs, 1024 outputs; fp32 16/15); with 8 blocks (1024 inputs) 19/17, 17/23.
 hipError_t launch_grouped(const GroupedCall& C, int kind, hipStream_t st) {
     const int64_t groups = std::min(C.n_experts, C.n_rows);
     const int64_t x_rows = C.flags & PM_GROUPED_GATHER ? (C.n_rows - 1) / C.top_k + 1 : 256;
@@ -33,7 +33,7 @@ hipError_t launch_grouped(const GroupedCall& C, int kind, hipStream_t st) {
     if (kind == kW4) {
         const int64_t blocks = (C.cols + 127) / 128, cus = compute_units();
         const int64_t rounds = (groups * ((C.rows + 255) / 256) + cus - 1) / cus;
-        if (far || (C.n_rows < 20 * groups && blocks * rounds > 4))
+        if (far || (C.n_rows < 16 * groups && blocks * rounds > 4))
             return C.x_type == PM_F32 ? launch_grouped_stream4f(C, st)
                                       : launch_grouped_stream4(C, st);
         return launch_grouped_tiles4(C, st);

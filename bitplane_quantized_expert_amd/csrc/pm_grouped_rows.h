@@ -15,13 +15,28 @@ struct RowRange {
     int row0, n;
 };
 
-// Sorted rows of expert e.  Offsets are clamped to 0..n_rows and taken to not
-// decrease, so a bad value reads and writes nothing out of bounds.
-__device__ inline RowRange group_rows(const GroupedCall& C, int e) {
+// Sorted rows from offset a on, up to offset b.  Offsets are clamped to
+// 0..n_rows and taken to not decrease, so a bad value reads and writes nothing
+// out of bounds.
+__device__ inline RowRange row_range(const GroupedCall& C, int a, int b) {
     RowRange r;
-    r.row0 = min(max(C.offsets[e], 0), C.n_rows);
-    r.n = max(min(C.offsets[e + 1], C.n_rows) - r.row0, 0);
+    r.row0 = min(max(a, 0), C.n_rows);
+    r.n = max(min(b, C.n_rows) - r.row0, 0);
     return r;
+}
+
+// Sorted rows of expert e.
+__device__ inline RowRange group_rows(const GroupedCall& C, int e) {
+    return row_range(C, C.offsets[e], C.offsets[e + 1]);
+}
+
+// The same for an expert that the whole wave shares, by scalar loads: these do
+// not wait for the vector loads under way.  (Nothing writes the offsets while
+// the kernel runs.)
+__device__ inline RowRange group_rows_uniform(const GroupedCall& C, int e) {
+    typedef const __attribute__((address_space(4))) int32_t* Constant;
+    const Constant o = (Constant)(reinterpret_cast<uintptr_t>(C.offsets));
+    return row_range(C, o[e], o[e + 1]);
 }
 
 // The number of row tiles of mt rows, no more than offsets that do not

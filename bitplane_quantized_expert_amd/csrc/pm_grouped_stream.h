@@ -44,7 +44,7 @@
 // takes 9 and finding the groups, converting x and the last sums the rest.
 // The decoding, repeated for every 16 columns, bounds 4-bit calls of more rows:
 // 64 experts of 4096 x 4096 with 32, 64, 128 bf16 rows each take 261, 500, 997
-// us here, which is why tiles take over from some 20 rows on.
+// us here, which is why tiles take over from some 16 rows on.
 #pragma once
 
 #include <hip/hip_runtime.h>

@@ -5,7 +5,7 @@
 //
 // (v_mfma_f32_16x16x32; q - z is exact in fp16 and bf16, sums are fp32.)
 // Streamed past 16 columns at a time, the weights are decoded once per 16 rows
-// of x, which bounds groups of more than some 20 rows; here once per 128.
+// of x, which bounds groups of more than some 16 rows; here once per 128.
 //
 // 8 waves, each with 32 weight rows and all 128 rows of x.  The codes go from
 // memory to registers, 16 bytes per lane and 128 inputs (as in the streamed
@@ -21,9 +21,10 @@
 //
 // Bound by LDS: every 1 KiB read of x feeds two products.  A wave of 64 x 64
 // would halve that, but decode every code twice.  Measured: 64 experts of 4096 x
-// 4096 with 128 bf16 rows each 339 us (811 TFLOP/s; the streamed kernel 997), with
-// 64 rows 244 us (500); 8 experts with 256 rows 93 us (223).  With fp32: 809 us (1930), 411 (968), 244 (416): the conversion and the
-// products of a wave follow each other.
+// 4096 with 128 bf16 rows each 337 us (816 TFLOP/s; the streamed kernel 997),
+// with 64 rows 235 us (500); 8 experts with 256 rows 91 us (223).  With fp32: 776
+// us (1930), 409 (968), 224 (416): the conversion and the products of a wave
+// follow each other.
 //
 // LDS holds rows of 128 inputs (256 bytes = 16 pieces); piece c of row r lies
 // at place c ^ (r % 16), so that the 16-byte reads of 16 rows fall in distinct
@@ -111,7 +112,7 @@ __global__ __launch_bounds__(kThreads4, 2) void tile4_kernel(const GroupedCall C
         if (i < n_tiles) {
             const int mt = i / nt;
             const int e = tile_expert(C, before, mt);
-            const RowRange g = group_rows(C, e);
+            const RowRange g = group_rows_uniform(C, e);
             const int64_t skip = int64_t(mt - before[e]) * kRows;
             const bool ok = skip >= 0 && skip < g.n;      // (not so only for bad offsets)
             w.e = uni(e);
@@ -125,23 +126,30 @@ __global__ __launch_bounds__(kThreads4, 2) void tile4_kernel(const GroupedCall C
     // ---- x: this lane's rows of a block, 4 loads of 4 rows per wave (fp32: of
     // one row, 8 lanes each)
     const int xrow = X32 ? int(threadIdx.x >> 3) : wv * 4 + q, piece = i16 ^ (xrow & 15);
+    // (loads only: they are waited for in set_rows, many blocks later)
     auto use_rows = [&](const Where& w, int* u) {
 #pragma unroll
-        for (int i = 0; i < XR; ++i)
-            u[i] = i * 32 + xrow < w.n ? use_of(C, w.row0 + i * 32 + xrow) : -1;
+        for (int i = 0; i < XR; ++i) u[i] = w.row0 + i * 32 + xrow;
+        if (C.order) {
+#pragma unroll
+            for (int i = 0; i < XR; ++i) u[i] = C.order[min(u[i], C.n_rows - 1)];
+        }
     };
     uint32_t pa[XR];
     auto set_rows = [&](const Where& w, const int* u, int parity) {
 #pragma unroll
         for (int i = 0; i < XR; ++i) {
             const int r = i * 32 + xrow;
-            const uint32_t xr = gather ? uint32_t(u[i]) / uint32_t(C.top_k) : uint32_t(r);
-            pa[i] = u[i] >= 0 ? uint32_t(xr * uint64_t(C.ldx) * XB) +
+            int use = u[i];
+            asm volatile("" : "+v"(use));                // (nothing is done to it before)
+            const bool ok = r < w.n && use >= 0 && use < C.n_rows;
+            const uint32_t xr = gather ? uint32_t(use) / uint32_t(C.top_k) : uint32_t(r);
+            pa[i] = ok ? uint32_t(xr * uint64_t(C.ldx) * XB) +
                                     (X32 ? (lane & 7) * 16 : piece * 16)
                               : kOutside;
             if ((lane & (X32 ? 7 : 15)) == 0)
                 ymap[parity * kRows + r] =
-                    u[i] < 0 ? -1 : (C.flags & PM_GROUPED_SCATTER ? u[i] : w.row0 + r);
+                    ok ? (C.flags & PM_GROUPED_SCATTER ? use : w.row0 + r) : -1;
         }
     };
     auto x_buffer = [&](const Where& w) {
@@ -176,10 +184,21 @@ __global__ __launch_bounds__(kThreads4, 2) void tile4_kernel(const GroupedCall C
             uni_ptr(const_cast<uint16_t*>(C.scales) + size_t(w.e) * C.rows * ng), 0,
             uni(int(uint32_t(C.rows) * uint32_t(ng) * 2)), kRawBuffer);
     };
+    // Zero points of one block are bytes of one aligned word, which is loaded
+    // whole: narrower values would be widened at the loop's end, which waits
+    // for them.  (A word that holds a zero point is on the same page with it.)
+    constexpr bool kZeroWords = ZEROS && GM != kAnyGroup;
+    uint32_t zmis = 0;                            // bytes from the word's start to the first
     auto z_buffer = [&](const Where& w) {
-        return __builtin_amdgcn_make_buffer_rsrc(
-            uni_ptr(const_cast<uint8_t*>(C.zeros) + size_t(w.e) * C.rows * ng), 0,
-            uni(int(uint32_t(C.rows) * uint32_t(ng))), kRawBuffer);
+        const uint8_t* p = C.zeros + size_t(w.e) * C.rows * ng;
+        uint32_t n = uint32_t(C.rows) * uint32_t(ng);
+        if constexpr (kZeroWords) {
+            zmis = uni(int(reinterpret_cast<uintptr_t>(p) & 3));
+            p -= zmis;
+            n = (n + zmis + 3) & ~3u;
+        }
+        return __builtin_amdgcn_make_buffer_rsrc(uni_ptr(const_cast<uint8_t*>(p)), 0, uni(int(n)),
+                                                 kRawBuffer);
     };
 
     // (blocks past the last input hold zeros; a tile has an even number)
@@ -260,7 +279,7 @@ __global__ __launch_bounds__(kThreads4, 2) void tile4_kernel(const GroupedCall C
         ++kx;
     };
     u32x4 w[2][2];
-    uint32_t sc[2][2][2], zp[2][2];               // [slot][weight row]
+    uint32_t sc[2][2][2], zp[2][2], zsh[2][2];    // [slot][weight row]
     auto issue_w = [&](auto slot) {
         constexpr int S = decltype(slot)::value;
 #pragma unroll
@@ -286,21 +305,21 @@ __global__ __launch_bounds__(kThreads4, 2) void tile4_kernel(const GroupedCall C
                 if constexpr (ZEROS) zp[S][b] = z;
             } else {
                 const uint32_t g = uint32_t(wrow[b]) * ng + uint32_t(kw) * kUnits;
-                const uint32_t so = chosen(some, g * 2), zo = chosen(some, g);
+                const uint32_t so = chosen(some, g * 2);
+                if constexpr (kZeroWords) {
+                    const uint32_t at = g + zmis;
+                    zsh[S][b] = (at & 3) * 8;
+                    zp[S][b] = __builtin_amdgcn_raw_buffer_load_b32(zb, chosen(some, at & ~3u), 0, 0);
+                }
                 if constexpr (kUnits == 1) {
                     sc[S][b][0] = uint16_t(__builtin_amdgcn_raw_buffer_load_b16(sb, so, 0, 0));
-                    if constexpr (ZEROS)
-                        zp[S][b] = uint8_t(__builtin_amdgcn_raw_buffer_load_b8(zb, zo, 0, 0));
                 } else if constexpr (kUnits == 2) {
                     sc[S][b][0] = __builtin_amdgcn_raw_buffer_load_b32(sb, so, 0, 0);
-                    if constexpr (ZEROS)
-                        zp[S][b] = uint16_t(__builtin_amdgcn_raw_buffer_load_b16(zb, zo, 0, 0));
                 } else {
                     const u32x2 v = __builtin_bit_cast(
                         u32x2, __builtin_amdgcn_raw_buffer_load_b64(sb, so, 0, 0));
                     sc[S][b][0] = v[0];
                     sc[S][b][1] = v[1];
-                    if constexpr (ZEROS) zp[S][b] = __builtin_amdgcn_raw_buffer_load_b32(zb, zo, 0, 0);
                 }
             }
         }
@@ -356,21 +375,27 @@ __global__ __launch_bounds__(kThreads4, 2) void tile4_kernel(const GroupedCall C
         float sf[2][kUnits];
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
+            uint32_t zeros4 = 0;
+            if constexpr (ZEROS) zeros4 = kZeroWords ? zp[S][b] >> zsh[S][b] : zp[S][b];
             const u32x4 c = kWhole ? w[S][b] : exchange(w[S][b]);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 f16x2 za = {_Float16(1032.0f), _Float16(1032.0f)};
                 f16x2 zc = {_Float16(72.0f), _Float16(72.0f)};
                 if constexpr (ZEROS) {
-                    const uint32_t z = zp[S][b] >> (8 * (j / kPer)) & 255u;
+                    const uint32_t z = zeros4 >> (8 * (j / kPer)) & 255u;
                     za = __builtin_bit_cast(f16x2, 0x64006400u | z | z << 16);
                     zc = za - f16x2{_Float16(960.0f), _Float16(960.0f)};
                 }
                 wf[b][j] = codes_in_order<BF16>(bits, c[j], za, zc);
             }
 #pragma unroll
-            for (int k = 0; k < kUnits; ++k)
+            for (int k = 0; k < kUnits; ++k) {
                 sf[b][k] = half_bits(sc[S][b][k / 2] >> (16 * (k & 1)));
+                // here, so that the next loads can take the scales' registers (else
+                // they are copied at the loop's end, which waits for them)
+                asm volatile("" : "+v"(sf[b][k]));
+            }
         }
         __builtin_amdgcn_sched_barrier(0);
         if (last) {

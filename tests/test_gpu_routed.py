@@ -449,14 +449,14 @@ def test_w4_many_inputs(group, C):
                                        (33, 32, 256), (33, 64, 256), (33, 128, 256), (33, 96, 192),
                                        (33, 128, 384), (33, 32, 512), (33, 64, 512), (33, 96, 480),
                                        (4, 32, 1024), (4, 128, 1280), (4, 96, 1152)])
-def test_w4_few_rows_16_bit(E, group, C, zeros):
-    """Few rows of 16-bit activations, with many experts where the inputs are
-    few."""
+def test_w4_few_rows(E, group, C, zeros):
+    """Few rows, with many experts where the inputs are few."""
     report(f"w4 few rows {E} experts group {group} cols {C} zeros {zeros}")
     counts = np.random.default_rng(E + C).integers(0, 4, E)
     counts[[0, E // 2, E - 1]] = [17, 5, 1]
     run_w4(counts.tolist(), 4096, C, group, zeros, "f16", "f32", 1, SCATTER, seed=8)
     run_w4(counts.tolist(), 4094, C, group, zeros, "bf16", "bf16", 2, GATHER | SWIGLU, seed=9)
+    run_w4(counts.tolist(), 4096, C, group, zeros, "f32", "f32", 1, 0, seed=10)
 
 
 @pytest.mark.parametrize("ty,y_ty", [("f16", "f16"), ("bf16", "f32"), ("bf16", "bf16"),
@@ -540,6 +540,36 @@ def test_w4_strides_and_rows_outside():
         want = rc.grouped_plain(lambda e: rc.decode_w4(q[e], sc[e], z[e], 32), x, off, order, 16,
                                 1, bool(flags & GATHER), bool(flags & SCATTER), False)
         rc.check_grouped(y, 3.0, want, f"flags {flags}")
+
+
+@pytest.mark.parametrize("ty", ["f32", "bf16"])
+def test_w4_wide_ranges_many_inputs(ty):
+    """The same through the streamed kernel (few rows) and through tiles, with
+    infinities and NaN in single rows."""
+    report(f"w4 wide ranges {ty}, many inputs")
+    run_w4([1, 3, 12], 48, 1280, 128, True, ty, "f32", 1, 0, seed=5, spread=True)
+    run_w4([65, 3, 130], 48, 1280, 64, False, ty, "f32", 1, 0, seed=6, spread=True)
+    q, s, z = make_w4(2, 32, 1280, 64, True, 1)
+    for counts in ([4, 3], [70, 60]):
+        off, _ = rc.groups(counts, 0)
+        n = sum(counts)
+        x = torch.randn(n, 1280, generator=rc.gen(2), device="cuda")
+        x[:5] *= torch.tensor([1e30, 1e-30, 0.0, 1e5, 1e-7], device="cuda")[:, None]
+        x = x.to(rc.TYPES[ty])
+        y = torch.full((n, 32), 3.0, device="cuda")
+        pm.pm_grouped_gemm_w4(q, s, z, 64, x, y, off)
+        want = rc.grouped_plain(lambda e: rc.decode_w4(q[e], s[e], z[e], 64), x, off, None, n, 1,
+                                False, False, False)
+        rc.check_grouped(y, 3.0, want, "row ranges")
+        assert not y[2].any()
+        bad = x.clone()
+        bad[3, 700], bad[6, 1279] = float("nan"), float("inf")
+        got = torch.empty_like(y)
+        pm.pm_grouped_gemm_w4(q, s, z, 64, bad, got, off)
+        keep = torch.ones(n, dtype=torch.bool, device="cuda")
+        keep[[3, 6]] = False
+        assert torch.equal(got[keep], y[keep])
+        assert torch.isnan(got[3]).all() and not torch.isfinite(got[6]).all()
 
 
 @pytest.mark.parametrize("ty", ["f32", "f16", "bf16"])
