@@ -26,9 +26,10 @@
 // us (1930), 409 (968), 224 (416): the conversion and the products of a wave
 // follow each other.
 //
-// LDS holds rows of 128 inputs (256 bytes = 16 pieces); piece c of row r lies
-// at place c ^ (r % 16), so that the 16-byte reads of 16 rows fall in distinct
-// banks.  Rows past the group and inputs past `cols` read as zero.
+// LDS holds rows of 128 inputs (256 bytes = 16 pieces).  The four pieces that
+// one product takes (a lane quarter's each) come to adjacent places 4 s + q, and
+// place p of row r lies at p ^ (r % 16): 16-byte reads are served 16 lanes at a
+// time, of two quarters and all rows, which so fall in distinct banks.  Rows past the group and inputs past `cols` read as zero.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -125,7 +126,11 @@ __global__ __launch_bounds__(kThreads4, 2) void tile4_kernel(const GroupedCall C
 
     // ---- x: this lane's rows of a block, 4 loads of 4 rows per wave (fp32: of
     // one row, 8 lanes each)
-    const int xrow = X32 ? int(threadIdx.x >> 3) : wv * 4 + q, piece = i16 ^ (xrow & 15);
+    const int xrow = X32 ? int(threadIdx.x >> 3) : wv * 4 + q;
+    // product s takes piece 4 q + s of quarter q where a scale covers the block,
+    // else 4 s + q; its place (and back)
+    auto place_piece = [](int p) { return kWhole ? (p & 3) * 4 + (p >> 2) : p; };
+    const int piece = place_piece(i16 ^ (xrow & 15));
     // (loads only: they are waited for in set_rows, many blocks later)
     auto use_rows = [&](const Where& w, int* u) {
 #pragma unroll
@@ -260,7 +265,7 @@ __global__ __launch_bounds__(kThreads4, 2) void tile4_kernel(const GroupedCall C
                 lo[i] = __builtin_bit_cast(uint16_t, l);
             }
             const int g = j * 8 + (lane & 7);            // these 4 inputs of the block
-            char* at = base + (((g >> 1) ^ (xrow & 15)) * 16) + (g & 1) * 8;
+            char* at = base + ((place_piece(g >> 1) ^ (xrow & 15)) * 16) + (g & 1) * 8;
             *reinterpret_cast<u32x2*>(at) = u32x2{hi[0] | uint32_t(hi[1]) << 16,
                                                   hi[2] | uint32_t(hi[3]) << 16};
             *reinterpret_cast<u32x2*>(at + 64 * 256) = u32x2{lo[0] | uint32_t(lo[1]) << 16,
@@ -344,7 +349,7 @@ __global__ __launch_bounds__(kThreads4, 2) void tile4_kernel(const GroupedCall C
     int place_of[4];
 #pragma unroll
     for (int s = 0; s < 4; ++s)
-        place_of[s] = i16 * 256 + (((kWhole ? q * 4 + s : s * 4 + q) ^ i16) * 16);
+        place_of[s] = i16 * 256 + (((s * 4 + q) ^ i16) * 16);
     f32x4 acc[kRows / 16][2];
     int xs = 0, parity = 0, arrived = 0;
     auto step = [&](auto slot, int t) {
