@@ -19,12 +19,14 @@
 // of the value, or 2^-50 of the largest.  Every lane holds 16 inputs of a row,
 // loaded a block ahead, and converts them while the last block is multiplied.
 //
-// Bound by LDS: every 1 KiB read of x feeds two products.  A wave of 64 x 64
-// would halve that, but decode every code twice.  Measured: 64 experts of 4096 x
-// 4096 with 128 bf16 rows each 337 us (816 TFLOP/s; the streamed kernel 997),
-// with 64 rows 235 us (500); 8 experts with 256 rows 91 us (223).  With fp32: 776
-// us (1930), 409 (968), 224 (416): the conversion and the products of a wave
-// follow each other.
+// Measured: 64 experts of 4096 x 4096 with 128 bf16 rows each 327 to 338 us (810
+// to 840 TFLOP/s; the streamed kernel 997), the matrix cores 39 % and LDS 20 %
+// busy: a wave decodes, then multiplies, and few of its instructions meet the
+// other wave's.  64 rows 235 us (500), 32 rows 205 (261); 8 experts with 256 rows
+// 92 us (223).  fp32: 752 to 784 us (1930), 407 (968), 323 (489).  Decoding the
+// next block between the products took 3 to 15 % longer (registers, and loads
+// later by most of a block); starting the tiles of an expert at different blocks
+// changed nothing.
 //
 // LDS holds rows of 128 inputs (256 bytes = 16 pieces).  The four pieces that
 // one product takes (a lane quarter's each) come to adjacent places 4 s + q, and
