@@ -10,7 +10,7 @@
 // with removal.  The softmax (fp64) of up to 4 tokens is taken together, 16
 // lanes each.
 //
-// Sorting: calls of up to 16 tokens do it in the same launch, in LDS.  Larger
+// Sorting: calls of few tokens do it in the same launch, in LDS.  Larger
 // ones leave, per block of tokens, how many uses every expert got, and
 // scatter_kernel adds up the columns of that table: the place of a use is the
 // sum over lower experts and earlier blocks, plus its rank among the uses of
@@ -234,7 +234,7 @@ __device__ inline void place_uses(int32_t* order, uint32_t* next, int id, int64_
     }
 }
 
-// A call of one block of up to 16 tokens, one wave each, sorted in LDS.
+// A call of few tokens by one workgroup, sorted in LDS.
 template <int VPT, int TYPE>
 __global__ __launch_bounds__(kRouteThreads) void route_small_kernel(const RouteCall C) {
     extern __shared__ uint32_t lds[];
@@ -377,7 +377,12 @@ template <int VPT, int TYPE>
 hipError_t launch_select_typed(const RouteCall& C, hipStream_t st) {
     // one wave per token, 16 tokens at a time
     const dim3 block(kWave * std::min(C.n_tokens, kRouteWaves));
-    if (C.offsets && C.n_blocks == 1 && C.n_tokens <= kRouteWaves) {
+    // one launch while a wave has few tokens and the last wave few uses to place:
+    // us in one against two launches at 24, 32, 48, 64 tokens: 5.9/7.6, 6.7/8.2,
+    // 8.4/8.6, 9.9/8.5 (60 experts, top-4), 7.4/8.3, 8.9/8.7, 11.4/9.2, 14.2/9.3
+    // (128, top-8), 9.5/11.2, 11.4/11.4, 15.5/11.5, 18.4/11.7 (512, top-10)
+    if (C.offsets && (C.n_tokens <= kRouteWaves ||
+                      (C.n_tokens <= 3 * kRouteWaves && C.n_tokens * C.top_k <= 256))) {
         const size_t lds = (size_t(C.n_experts) + size_t(C.n_tokens) * C.top_k) * 4;
         hipLaunchKernelGGL((route_small_kernel<VPT, TYPE>), dim3(1), block, lds, st, C);
         return hipGetLastError();

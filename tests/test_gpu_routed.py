@@ -46,7 +46,9 @@ def check_route(logits, top_k, got=None, what=""):
 @pytest.mark.parametrize("T,E,K", [(1, 1, 1), (1, 512, 10), (2, 4, 4), (5, 64, 8), (15, 65, 3),
                                    (16, 128, 2), (17, 200, 64), (33, 512, 10), (64, 256, 8),
                                    (65, 60, 4), (300, 1000, 10), (1003, 60, 4), (257, 4096, 64),
-                                   (4100, 512, 10), (9000, 33, 1)])
+                                   (4100, 512, 10), (9000, 33, 1), (24, 512, 10), (25, 512, 10),
+                                   (26, 512, 10), (32, 60, 8), (33, 60, 8), (48, 300, 5),
+                                   (49, 300, 5), (47, 4096, 2), (48, 8, 1), (16, 4096, 64)])
 def test_route_sizes(T, E, K):
     report(f"route {T} x {E} top-{K}")
     g = rc.gen(T * 7 + E)
