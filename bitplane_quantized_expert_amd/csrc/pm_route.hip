@@ -37,6 +37,11 @@ namespace {
 constexpr int kRouteThreads = 1024;
 constexpr int kRouteWaves = kRouteThreads / kWave;
 
+// Waves of a workgroup that selects: 32 and 64 logits per lane need up to 256
+// registers (with 16 waves, spilled: 67 us for 24 tokens of 4096 experts, now 41;
+// of 1500, 56 and now 14).
+constexpr int select_waves(int vpt) { return vpt > 32 ? 4 : vpt > 16 ? 8 : kRouteWaves; }
+
 // Orders like the logits; 0 for -inf and NaN, which are never selected.
 __device__ inline uint32_t order_key(float l) {
     if (!(l > -INFINITY)) return 0;
@@ -177,7 +182,7 @@ __device__ inline void route_tokens(const RouteCall& C, int t0, int t1, int step
 }
 
 template <int VPT, int TYPE>
-__global__ __launch_bounds__(kRouteThreads) void route_kernel(const RouteCall C) {
+__global__ __launch_bounds__(kWave * select_waves(VPT)) void route_kernel(const RouteCall C) {
     extern __shared__ uint32_t hist[];                      // [n_experts]
     const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
     const bool sort = C.offsets != nullptr;
@@ -236,7 +241,7 @@ __device__ inline void place_uses(int32_t* order, uint32_t* next, int id, int64_
 
 // A call of few tokens by one workgroup, sorted in LDS.
 template <int VPT, int TYPE>
-__global__ __launch_bounds__(kRouteThreads) void route_small_kernel(const RouteCall C) {
+__global__ __launch_bounds__(kWave * select_waves(VPT)) void route_small_kernel(const RouteCall C) {
     extern __shared__ uint32_t lds[];
     __shared__ uint32_t wave_tot[kRouteWaves];
     const int E = C.n_experts, n = C.n_tokens * C.top_k;
@@ -246,7 +251,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_small_kernel(const RouteC
     for (int e = threadIdx.x; e < E; e += blockDim.x) count[e] = 0;
     for (int u = threadIdx.x; u < n; u += blockDim.x) ids[u] = -1;
     __syncthreads();
-    route_tokens<VPT, TYPE>(C, wv, C.n_tokens, kRouteWaves, lane, [&](int64_t u, int id) {
+    route_tokens<VPT, TYPE>(C, wv, C.n_tokens, blockDim.x >> 6, lane, [&](int64_t u, int id) {
         atomicAdd(&count[id], 1u);
         ids[u] = id;
     });
@@ -375,14 +380,16 @@ __global__ void route_nothing_kernel(const RouteCall C) {
 
 template <int VPT, int TYPE>
 hipError_t launch_select_typed(const RouteCall& C, hipStream_t st) {
-    // one wave per token, 16 tokens at a time
-    const dim3 block(kWave * std::min(C.n_tokens, kRouteWaves));
+    // one wave per token, 16 tokens (of more than 1024 experts 8, of more than
+    // 2048 4) at a time
+    constexpr int kWaves = select_waves(VPT);
+    const dim3 block(kWave * std::min(C.n_tokens, kWaves));
     // one launch while a wave has few tokens and the last wave few uses to place:
     // us in one against two launches at 24, 32, 48, 64 tokens: 5.9/7.6, 6.7/8.2,
     // 8.4/8.6, 9.9/8.5 (60 experts, top-4), 7.4/8.3, 8.9/8.7, 11.4/9.2, 14.2/9.3
     // (128, top-8), 9.5/11.2, 11.4/11.4, 15.5/11.5, 18.4/11.7 (512, top-10)
-    if (C.offsets && (C.n_tokens <= kRouteWaves ||
-                      (C.n_tokens <= 3 * kRouteWaves && C.n_tokens * C.top_k <= 256))) {
+    if (C.offsets && (C.n_tokens <= kWaves ||
+                      (C.n_tokens <= 3 * kWaves && C.n_tokens * C.top_k <= 256))) {
         const size_t lds = (size_t(C.n_experts) + size_t(C.n_tokens) * C.top_k) * 4;
         hipLaunchKernelGGL((route_small_kernel<VPT, TYPE>), dim3(1), block, lds, st, C);
         return hipGetLastError();
@@ -423,6 +430,7 @@ hipError_t launch_route(const RouteCall& C, hipStream_t st) {
     if (per_lane <= 4) return launch_select<4>(C, st);
     if (per_lane <= 8) return launch_select<8>(C, st);
     if (per_lane <= 16) return launch_select<16>(C, st);
+    if (per_lane <= 32) return launch_select<32>(C, st);
     return launch_select<64>(C, st);
 }
 

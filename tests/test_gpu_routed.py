@@ -48,7 +48,9 @@ def check_route(logits, top_k, got=None, what=""):
                                    (65, 60, 4), (300, 1000, 10), (1003, 60, 4), (257, 4096, 64),
                                    (4100, 512, 10), (9000, 33, 1), (24, 512, 10), (25, 512, 10),
                                    (26, 512, 10), (32, 60, 8), (33, 60, 8), (48, 300, 5),
-                                   (49, 300, 5), (47, 4096, 2), (48, 8, 1), (16, 4096, 64)])
+                                   (49, 300, 5), (47, 4096, 2), (48, 8, 1), (16, 4096, 64),
+                                   (4, 4096, 8), (13, 2049, 8), (8, 2048, 16), (23, 1500, 4),
+                                   (9, 1025, 64), (700, 2048, 10), (1, 1024, 1)])
 def test_route_sizes(T, E, K):
     report(f"route {T} x {E} top-{K}")
     g = rc.gen(T * 7 + E)
