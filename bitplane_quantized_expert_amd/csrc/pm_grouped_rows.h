@@ -54,29 +54,22 @@ __device__ inline int use_of(const GroupedCall& C, int i) {
 
 __device__ inline float silu_up(float g, float u) { return g / (1.0f + expf(-g)) * u; }
 
-// Four adjacent outputs of row y + at, those below `left`.
+// Four adjacent outputs of row y + at, those below `left`.  Rows of y need no
+// alignment beyond their element's: the hardware splits the stores that cross a
+// line.
 template <int YT>
-__device__ inline void store4(void* y, int64_t at, int left, bool vec, const float* v) {
-    if (vec && left >= 4) {
-        if constexpr (YT == PM_F32) {
-            *reinterpret_cast<f32x4*>(static_cast<float*>(y) + at) = f32x4{v[0], v[1], v[2], v[3]};
-        } else {
-            uint16_t h[4];
+__device__ inline void store4(void* y, int64_t at, int left, const float* v) {
+    constexpr int B = YT == PM_F32 ? 4 : 2;
+    if (left >= 4) {
+        alignas(16) char o[4 * B];
 #pragma unroll
-            for (int r = 0; r < 4; ++r) store_f32<YT>(h, r, v[r]);
-            *reinterpret_cast<uint64_t*>(static_cast<uint16_t*>(y) + at) =
-                uint64_t(h[0]) | uint64_t(h[1]) << 16 | uint64_t(h[2]) << 32 | uint64_t(h[3]) << 48;
-        }
+        for (int r = 0; r < 4; ++r) store_f32<YT>(o, r, v[r]);
+        __builtin_memcpy(static_cast<char*>(y) + at * B, o, 4 * B);
         return;
     }
 #pragma unroll
     for (int r = 0; r < 4; ++r)
         if (r < left) store_f32<YT>(y, at + r, v[r]);
-}
-
-// Whether rows of y can be stored 4 elements at a time.
-inline bool stores_by_4(const GroupedCall& C) {
-    return reinterpret_cast<uintptr_t>(C.y) % (4 * type_bytes(C.y_type)) == 0 && C.ldy % 4 == 0;
 }
 
 // before[e] = row tiles of mt rows of the experts below e, e <= n_experts;

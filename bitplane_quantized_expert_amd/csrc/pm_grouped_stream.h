@@ -64,7 +64,6 @@ namespace pm {
 // KW * KB * 128 inputs, row tiles of a matrix.
 struct StreamPlan {
     int kw_log, panels, row_tiles;
-    int vec;                       // y takes 4 elements at a time
 };
 
 namespace {
@@ -646,9 +645,9 @@ __global__ __launch_bounds__(NW * kWave, 2) void stream_kernel(const GroupedCall
 #pragma unroll
                 for (int i = 0; i < 4; ++i) y[i] = glu ? silu_up(p0[i], p1[i]) : p0[i];
                 const int64_t at = int64_t(yr) * C.ldy + o;
-                if (C.y_type == PM_F32) store4<PM_F32>(C.y, at, out - o, P.vec, y);
-                else if (C.y_type == PM_F16) store4<PM_F16>(C.y, at, out - o, P.vec, y);
-                else store4<PM_BF16>(C.y, at, out - o, P.vec, y);
+                if (C.y_type == PM_F32) store4<PM_F32>(C.y, at, out - o, y);
+                else if (C.y_type == PM_F16) store4<PM_F16>(C.y, at, out - o, y);
+                else store4<PM_BF16>(C.y, at, out - o, y);
             }
             buf ^= 1;
         }
@@ -685,7 +684,6 @@ inline StreamPlan plan_stream(const GroupedCall& C, int* nw, int* kb) {
     const int out = C.flags & PM_GROUPED_SWIGLU ? C.rows / 2 : C.rows;
     const int per_tile = C.flags & PM_GROUPED_SWIGLU ? 8 : 16;
     P.row_tiles = (out + per_tile - 1) / per_tile;
-    P.vec = stores_by_4(C);
     return P;
 }
 

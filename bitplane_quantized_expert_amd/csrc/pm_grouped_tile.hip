@@ -74,8 +74,7 @@ __device__ inline f32x4 mfma16(const u32x4& a, const u32x4& b, const f32x4& c) {
 
 // BM rows by 256 weight rows, S stages of 64 inputs in LDS.
 template <int WT, int YT, bool GLU, int BM, int S>
-__global__ __launch_bounds__(kTileThreads, 2) void tile_kernel(const GroupedCall C, int nt,
-                                                               bool vec) {
+__global__ __launch_bounds__(kTileThreads, 2) void tile_kernel(const GroupedCall C, int nt) {
 #ifdef __HIP_DEVICE_COMPILE__
     constexpr int kStageA = BM * kTileK * 2, kStage = kStageA + kTileN * kTileK * 2;
     constexpr int LA = BM / 64, LB = kTileN / 64, L = LA + LB;   // a wave's loads per stage
@@ -322,14 +321,14 @@ __global__ __launch_bounds__(kTileThreads, 2) void tile_kernel(const GroupedCall
                         float v[4];
 #pragma unroll
                         for (int r = 0; r < 4; ++r) v[r] = silu_up(acc[i][j][r], acc[i][j + 1][r]);
-                        store4<YT>(C.y, at + o + 2 * j, out - o - 2 * j, vec, v);
+                        store4<YT>(C.y, at + o + 2 * j, out - o - 2 * j, v);
                     }
                 } else {
                     const int o = cur.o0 + wn * 64 + q * 16;
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         const float v[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
-                        store4<YT>(C.y, at + o + 4 * j, out - o - 4 * j, vec, v);
+                        store4<YT>(C.y, at + o + 4 * j, out - o - 4 * j, v);
                     }
                 }
             }
@@ -359,7 +358,7 @@ hipError_t run_tiles(const GroupedCall& C, hipStream_t st) {
     if (e != hipSuccess) return e;
     const int64_t tiles = (int64_t(std::min(C.n_rows, C.n_experts)) + C.n_rows / BM) * nt;
     const unsigned grid = unsigned(std::min<int64_t>(tiles, compute_units()));
-    hipLaunchKernelGGL(f, dim3(grid), dim3(kTileThreads), lds, st, C, nt, stores_by_4(C));
+    hipLaunchKernelGGL(f, dim3(grid), dim3(kTileThreads), lds, st, C, nt);
     return hipGetLastError();
 }
 
