@@ -95,7 +95,8 @@ __global__ __launch_bounds__(256) void encode_w4_kernel(size_t n_groups, int gro
         hi = fmaxf(hi, v);
     }
     const float range = zeros ? (hi - lo) / 15.0f : fmaxf(hi, -lo) / 7.0f;
-    const __half s = __float2half(range);
+    // (a scale beyond fp16 would be infinite, and zeros NaN)
+    const __half s = __float2half(fminf(range, 65504.0f));
     const float sf = __half2float(s);
     float z = 8.0f;
     if (zeros) z = sf > 0.0f ? fminf(fmaxf(rintf(-lo / sf), 0.0f), 15.0f) : 0.0f;

@@ -459,7 +459,8 @@ pm_status pm_grouped_gemm_w4(pm_grouped_shape s, int group, const uint8_t* d_q,
  * q = clamp(rint(w / scale), -8, 7) + 8; with d_zeros, lo = min(w, 0) and
  * hi = max(w, 0), scale = fp16((hi - lo) / 15), z = clamp(rint(-lo / scale), 0, 15)
  * and q = clamp(rint(w / scale) + z, 0, 15).  A scale of 0 gives q = 8
- * (q = z = 0 with d_zeros).  Weights must be finite (other values give
+ * (q = z = 0 with d_zeros); one beyond fp16's largest value, 65504, is that
+ * value, and the codes clamp.  Weights must be finite (other values give
  * unspecified codes).  d_w and d_q 16-byte aligned. */
 pm_status pm_encode_w4_device(pm_matrix_shape s, const void* d_w, int type, uint8_t* d_q,
                               uint16_t* d_scales, uint8_t* d_zeros, void* stream);
