@@ -3,7 +3,8 @@
 //
 //   D[m][o] = sum_g scale[o][g] sum_{k in g} x[m][k] (q - z)[o][k]
 //
-// (v_mfma_f32_16x16x32; q - z is exact in fp16 and bf16, sums are fp32.)
+// (v_mfma_f32_16x16x32; q - z is exact in fp16, and (q - z) 2^-15 in bf16, sums
+// are fp32.)
 // Streamed past 16 columns at a time, the weights are decoded once per 16 rows
 // of x, which bounds groups of more than some 16 rows; here once per 128.
 //
@@ -19,11 +20,11 @@
 // of the value, or 2^-50 of the largest.  Every lane holds 16 inputs of a row,
 // loaded a block ahead, and converts them while the last block is multiplied.
 //
-// Measured: 64 experts of 4096 x 4096 with 128 bf16 rows each 327 to 338 us (810
-// to 840 TFLOP/s; the streamed kernel 997), the matrix cores 39 % and LDS 20 %
+// Measured: 64 experts of 4096 x 4096 with 128 bf16 rows each 333 to 338 us (815
+// to 825 TFLOP/s; the streamed kernel 997), the matrix cores 39 % and LDS 20 %
 // busy: a wave decodes, then multiplies, and few of its instructions meet the
-// other wave's.  64 rows 235 us (500), 32 rows 205 (261); 8 experts with 256 rows
-// 92 us (223).  fp32: 752 to 784 us (1930), 407 (968), 323 (489).  Decoding the
+// other wave's.  64 rows 238 us (500), 32 rows 213 (261); 8 experts with 256 rows
+// 90 us (223).  fp32: 752 to 784 us (1930), 405 (968), 318 (489).  Decoding the
 // next block between the products took 3 to 15 % longer (registers, and loads
 // later by most of a block); starting the tiles of an expert at different blocks
 // changed nothing.
@@ -56,7 +57,17 @@ constexpr uint32_t kOutside = 0xFFFFFFF0u;      // an offset beyond any buffer
 
 typedef __attribute__((address_space(3))) void lds_void;
 
-// The 8 codes of word w minus the zero point, as 16-bit operands in order.
+// bf16 activations reach fp32's largest values, so that their products with
+// codes and zero points up to 255, summed over 128 inputs, would pass it where
+// the scaled result does not.  Their weight operands are (q - z) 2^-15 and the
+// scales 2^15 larger: 255 * 128 * 2^-15 < 1.  Nothing is lost at the small end:
+// a bf16 value is a multiple of 2^-133, a product of 2^-148, and fp32 holds
+// multiples of 2^-149.  (The factor costs 3 % at 32 rows per expert, nothing at
+// 128.)
+constexpr float kCodeUnit = 1.0f / 32768.0f;
+
+// The 8 codes of word w minus the zero point, as 16-bit operands in order
+// (bf16: in units of kCodeUnit).
 template <bool BF16>
 __device__ inline u32x4 codes_in_order(const CodeBits& k, uint32_t w, f16x2 za, f16x2 zb) {
     const u32x4 c = codes_to_f16(k, w, za, zb);          // 0 4 | 1 5 | 2 6 | 3 7
@@ -66,14 +77,14 @@ __device__ inline u32x4 codes_in_order(const CodeBits& k, uint32_t w, f16x2 za, 
                      __builtin_amdgcn_perm(c[1], c[0], 0x07060302u),
                      __builtin_amdgcn_perm(c[3], c[2], 0x07060302u)};
     } else {
-        // (integers of 8 bits: the upper half of the fp32 value is exact)
+        // (8 significant bits: the upper half of the fp32 value is exact)
         uint32_t lo[4], hi[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const uint32_t pair = c[i];                  // (a bit_cast of c[i] takes c[0])
             const f16x2 h = __builtin_bit_cast(f16x2, pair);
-            lo[i] = __float_as_uint(float(h[0]));
-            hi[i] = __float_as_uint(float(h[1]));
+            lo[i] = __float_as_uint(fmaf(float(h[0]), kCodeUnit, 0.0f));
+            hi[i] = __float_as_uint(fmaf(float(h[1]), kCodeUnit, 0.0f));
         }
         return u32x4{__builtin_amdgcn_perm(lo[1], lo[0], 0x07060302u),
                      __builtin_amdgcn_perm(lo[3], lo[2], 0x07060302u),
@@ -399,6 +410,7 @@ __global__ __launch_bounds__(kThreads4, 2) void tile4_kernel(const GroupedCall C
 #pragma unroll
             for (int k = 0; k < kUnits; ++k) {
                 sf[b][k] = half_bits(sc[S][b][k / 2] >> (16 * (k & 1)));
+                if constexpr (BF16) sf[b][k] *= 1.0f / kCodeUnit;
                 // here, so that the next loads can take the scales' registers (else
                 // they are copied at the loop's end, which waits for them)
                 asm volatile("" : "+v"(sf[b][k]));

@@ -52,3 +52,72 @@ def test_w4_encoder_of_large_weights(ty, zeros):
     assert np.array_equal(np.stack((b & 15, b >> 4), -1).reshape(8, 2, 32), code)
     dec = rc.decode_w4(q, s, z, 32)
     assert torch.isfinite(dec).all() and not dec[:, 5].any()
+
+
+# ---------------------------------------------------------------- 4-bit products
+FEW, MANY = [4, 0, 3], [70, 0, 60]        # rows per expert: streamed weights, tiles
+
+
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("group", [128, 64, 32, 160])
+@pytest.mark.parametrize("counts", [FEW, MANY])
+def test_w4_bf16_rows_of_any_size(counts, group, zeros):
+    """bf16 activations up to the type's largest value under scales that keep
+    the result finite: nothing in between overflows, with zero points up to 255."""
+    report(f"w4 bf16 up to its largest value {counts} group {group} zeros {zeros}")
+    E, R, C = len(counts), 48, 1280
+    g = rc.gen(group)
+    q = torch.randint(0, 256, (E, R, C // 2), generator=g, device="cuda", dtype=torch.uint8)
+    # |q - z| <= 255 and scales of 2^-24 to 2^-20: sums below 2^128 * 255 * 1280 * 2^-20
+    s = (torch.randint(1, 17, (E, R, C // group), generator=g, device="cuda") * 2.0 ** -24).half()
+    z = None
+    if zeros:
+        z = torch.randint(0, 256, (E, R, C // group), generator=g, device="cuda",
+                          dtype=torch.uint8)
+    off, _ = rc.groups(counts, 0)
+    n = sum(counts)
+    x = torch.randn(n, C, generator=g, device="cuda")
+    x[0] *= 1e37
+    x[1] = torch.finfo(torch.bfloat16).max
+    x[2] = torch.finfo(torch.bfloat16).max * x[2].sign()
+    x[4, ::3] *= 1e37
+    x[5] *= 1e37
+    x[n - 1] *= 1e30
+    x = x.to(torch.bfloat16)
+    assert torch.isfinite(x).all()
+    want = rc.grouped_plain(lambda e: rc.decode_w4(q[e], s[e], None if z is None else z[e], group),
+                            x, off, None, n, 1, False, False, False)
+    assert max(float(p.abs().max()) for _, p, _ in want) < 2.0 ** 127
+    for ty in (torch.float32, torch.bfloat16):
+        y = torch.full((n, R), 3.0, dtype=ty, device="cuda")
+        pm.pm_grouped_gemm_w4(q, s, z, group, x, y, off)
+        assert torch.isfinite(y).all()
+        rc.check_grouped(y, 3.0, want, f"{ty}")
+
+
+@pytest.mark.parametrize("group", [128, 64, 32, 160])
+@pytest.mark.parametrize("counts", [FEW, MANY])
+def test_w4_bf16_smallest_values(counts, group):
+    """One-hot rows of bf16's subnormal and smallest normal values: exact, for
+    (q - z) * scale of them is a multiple of 2^-133 below 2^-100."""
+    report(f"w4 bf16 smallest values {counts} group {group}")
+    E, R, C = len(counts), 48, 1280
+    g = rc.gen(group + 1)
+    q = torch.randint(0, 256, (E, R, C // 2), generator=g, device="cuda", dtype=torch.uint8)
+    s = torch.exp2(torch.randint(0, 11, (E, R, C // group), generator=g, device="cuda").float()).half()
+    z = torch.randint(0, 256, (E, R, C // group), generator=g, device="cuda", dtype=torch.uint8)
+    off, _ = rc.groups(counts, 0)
+    n = sum(counts)
+    values = torch.tensor([2.0 ** -133, -3 * 2.0 ** -133, 127 * 2.0 ** -133, 2.0 ** -126,
+                           -255 * 2.0 ** -133, 2.0 ** -120, 1.0], dtype=torch.float64)
+    x = torch.zeros(n, C, dtype=torch.float64)
+    col = torch.arange(n) * 97 % C
+    x[torch.arange(n), col] = values[torch.arange(n) % len(values)]
+    xb = x.to(torch.bfloat16)
+    assert torch.equal(xb.double(), x)
+    y = torch.empty(n, R, device="cuda")
+    pm.pm_grouped_gemm_w4(q, s, z, group, xb.cuda(), y, off)
+    for e in range(E):
+        a, b = int(off[e]), int(off[e + 1])
+        w = rc.decode_w4(q[e], s[e], z[e], group)
+        assert torch.equal(y[a:b].double(), x[a:b].cuda() @ w.T), e
