@@ -121,3 +121,63 @@ def test_w4_bf16_smallest_values(counts, group):
         a, b = int(off[e]), int(off[e + 1])
         w = rc.decode_w4(q[e], s[e], z[e], group)
         assert torch.equal(y[a:b].double(), x[a:b].cuda() @ w.T), e
+
+
+@pytest.mark.parametrize("ty", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("group", [128, 64, 32, 160])
+@pytest.mark.parametrize("counts", [FEW, MANY])
+def test_w4_zero_points_of_eight_bits(counts, group, ty):
+    """Zero points of 0 to 255: q - z is exact, and with whole numbers so are
+    the sums (below 255 * 3 * 1280 < 2^24)."""
+    report(f"w4 zero points up to 255 {ty} {counts} group {group}")
+    E, R, C = len(counts), 48, 1280
+    g = rc.gen(group + 2)
+    q = torch.randint(0, 256, (E, R, C // 2), generator=g, device="cuda", dtype=torch.uint8)
+    s = torch.ones(E, R, C // group, dtype=torch.float16, device="cuda")
+    z = torch.randint(0, 256, (E, R, C // group), generator=g, device="cuda", dtype=torch.uint8)
+    off, _ = rc.groups(counts, 0)
+    n = sum(counts)
+    x = torch.randint(-3, 4, (n, C), generator=g, device="cuda").to(rc.TYPES[ty])
+    y = torch.full((n, R), 0.5, device="cuda")
+    pm.pm_grouped_gemm_w4(q, s, z, group, x, y, off)
+    for e in range(E):
+        a, b = int(off[e]), int(off[e + 1])
+        w = rc.decode_w4(q[e], s[e], z[e], group)
+        assert torch.equal(y[a:b].double(), x[a:b].double() @ w.T), e
+
+
+@pytest.mark.parametrize("ty", ["f32", "f16", "bf16"])
+def test_w4_without_inputs_gives_zeros(ty):
+    report(f"w4 cols 0 {ty}")
+    for zeros in (False, True):
+        for n in (5, 100):
+            off = torch.tensor([0, 2, n], dtype=torch.int32, device="cuda")
+            q = torch.empty(2, 10, 0, dtype=torch.uint8, device="cuda")
+            s = torch.empty(2, 10, 0, dtype=torch.float16, device="cuda")
+            z = torch.empty(2, 10, 0, dtype=torch.uint8, device="cuda") if zeros else None
+            x = torch.empty(n, 0, dtype=rc.TYPES[ty], device="cuda")
+            for flags, out in ((0, 10), (SWIGLU, 5)):
+                y = torch.full((n, out), 3.0, device="cuda")
+                pm.pm_grouped_gemm_w4(q, s, z, 32, x, y, off, None, 1, flags)
+                assert not y.any()
+
+
+@pytest.mark.parametrize("ty", ["f32", "bf16"])
+def test_w4_offsets_beyond_32_bits(ty):
+    """Rows of x whose byte offsets pass 2^32, in calls of few and of many rows
+    (which then take the streamed kernel)."""
+    report(f"w4 offsets beyond 32 bits {ty}")
+    C, R, group, ld = 192, 48, 64, 1 << 30
+    x = torch.empty(2 * ld + C, dtype=rc.TYPES[ty], device="cuda").as_strided((3, C), (ld, 1))
+    x.copy_(torch.randn(3, C, generator=rc.gen(1), device="cuda"))
+    g = rc.gen(2)
+    q = torch.randint(0, 256, (2, R, C // 2), generator=g, device="cuda", dtype=torch.uint8)
+    s = (torch.rand(2, R, C // group, generator=g, device="cuda") * 0.02 + 0.001).half()
+    for counts, top_k in (([3, 3], 2), ([400, 300], 234)):
+        off, order = rc.groups(counts, 3)
+        n = sum(counts)
+        y = torch.full((n, R), 3.0, device="cuda")
+        pm.pm_grouped_gemm_w4(q, s, None, group, x, y, off, order, top_k, GATHER | SCATTER)
+        want = rc.grouped_plain(lambda e: rc.decode_w4(q[e], s[e], None, group), x, off, order, n,
+                                top_k, True, True, False)
+        rc.check_grouped(y, 3.0, want, f"{n} rows")
