@@ -15,13 +15,13 @@ struct RowRange {
     int row0, n;
 };
 
-// Sorted rows from offset a on, up to offset b.  Offsets are clamped to
-// 0..n_rows and taken to not decrease, so a bad value reads and writes nothing
-// out of bounds.
+// Sorted rows from offset a on, up to offset b.  Both are clamped to 0..n_rows
+// (their difference fits 32 bits then, whatever they hold) and taken to not
+// decrease, so a bad value reads and writes nothing out of bounds.
 __device__ inline RowRange row_range(const GroupedCall& C, int a, int b) {
     RowRange r;
     r.row0 = min(max(a, 0), C.n_rows);
-    r.n = max(min(b, C.n_rows) - r.row0, 0);
+    r.n = max(min(max(b, 0), C.n_rows) - r.row0, 0);
     return r;
 }
 

@@ -99,9 +99,8 @@ __device__ inline Eight load_eight(const GroupedCall& C, int e) {
 }
 // First row and rows of expert e + k of them, none from `end` on.
 __device__ inline RowRange range_of(const GroupedCall& C, const Eight& s, int e, int k, int end) {
-    RowRange r;
-    r.row0 = min(max(s.o[k], 0), C.n_rows);
-    r.n = e + k < end ? max(min(s.o[k + 1], C.n_rows) - r.row0, 0) : 0;
+    RowRange r = row_range(C, s.o[k], s.o[k + 1]);
+    if (e + k >= end) r.n = 0;
     return r;
 }
 

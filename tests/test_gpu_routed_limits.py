@@ -181,3 +181,61 @@ def test_w4_offsets_beyond_32_bits(ty):
         want = rc.grouped_plain(lambda e: rc.decode_w4(q[e], s[e], None, group), x, off, order, n,
                                 top_k, True, True, False)
         rc.check_grouped(y, 3.0, want, f"{n} rows")
+
+
+# ---------------------------------------------------------------- offsets that decrease
+def bad_offsets(E, n, seed):
+    """Lists of E + 1 offsets that decrease, repeat, are negative or pass n."""
+    rng = np.random.default_rng(seed)
+    lists = [rng.integers(-2 * n, 3 * n, E + 1) for _ in range(3)]
+    lists += [np.where(np.arange(E + 1) % 2, n, 0), np.full(E + 1, n), np.full(E + 1, -1),
+              np.arange(E, -1, -1) * n // E, np.full(E + 1, 2 ** 31 - 1),
+              np.where(np.arange(E + 1) % 2, 2 ** 31 - 1, -2 ** 31)]
+    return [torch.from_numpy(o.astype(np.int32)).cuda() for o in lists]
+
+
+# name, weights (16 bits, or the group), x, experts, rows, outputs, inputs
+KERNELS = [("streamed", 16, "bf16", 3, 7, 40, 2056), ("streamed", 16, "f16", 70, 90, 40, 4104),
+           ("128-row tiles", 16, "bf16", 3, 200, 258, 136),
+           ("256-row tiles", 16, "f16", 2, 2100, 16640, 64),
+           ("streamed", 128, "bf16", 3, 7, 40, 1280), ("streamed", 64, "f16", 70, 90, 40, 4160),
+           ("streamed", 128, "f32", 3, 7, 40, 1280), ("streamed", 96, "f32", 70, 90, 40, 4128),
+           ("tiles", 128, "bf16", 3, 200, 258, 256), ("tiles", 32, "f32", 3, 200, 258, 256)]
+
+
+@pytest.mark.parametrize("name,bits,ty,E,n,R,C", KERNELS)
+def test_grouped_offsets_that_decrease(name, bits, ty, E, n, R, C):
+    """Any offsets: rows of y outside the call's stay, no row of x outside it is
+    read (they are NaN here), and the next call is right."""
+    report(f"bad offsets: {name} {bits} {ty} {E} experts {n} rows {R} x {C}")
+    g = rc.gen(E + n)
+    dt = rc.TYPES[ty]
+    xbuf = torch.full((n + 600, C), float("nan"), dtype=dt, device="cuda")
+    x = xbuf[300:300 + n]
+    x.copy_(torch.randn(n, C, generator=g, device="cuda"))
+    ybuf = torch.full((n + 600, R), 3.0, device="cuda")
+    y = ybuf[300:300 + n]
+    order = torch.randperm(n, generator=g, device="cuda").to(torch.int32)
+    if bits == 16:
+        w = torch.empty(E, R, C, dtype=dt, device="cuda").normal_(0, 0.05, generator=g)
+
+        def call(off):
+            pm.pm_grouped_gemm(w, x, y, off, order, 1, SCATTER)
+    else:
+        q = torch.randint(0, 256, (E, R, C // 2), generator=g, device="cuda", dtype=torch.uint8)
+        s = (torch.rand(E, R, C // bits, generator=g, device="cuda") * 0.02 + 0.001).half()
+        z = torch.randint(0, 16, (E, R, C // bits), generator=g, device="cuda", dtype=torch.uint8)
+
+        def call(off):
+            pm.pm_grouped_gemm_w4(q, s, z, bits, x, y, off, order, 1, SCATTER)
+    good = torch.linspace(0, n, E + 1).int().cuda()
+    call(good)
+    want = y.clone()
+    assert torch.isfinite(want).all()
+    for off in bad_offsets(E, n, n):
+        call(off)
+        assert torch.isfinite(y).all(), off.tolist()[:8]
+        assert torch.all(ybuf[:300] == 3.0) and torch.all(ybuf[300 + n:] == 3.0), off.tolist()[:8]
+    y.fill_(3.0)
+    call(good)
+    assert torch.equal(y, want)
