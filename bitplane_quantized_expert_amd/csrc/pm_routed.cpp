@@ -182,9 +182,20 @@ static pm_status check_grouped(pm_grouped_shape s, pm_grouped_rows r, const void
     if (!aligned(d_y, type_bytes(y_type)) || !aligned(r.d_offsets, 4) || !aligned(r.d_order, 4))
         return failf(PM_ERR_ARG, "grouped: misaligned device pointer");
     const size_t nx = flags & PM_GROUPED_GATHER ? size_t(r.n_rows - 1) / r.top_k + 1 : r.n_rows;
-    if (overlap(d_x, span(nx, ldx, s.cols, x_type), d_y, span(r.n_rows, ldy, out, y_type)))
+    const size_t ny = span(r.n_rows, ldy, out, y_type);
+    if (overlap(d_x, span(nx, ldx, s.cols, x_type), d_y, ny))
         return failf(PM_ERR_ARG, "grouped: x and y overlap");
+    if (overlap(r.d_offsets, 4 * (size_t(s.n_experts) + 1), d_y, ny) ||
+        (r.d_order && overlap(r.d_order, 4 * size_t(r.n_rows), d_y, ny)))
+        return failf(PM_ERR_ARG, "grouped: y overlaps the offsets or the order");
     return PM_OK;
+}
+
+// Whether y of a checked call overlaps `per_expert` bytes of weights at p.
+static bool in_weights(pm_grouped_shape s, pm_grouped_rows r, const void* p, size_t per_expert,
+                       const void* d_y, int y_type, int64_t ldy, uint32_t flags) {
+    const int out = flags & PM_GROUPED_SWIGLU ? s.rows / 2 : s.rows;
+    return p && overlap(p, per_expert * s.n_experts, d_y, span(r.n_rows, ldy, out, y_type));
 }
 
 static GroupedCall grouped_call(pm_grouped_shape s, pm_grouped_rows r, const void* d_x, int x_type,
@@ -219,6 +230,9 @@ extern "C" pm_status pm_grouped_gemm(pm_grouped_shape s, int type, const void* d
     if (r.n_rows == 0 || s.rows == 0) return PM_OK;
     if (s.cols > 0 && (!d_w || !aligned(d_w, 16)))
         return failf(PM_ERR_ARG, "grouped: weights null or not 16-byte aligned");
+    const size_t weights = size_t(s.rows) * s.cols;
+    if (in_weights(s, r, d_w, 2 * weights, d_y, y_type, ldy, flags))
+        return failf(PM_ERR_ARG, "grouped: y overlaps the weights");
     GroupedCall C = grouped_call(s, r, d_x, type, ldx, d_y, y_type, ldy, flags);
     C.w = d_w;
     C.w_type = type;
@@ -239,6 +253,11 @@ extern "C" pm_status pm_grouped_gemm_w4(pm_grouped_shape s, int group, const uin
     if (r.n_rows == 0 || s.rows == 0) return PM_OK;
     if (s.cols > 0 && (!d_q || !d_scales || !aligned(d_q, 16) || !aligned(d_scales, 2)))
         return failf(PM_ERR_ARG, "grouped: codes or scales null or misaligned");
+    const size_t weights = size_t(s.rows) * s.cols, groups = weights / group;
+    if (in_weights(s, r, d_q, weights / 2, d_y, y_type, ldy, flags) ||
+        in_weights(s, r, d_scales, 2 * groups, d_y, y_type, ldy, flags) ||
+        in_weights(s, r, d_zeros, groups, d_y, y_type, ldy, flags))
+        return failf(PM_ERR_ARG, "grouped: y overlaps the codes, scales or zero points");
     GroupedCall C = grouped_call(s, r, d_x, x_type, ldx, d_y, y_type, ldy, flags);
     C.w = d_q;
     C.scales = d_scales;

@@ -423,7 +423,7 @@ pm_status pm_route_topk_device(int n_tokens, int n_experts, int top_k, const voi
  *   An expert without rows is not read, and NaN in rows of x that no i maps
  *   to reach no output.
  * Alignment: weights, d_x and each row of x 16 bytes (ldx a multiple of 16
- * bytes), d_y its element.  x and y may not overlap (PM_ERR_ARG).  One
+ * bytes), d_y its element.  y may not overlap any input (PM_ERR_ARG).  One
  * matrix has fewer than 2^30 rows and weights (PM_ERR_SHAPE).  cols == 0 gives
  * zeros. */
 #define PM_GROUPED_MAX_EXPERTS 4096

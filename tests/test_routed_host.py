@@ -188,3 +188,24 @@ def test_binding_refuses_tensors_it_cannot_pass():
         pm.pm_combine_uses(f(4, 8), f(4), f(2, 8))
     with pytest.raises(ValueError, match="contiguous"):
         pm.pm_encode_w4_device(f(8, 64).t(), 32, f(8), f(8))
+
+
+@pytest.mark.parametrize("call", [gemm, w4])
+def test_grouped_outputs_over_other_inputs_are_refused(call):
+    """y in the offsets, the order or the weights would change them under the
+    running call."""
+    near = D + 8 * 64 * 4 - 4                        # the last element of y
+    for kw in ({"r": rows(off=D)}, {"r": rows(off=near, order=None)}, {"r": rows(order=D + 16)},
+               {"y": OFF}, {"y": ORD + 28, "r": rows()}, {"y": OFF + 16}, {"y": ORD - 64}):
+        refused(call(yt=pm.PM_F32, **kw), pm.PM_ERR_ARG, "offsets or the order")
+
+
+def test_grouped_outputs_over_weights_are_refused():
+    E, R, C, G = 4, 64, 128, 32
+    last = A + E * R * C * 2 - 2
+    refused(gemm(y=A), pm.PM_ERR_ARG, "overlaps the weights")
+    refused(gemm(y=last), pm.PM_ERR_ARG, "overlaps the weights")
+    S, Z = A + (1 << 34), A + (2 << 34)
+    for y in (A, A + E * R * C // 2 - 4, S, S + E * R * (C // G) * 2 - 4, Z,
+              Z + E * R * (C // G) - 4):
+        refused(w4(y=y, sc=S, z=Z), pm.PM_ERR_ARG, "overlaps the codes")
