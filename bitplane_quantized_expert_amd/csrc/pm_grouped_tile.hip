@@ -354,7 +354,8 @@ hipError_t run_tiles(const GroupedCall& C, hipStream_t st) {
     const int nt = (out + per - 1) / per;
     const size_t lds = tile_lds(C, BM, S);
     auto* f = tile_kernel<WT, YT, GLU, BM, S>;
-    hipError_t e = allow_lds(reinterpret_cast<const void*>(f), kTileMaxLds);
+    static std::atomic<uint64_t> allowed{0};
+    hipError_t e = allow_lds(reinterpret_cast<const void*>(f), kTileMaxLds, &allowed);
     if (e != hipSuccess) return e;
     const int64_t tiles = (int64_t(std::min(C.n_rows, C.n_experts)) + C.n_rows / BM) * nt;
     const unsigned grid = unsigned(std::min<int64_t>(tiles, compute_units()));

@@ -538,7 +538,8 @@ hipError_t run_tiles4(const GroupedCall& C, hipStream_t st) {
     const size_t lds =
         size_t(tile4_stages(X32)) * kStageBytes + (2 * kRows + C.n_experts + 1) * sizeof(int);
     auto* f = tile4_kernel<BF16, X32, GM, ZEROS>;
-    hipError_t e = allow_lds(reinterpret_cast<const void*>(f), kTileMaxLds);
+    static std::atomic<uint64_t> allowed{0};
+    hipError_t e = allow_lds(reinterpret_cast<const void*>(f), kTileMaxLds, &allowed);
     if (e != hipSuccess) return e;
     const int64_t tiles = (int64_t(std::min(C.n_rows, C.n_experts)) + C.n_rows / kRows) * nt;
     const unsigned grid = unsigned(std::min<int64_t>(tiles, compute_units()));

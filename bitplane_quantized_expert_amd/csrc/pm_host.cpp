@@ -10,7 +10,6 @@
 #include <cstring>
 #include <map>
 #include <mutex>
-#include <string>
 #include <vector>
 
 #include "pm_encoder.h"
@@ -21,15 +20,16 @@
 using namespace pm;
 
 // ---------------------------------------------------------------- errors
-static thread_local std::string g_last_error;
+// (a fixed buffer: reporting an error cannot throw)
+static thread_local char g_last_error[512] = "";
 
 pm_status pm::failf(pm_status st, const char* fmt, ...) {
-    char buf[512];
+    char buf[sizeof g_last_error] = "";
     va_list ap;
     va_start(ap, fmt);
     vsnprintf(buf, sizeof buf, fmt, ap);
     va_end(ap);
-    g_last_error = buf;
+    std::memcpy(g_last_error, buf, sizeof buf);
     return st;
 }
 
@@ -43,7 +43,7 @@ static pm_status hip_fail(hipError_t e, const char* what) {
         if (_e != hipSuccess) return hip_fail(_e, #expr);       \
     } while (0)
 
-extern "C" const char* pm_last_error(void) { return g_last_error.c_str(); }
+extern "C" const char* pm_last_error(void) { return g_last_error; }
 extern "C" const char* pm_version(void) { return "libpm 0.1 (gfx950)"; }
 
 // ---------------------------------------------------------------- shapes

@@ -1,11 +1,8 @@
 // Entry points of the routed experts on the device (include/pm.h): argument
-// checks and launches.  Nothing here allocates, copies or waits, so every
-// call can be captured into a HIP graph.
+// checks and launches.  Nothing here allocates (so nothing throws), copies or
+// waits, so every call can be captured into a HIP graph.
 #include <algorithm>
 #include <atomic>
-#include <mutex>
-#include <set>
-#include <utility>
 
 #include "pm_error.h"
 #include "pm_routed.h"
@@ -55,18 +52,15 @@ int pm::compute_units() {
     return n;
 }
 
-hipError_t pm::allow_lds(const void* kernel, int bytes) {
-    // never destroyed: no destructor of this library runs at process exit
-    static std::mutex& mu = *new std::mutex();
-    static std::set<std::pair<const void*, int>>& done =
-        *new std::set<std::pair<const void*, int>>();
+hipError_t pm::allow_lds(const void* kernel, int bytes, std::atomic<uint64_t>* done) {
     int dev = 0;
     hipError_t e = hipGetDevice(&dev);
     if (e != hipSuccess) return e;
-    std::lock_guard<std::mutex> lk(mu);
-    if (done.count({kernel, dev})) return hipSuccess;
+    const uint64_t bit = uint64_t(1) << (dev & (kMaxDevices - 1));
+    if (dev < kMaxDevices && (done->load(std::memory_order_relaxed) & bit)) return hipSuccess;
+    // (several threads may set the same value)
     e = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e == hipSuccess) done.insert({kernel, dev});
+    if (e == hipSuccess && dev < kMaxDevices) done->fetch_or(bit, std::memory_order_relaxed);
     return e;
 }
 

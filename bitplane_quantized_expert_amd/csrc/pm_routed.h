@@ -7,6 +7,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/pm.h"
 
 namespace pm {
@@ -66,9 +68,10 @@ hipError_t launch_grouped_stream4f(const GroupedCall& C, hipStream_t st);
 
 // Compute units of the current device.
 int compute_units();
-// Lets a kernel take up to `bytes` of dynamic LDS on the current device.
+// Lets a kernel take up to `bytes` of dynamic LDS on the current device; `done`
+// holds a bit for every device where it may, one word per kernel.
 constexpr int kTileMaxLds = 160 * 1024 - 1024;
-hipError_t allow_lds(const void* kernel, int bytes);
+hipError_t allow_lds(const void* kernel, int bytes, std::atomic<uint64_t>* done);
 
 // ---------------------------------------------------------------- 4-bit encoder, combine
 hipError_t launch_encode_w4(size_t n_groups, int group, const void* w, int type, uint8_t* q,

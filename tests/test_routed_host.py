@@ -1,12 +1,16 @@
 """Argument checks of the routed experts' device operators, without a GPU:
 every refusal happens before any HIP call, so made-up addresses are never
 used."""
+import concurrent.futures
 import ctypes
+import os
+import subprocess
 
 import pytest
 import torch
 
 import bitplane_quantized_expert_amd as pm
+from bitplane_quantized_expert_amd import build
 
 A = 1 << 40                   # made-up device addresses, far apart
 B = A + (1 << 36)
@@ -209,3 +213,26 @@ def test_grouped_outputs_over_weights_are_refused():
     for y in (A, A + E * R * C // 2 - 4, S, S + E * R * (C // G) * 2 - 4, Z,
               Z + E * R * (C // G) - 4):
         refused(w4(y=y, sc=S, z=Z), pm.PM_ERR_ARG, "overlaps the codes")
+
+
+ROUTED_SOURCES = [s for s in build.TARGETS[0][1] if "pm_rout" in s or "pm_grouped" in s or
+                  s.endswith("pm_combine.hip")]
+
+
+def test_entry_points_have_nothing_that_throws(tmp_path):
+    """The host code of the operators neither allocates nor locks: no C++
+    exception can leave a C entry point."""
+    assert len(ROUTED_SOURCES) == 9
+
+    def undefined(src):
+        obj = tmp_path / (os.path.basename(src) + ".o")
+        subprocess.run([build.hipcc(), *build.COMPILE_FLAGS, "--cuda-host-only", "-x", "hip", "-c",
+                        src, "-o", str(obj)], check=True, capture_output=True)
+        return subprocess.run(["nm", "-u", str(obj)], check=True, capture_output=True,
+                              text=True).stdout
+    with concurrent.futures.ThreadPoolExecutor(4) as ex:
+        for src, names in zip(ROUTED_SOURCES, ex.map(undefined, ROUTED_SOURCES)):
+            assert "hipLaunchKernel" in names or src.endswith(("pm_routed.cpp", "pm_grouped.hip"))
+            for bad in ("_Znw", "_Zna", "__cxa_throw", "__cxa_allocate_exception", "_ZSt", "malloc",
+                        "pthread_mutex"):
+                assert bad not in names, (src, bad, names)
