@@ -341,9 +341,12 @@ def pm_allocate_bits(ids, w, err_profiles, budget):
 
 
 # ---------------------------------------------------------------- routed experts on the device
-# These take torch tensors only: types, sizes and strides come from them.  A
-# decode step's kernel takes 3 to 10 us, so the checks of the calls that a step
-# makes are written out in line, each property of a tensor read once.
+# These take torch tensors only: types, sizes and strides come from them.
+# `stream` is a torch stream or a raw handle; None is the null stream, as in
+# every call of this module, not torch's current stream: inside
+# `with torch.cuda.stream(s)` or a capture, pass s.  A decode step's kernel
+# takes 3 to 10 us, so the checks of the calls that a step makes are written out
+# in line, each property of a tensor read once.
 _types = {}
 _int32 = _uint8 = None
 
@@ -391,7 +394,8 @@ def pm_route_topk_device(d_logits, top_k, d_ids, d_w, d_offsets=None, d_order=No
     """d_logits [n_tokens][n_experts] (float32, float16 or bfloat16, any row
     distance) -> d_ids int32, d_w float32 [n_tokens][top_k], and the uses
     sorted by expert: d_offsets int32 [n_experts + 1], d_order int32
-    [n_tokens * top_k], with d_ws of pm_route_workspace_bytes bytes."""
+    [n_tokens * top_k], with d_ws of pm_route_workspace_bytes bytes.  stream=None
+    is the null stream, not torch's current one."""
     shape, strides = d_logits.shape, d_logits.stride()
     if len(shape) != 2 or (shape[1] > 1 and strides[1] != 1):
         raise ValueError(f"logits: rows of adjacent elements, not {tuple(shape)} with strides "
@@ -467,7 +471,8 @@ def _grouped_args(dev, d_w, n_experts, rows, cols, d_x, d_y, d_offsets, d_order,
 
 def pm_grouped_gemm(d_w, d_x, d_y, d_offsets, d_order=None, top_k=1, flags=0, stream=None):
     """d_w [n_experts][rows][cols] float16 or bfloat16, contiguous; d_x rows
-    of cols of the same type; d_y rows of that type or float32."""
+    of cols of the same type; d_y rows of that type or float32.  stream=None is
+    the null stream, not torch's current one."""
     shape = d_w.shape
     if len(shape) != 3 or not d_w.is_contiguous():
         raise ValueError("w: contiguous [n_experts][rows][cols]")
@@ -486,7 +491,7 @@ def pm_grouped_gemm_w4(d_q, d_scales, d_zeros, group, d_x, d_y, d_offsets, d_ord
                        top_k=1, flags=0, stream=None):
     """d_q uint8 [n_experts][rows][cols/2], d_scales float16 and d_zeros uint8
     (or None) [n_experts][rows][cols/group]; d_x rows of cols, d_y rows of x's
-    type or float32."""
+    type or float32.  stream=None is the null stream, not torch's current one."""
     shape = d_q.shape
     if len(shape) != 3:
         raise ValueError("q: contiguous uint8 [n_experts][rows][cols/2]")
@@ -519,7 +524,8 @@ def pm_grouped_gemm_w4(d_q, d_scales, d_zeros, group, d_x, d_y, d_offsets, d_ord
 
 def pm_encode_w4_device(d_w, group, d_q, d_scales, d_zeros=None, stream=None):
     """d_w [rows][cols] (contiguous) -> d_q uint8 [rows][cols/2], d_scales
-    float16 and, for an asymmetric code, d_zeros uint8 [rows][cols/group]."""
+    float16 and, for an asymmetric code, d_zeros uint8 [rows][cols/group].
+    stream=None is the null stream, not torch's current one."""
     if d_w.dim() != 2 or not d_w.is_contiguous():
         raise ValueError("w: contiguous [rows][cols]")
     rows, cols = d_w.shape
@@ -543,7 +549,8 @@ def pm_encode_w4_device(d_w, group, d_q, d_scales, d_zeros=None, stream=None):
 
 def pm_combine_uses(d_z, d_w, d_y, stream=None):
     """d_y[t] = sum_j d_w[t][j] * d_z[t * top_k + j]: d_w float32
-    [n_tokens][top_k], d_z rows of hidden, d_y rows of z's type or float32."""
+    [n_tokens][top_k], d_z rows of hidden, d_y rows of z's type or float32.
+    stream=None is the null stream, not torch's current one."""
     shape, zs, ys, ldz, ldy = d_w.shape, d_z.shape, d_y.shape, d_z.stride(), d_y.stride()
     if len(shape) != 2 or len(zs) != 2 or len(ys) != 2:
         raise ValueError("z, w and y are 2-D")

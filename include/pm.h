@@ -373,23 +373,26 @@ pm_status pm_moe_token_forward(pm_store* s, int layer, int n_tokens, int top_k,
  * pm_grouped_gemm_w4 takes the place of pm_grouped_gemm for 4-bit experts.
  * Sums run in fp32 in a fixed order (no atomics); each output is rounded
  * once, to nearest even, to its type.  A call has at most PM_ROUTED_MAX_USES
- * uses (else PM_ERR_ARG).  Element types: */
+ * uses (else PM_ERR_ARG).  Calls are ordered by `stream` alone (null: the null
+ * stream).  Element types: */
 #define PM_ROUTED_MAX_USES 0x7FFF0000
 enum { PM_F32 = 0, PM_F16 = 1, PM_BF16 = 2 };
 
-/* Router [T c4], the selection of pm_route_topk on the device.
+/* Router [T c4]: of finite logits the selection of pm_route_topk, on the device.
  *   d_logits [n_tokens] rows of n_experts values of logits_type, ld apart
  *   (in elements, >= n_experts).
  *   d_ids int32, d_w fp32 [n_tokens][top_k]: largest logit first, ties to the
  *   lower id; softmax over the selected, in fp64, rounded to fp32.
- * A logit that is -inf or NaN is never selected: a token with fewer than
- * top_k others has id -1 and weight 0 in its last slots, and one with none
- * (padding) is routed nowhere.  Several +inf share the weight equally.
+ * Others differ from it (values on the device cannot be refused, and rows are
+ * padded with -inf): a logit that is -inf or NaN is never selected, where
+ * pm_route_topk refuses NaN and takes -inf.  A token with fewer than top_k
+ * others has id -1 and weight 0 in its last slots, and one with none (padding)
+ * is routed nowhere.  Several +inf share the weight equally.
  *   d_offsets int32 [n_experts + 1], d_order int32 [n_tokens * top_k], both
  *   null (no sorting) or neither (d_order may be null without tokens): the
  *   uses of expert e are d_order[d_offsets[e] .. d_offsets[e+1]), in ascending
- *   order.  Entries of d_order from
- *   d_offsets[n_experts] on are left as they were.
+ *   order.  Entries of d_order from d_offsets[n_experts] on are left as they
+ *   were.
  *   d_ws: pm_route_workspace_bytes(...) bytes of workspace, 16-byte aligned
  *   (null when that is 0 or d_order is null); its contents need not be kept
  *   or cleared, and calls that may overlap need one each.
@@ -413,11 +416,12 @@ pm_status pm_route_topk_device(int n_tokens, int n_experts, int top_k, const voi
  * gate and the others the up matrix, y has rows/2 columns and
  *     y[yr] = SiLU(p[0 .. rows/2)) * p[rows/2 .. rows),  SiLU(g) = g / (1 + e^-g).
  *   s.n_experts in 1 .. PM_GROUPED_MAX_EXPERTS (else PM_ERR_SHAPE); n_rows is
- *   the number of entries of d_order, at least d_offsets[n_experts]; d_offsets[0] = 0 and they do not decrease (other
- *   offsets read and write nothing out of bounds, but give unspecified
- *   rows).  Rows of y that no i maps to are left as they were, and an
- *   i whose u is outside 0 .. n_rows-1 is left out.  A u that occurs twice under
- *   PM_GROUPED_SCATTER leaves one of its results in each element.
+ *   the number of entries of d_order, at least d_offsets[n_experts];
+ *   d_offsets[0] = 0 and they do not decrease (other offsets read and write
+ *   nothing out of bounds, but give unspecified rows).  Rows of y that no i
+ *   maps to are left as they were, and an i whose u is outside 0 .. n_rows-1
+ *   is left out.  A u that occurs twice under PM_GROUPED_SCATTER leaves one of
+ *   its results in each element.
  *   d_x: rows ldx elements apart, (n_rows - 1) / top_k + 1 of them under
  *   PM_GROUPED_GATHER, else n_rows.  d_y: n_rows rows, ldy elements apart.
  *   An expert without rows is not read, and NaN in rows of x that no i maps
@@ -447,9 +451,11 @@ pm_status pm_grouped_gemm(pm_grouped_shape s, int type, const void* d_w, pm_grou
  *   group % 32 == 0, cols % group == 0 (PM_ERR_SHAPE).
  * x and y are fp32, fp16 or bf16, y fp32 or of x's type.  The products take
  * fp16 values (bf16 ones where a group has many rows): x in fp16 enters as it
- * is, bf16 and fp32 times a power of two per row and share of 128 to 512 inputs.  What bf16 loses thereby is at most
- * 2^-39 of the share's largest; fp32 enters as the sum of two halves, off by
- * at most 2^-23 of its value or 2^-50 of the share's largest. */
+ * is, bf16 and fp32 times a power of two per row and share of 128 to 512
+ * inputs.  What bf16 loses thereby is at most 2^-39 of the share's largest;
+ * fp32 enters as the sum of two halves, off by at most 2^-23 of its value or
+ * 2^-50 of the share's largest: inputs some 2^27 below the largest lose
+ * relative accuracy, which shows where the largest meets weights of 0. */
 pm_status pm_grouped_gemm_w4(pm_grouped_shape s, int group, const uint8_t* d_q,
                              const uint16_t* d_scales, const uint8_t* d_zeros,
                              pm_grouped_rows r, const void* d_x, int x_type, int64_t ldx,
