@@ -79,8 +79,11 @@ __global__ __launch_bounds__(256) void combine_uses_kernel(int n_tokens, int top
     }
 }
 
-// Offline: bound by reading the weights twice, by one thread per group of
-// inputs of one row, so that no sum or maximum crosses threads.
+// Offline, and simple: one thread per group of inputs of one row, so that no sum
+// or maximum crosses threads.  Neighbouring lanes read a group apart, one element
+// at a time, and a cache line is fetched again for most of its elements: 65536 x
+// 4096 bf16 weights take 10 ms in groups of 128 (61 GB fetched for 0.54) and 1.2
+// in groups of 32, fp32 ones 10 ms in both, where the bytes need 0.1 to 0.2.
 template <int TYPE>
 __global__ __launch_bounds__(256) void encode_w4_kernel(size_t n_groups, int group, const void* w,
                                                         uint8_t* q, uint16_t* scales,
@@ -142,7 +145,9 @@ static hipError_t combine_typed(int n_tokens, int top_k, int hidden, const void*
     const int per_wave = kWave * (ZT == PM_F32 ? 4 : 8);
     const int chunks = hidden / per_wave + (hidden % per_wave != 0);
     const dim3 grid(unsigned(std::min<int64_t>((int64_t(n_tokens) * chunks + 3) / 4, 1 << 20)));
-    // all rows of a token together where they are 10 at most
+    // all rows of a token together where they are 10 at most: 8 fp32 tokens of
+    // top-10 3.2 us against 3.7 with 8 rows at a time, 512 bf16 tokens 10.7
+    // against 11.3, from some thousands on equal within 1 %
     auto* f = &combine_uses_kernel<ZT, YT, 8>;
     if (top_k <= 2) f = &combine_uses_kernel<ZT, YT, 2>;
     else if (top_k <= 4) f = &combine_uses_kernel<ZT, YT, 4>;

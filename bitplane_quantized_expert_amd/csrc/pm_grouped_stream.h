@@ -37,11 +37,19 @@
 // rounded again: off by 2^-23 of the value, or 2^-50 of the largest.  The waves convert a few columns at a time into LDS and
 // take their operands from there.
 //
-// Measured: 80 rows over 512 experts, 2048 x 4096 fp16 with gate and up: 212 to
-// 230 us, 5.4 to 5.9 TB/s (a large copy reaches 4.8).  4-bit: 640 rows over 512
-// experts, 4096 x 1024 with zero points, bf16: 163 to 170 us, 4.9 TB/s; 10 rows
-// of fp32, 2048 x 4096 with gate and up: 20 us for 43 MB, of which the stream
-// takes 9 and finding the groups, converting x and the last sums the rest.
+// Measured: 80 rows over 512 experts, 2048 x 4096 fp16 with gate and up: 218 to
+// 230 us, 5.4 to 5.7 TB/s (of 6.2 that a plain elementwise kernel reaches).  4-bit:
+// 640 rows over 512 experts, 4096 x 1024 with zero points, bf16: 164 to 170 us,
+// 4.9 TB/s; 10 rows of fp32, 2048 x 4096 with gate and up: 20 us for 43 MB, of
+// which the stream takes 9 (a fifth more than equal shares: 128 row tiles of a
+// group over 25 workgroups are up to 6 each, 5.1 on average) and finding the
+// groups, converting x and the last sums the rest.
+// More than 4096 inputs take panels, and x is loaded (4-bit: converted) anew for
+// every 4 row tiles of a wave.  256 experts, 2048 outputs, top-8, bf16, at 4096,
+// 5120, 7168, 8192 inputs: 8 tokens 178, 290, 348, 351 us (5.4, 4.2, 4.8, 5.5 TB/s),
+// 64 tokens 616, 1075, 1313, 1297; 4-bit 60, 132, 140, 146 (4.1, 2.4, 3.1, 3.4) and
+// 190, 637, 661, 685; 4-bit with fp32 x 61, 146, 154, 161 and 203, 758, 777, 807.
+// (5120 and 7168 inputs fill two panels of 4096 only in part.)
 // The decoding, repeated for every 16 columns, bounds 4-bit calls of more rows:
 // 64 experts of 4096 x 4096 with 32, 64, 128 bf16 rows each take 261, 500, 997
 // us here, which is why tiles take over from some 16 rows on.

@@ -32,13 +32,13 @@
 // bound the call, and the third stage covers more of memory's latency.
 //
 // Measured: 65536 rows over 32 uneven experts, 2048 x 4096 bf16 with gate and
-// up: 900 to 930 us, 1.2 PFLOP/s, the matrix cores 68 % busy (a large library
-// product reaches 1.4 at these sizes; with all stages served by L2 this kernel
+// up: 930 to 940 us, 1.2 PFLOP/s, the matrix cores 67 % busy (a large library
+// product reaches 1.5 at these sizes; with all stages served by L2 this kernel
 // reached 1.35).  Two stages without the half-stage pipeline gave 0.99 PFLOP/s,
 // stages of 32 inputs 1.05 to 1.18, two workgroups of 128 x 256 per compute
 // unit 0.97, four waves of 128 x 128 1.13.  128-row tiles: 40960 rows over 512
-// experts, 4096 x 1024: 910 to 950 us, 5.0 TB/s; 1998 rows over 40 experts,
-// 1426 x 1000 with gate and up: 28 us, 4.3 TB/s.
+// experts, 4096 x 1024: 935 us, 5.0 TB/s; 1998 rows over 40 experts, 1426 x 1000
+// with gate and up: 35 us, 3.4 TB/s (28 where the 116 MB stay in the last cache).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>

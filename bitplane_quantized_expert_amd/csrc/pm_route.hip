@@ -5,10 +5,9 @@
 // that orders like it.  The top_k-th largest of the 64 lanes' own maxima, found
 // bit by bit with ballots, is a bound that the whole top-k meets and few other
 // logits do (two or three of 512); those that meet it are inserted one by one
-// into a list that lies sorted across the lanes.  About 170 vector
-// instructions for top-10 of 512, against 350 for ten rounds of a wave maximum
-// with removal.  The softmax (fp64) of up to 4 tokens is taken together, 16
-// lanes each.
+// into a list that lies sorted across the lanes: about half the vector
+// instructions of ten rounds of a wave maximum with removal, for top-10 of 512.
+// The softmax (fp64) of up to 4 tokens is taken together, 16 lanes each.
 //
 // Sorting: calls of few tokens do it in the same launch, in LDS.  Larger
 // ones leave, per block of tokens, how many uses every expert got, and
@@ -19,9 +18,12 @@
 //
 // Measured (kernel time): 1 token, 512 experts, top-10: 5.6 us in one launch,
 // bound by the chain of dependent steps of one wave.  1003 tokens, 60 experts,
-// top-4: 4.8 + 6.0 us.  16384 tokens, 512 experts, top-10: 15.5 us (33.6 MB of
-// logits, 2.2 TB/s; the selection's instructions bound it) + 11.1 us of sorting,
-// of which adding up the table's columns in every workgroup is the most.
+// top-4: 4.9 + 6.1 us.  16384 tokens, 512 experts, top-10: 16.1 us (33.6 MB of
+// logits, 2.1 TB/s) + 11.5 us of sorting, of which adding up the table's columns
+// in every workgroup is the most.  The selection takes 259 vector and 212 scalar
+// instructions per token (loads and softmax among them): the vector units are
+// busy half of the time, and the waves, 4 on a SIMD, wait for 56 % of theirs, for
+// the ballots and insertions of a token follow from one another.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
