@@ -123,6 +123,42 @@ def test_w4_bf16_smallest_values(counts, group):
         assert torch.equal(y[a:b].double(), x[a:b].cuda() @ w.T), e
 
 
+@pytest.mark.parametrize("group", [128, 64, 32, 160])
+@pytest.mark.parametrize("counts", [FEW, MANY])
+def test_w4_fp32_rows_of_any_size(counts, group):
+    """fp32 activations up to the type's largest value, and one-hot rows down to
+    its smallest (exact: a value of one bit is one half)."""
+    report(f"w4 fp32 up to its largest value {counts} group {group}")
+    E, R, C = len(counts), 48, 1280
+    g = rc.gen(group + 3)
+    q = torch.randint(0, 256, (E, R, C // 2), generator=g, device="cuda", dtype=torch.uint8)
+    s = (torch.randint(1, 17, (E, R, C // group), generator=g, device="cuda") * 2.0 ** -24).half()
+    z = torch.randint(0, 256, (E, R, C // group), generator=g, device="cuda", dtype=torch.uint8)
+    off, _ = rc.groups(counts, 0)
+    n = sum(counts)
+    x = torch.randn(n, C, generator=g, device="cuda")
+    x[0] *= 1e37
+    x[1] = torch.finfo(torch.float32).max
+    x[2] = torch.finfo(torch.float32).max * x[2].sign()
+    x[4, ::3] *= 1e37
+    x[n - 1] *= 1e30
+    want = rc.grouped_plain(lambda e: rc.decode_w4(q[e], s[e], z[e], group), x, off, None, n, 1,
+                            False, False, False)
+    y = torch.full((n, R), 3.0, device="cuda")
+    pm.pm_grouped_gemm_w4(q, s, z, group, x, y, off)
+    rc.check_grouped(y, 3.0, want, "large")
+    s = torch.exp2(torch.randint(0, 11, (E, R, C // group), generator=g, device="cuda").float()).half()
+    values = torch.tensor([2.0 ** -149, -2.0 ** -140, 2.0 ** -126, -2.0 ** -100, 2.0 ** 100],
+                          dtype=torch.float64)
+    x = torch.zeros(n, C, dtype=torch.float64)
+    x[torch.arange(n), torch.arange(n) * 97 % C] = values[torch.arange(n) % len(values)]
+    pm.pm_grouped_gemm_w4(q, s, z, group, x.float().cuda(), y, off)
+    for e in range(E):
+        a, b = int(off[e]), int(off[e + 1])
+        w = rc.decode_w4(q[e], s[e], z[e], group)
+        assert torch.equal(y[a:b].double(), x[a:b].cuda() @ w.T), e
+
+
 @pytest.mark.parametrize("ty", ["f32", "f16", "bf16"])
 @pytest.mark.parametrize("group", [128, 64, 32, 160])
 @pytest.mark.parametrize("counts", [FEW, MANY])
@@ -239,3 +275,94 @@ def test_grouped_offsets_that_decrease(name, bits, ty, E, n, R, C):
     y.fill_(3.0)
     call(good)
     assert torch.equal(y, want)
+
+
+# ---------------------------------------------------------------- most experts, far rows
+@pytest.mark.parametrize("bits,ty,C", [(16, "bf16", 2056), (16, "bf16", 64), (128, "f32", 1280),
+                                       (128, "bf16", 1280), (64, "f16", 128)])
+@pytest.mark.parametrize("many", [False, True])
+def test_grouped_most_experts(bits, ty, C, many):
+    """4096 experts, nearly all of them empty, the first and last not."""
+    E, R = 4096, 18
+    report(f"grouped 4096 experts {bits} {ty} cols {C} many {many}")
+    g = rc.gen(C)
+    dt = rc.TYPES[ty]
+    counts = np.zeros(E, np.int64)
+    counts[[0, 1, 7, 8, 63, 64, 65, 511, 2047, 2048, 4094, 4095]] = [1, 2, 9, 3, 1, 17, 2, 1, 1, 20, 5, 1]
+    if many:
+        counts[[3, 4093]] = [40000, 30000]
+    off, order = rc.groups(counts, 1)
+    n = int(counts.sum())
+    x = torch.randn(n, C, generator=g, device="cuda").to(dt)
+    y = torch.full((n, R), 3.0, device="cuda")
+    if bits == 16:
+        w = torch.empty(E, R, C, dtype=dt, device="cuda").normal_(0, 0.05, generator=g)
+        pm.pm_grouped_gemm(w, x, y, off, order, 1, SCATTER)
+
+        def w64(e):
+            return w[e].double()
+    else:
+        q = torch.randint(0, 256, (E, R, C // 2), generator=g, device="cuda", dtype=torch.uint8)
+        s = (torch.rand(E, R, C // bits, generator=g, device="cuda") * 0.02 + 0.001).half()
+        pm.pm_grouped_gemm_w4(q, s, None, bits, x, y, off, order, 1, SCATTER)
+
+        def w64(e):
+            return rc.decode_w4(q[e], s[e], None, bits)
+    rc.check_grouped(y, 3.0, rc.grouped_plain(w64, x, off, order, n, 1, False, True, False))
+
+
+def test_rows_far_apart():
+    """Router and combine on rows whose byte offsets pass 2^32."""
+    report("router and combine beyond 32 bits")
+    ld = 1 << 30
+    buf = torch.empty(4 * ld + 64, dtype=torch.bfloat16, device="cuda")
+    l = buf.as_strided((5, 64), (ld, 1))
+    l.copy_(torch.randn(5, 64, generator=rc.gen(1), device="cuda"))
+    ids = torch.empty(5, 3, dtype=torch.int32, device="cuda")
+    w = torch.empty(5, 3, device="cuda")
+    off = torch.empty(65, dtype=torch.int32, device="cuda")
+    order = torch.empty(15, dtype=torch.int32, device="cuda")
+    ws = torch.empty(pm.pm_route_workspace_bytes(5, 64, 3), dtype=torch.uint8, device="cuda")
+    pm.pm_route_topk_device(l, 3, ids, w, off, order, ws)
+    wi, _, woff, word = rc.route_plain(l, 3)
+    assert np.array_equal(ids.cpu().numpy(), wi)
+    assert np.array_equal(off.cpu().numpy(), woff) and np.array_equal(order.cpu().numpy(), word)
+    z = buf.as_strided((4, 40), (ld, 1))
+    yb = torch.empty(ld + 40, dtype=torch.bfloat16, device="cuda")
+    y = yb.as_strided((2, 40), (ld, 1))
+    pm.pm_combine_uses(z, torch.tensor([[1.0, 0.0], [0.0, 0.5]], device="cuda"), y)
+    assert torch.equal(y[0], z[0]) and torch.equal(y[1], z[3] * 0.5)
+
+
+@pytest.mark.parametrize("K", [63, 65, 130])
+@pytest.mark.parametrize("H", [3, 40])
+def test_combine_of_many_slots(K, H):
+    """More slots than a wave has lanes, whole numbers: exact."""
+    report(f"combine top-{K} of {H} columns")
+    g = rc.gen(K)
+    z = torch.randint(-9, 10, (5 * K, H), generator=g, device="cuda").half()
+    w = torch.randint(-9, 10, (5, K), generator=g, device="cuda").float()
+    y = torch.empty(5, H, device="cuda")
+    pm.pm_combine_uses(z, w, y)
+    assert torch.equal(y.double(), (w.double()[:, :, None] * z.double().reshape(5, K, H)).sum(1))
+
+
+@pytest.mark.parametrize("T,E", [(3, 64), (40, 64), (2, 70), (300, 64)])
+def test_route_takes_every_expert_of_64(T, E):
+    """top-64: the list of the selected fills the wave."""
+    report(f"route {T} x {E} top-64")
+    l = torch.randn(T, E, generator=rc.gen(T), device="cuda").mul_(3).round_()
+    l[0, 5] = -float("inf")
+    ids = torch.empty(T, 64, dtype=torch.int32, device="cuda")
+    w = torch.empty(T, 64, device="cuda")
+    off = torch.empty(E + 1, dtype=torch.int32, device="cuda")
+    order = torch.full((T * 64,), -7, dtype=torch.int32, device="cuda")
+    ws = torch.empty(pm.pm_route_workspace_bytes(T, E, 64), dtype=torch.uint8, device="cuda")
+    pm.pm_route_topk_device(l, 64, ids, w, off, order, ws)
+    wi, ww, woff, word = rc.route_plain(l, 64)
+    assert np.array_equal(ids.cpu().numpy(), wi)
+    # fp64 softmax rounded to fp32: half a step, and a little for the exponential
+    assert np.all(np.abs(w.cpu().numpy() - ww) <= 1.01 * 2.0 ** -24 * ww + 2.0 ** -149)
+    n = woff[-1]
+    assert np.array_equal(off.cpu().numpy(), woff)
+    assert np.array_equal(order.cpu().numpy()[:n], word) and np.all(order.cpu().numpy()[n:] == -7)
