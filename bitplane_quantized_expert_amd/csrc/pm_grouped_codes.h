@@ -1,5 +1,5 @@
-// Pieces that the streamed kernels and the 4-bit tiles share: matrix products,
-// 4-bit codes as halves, offsets beyond a buffer.  Internal linkage.
+// Pieces that the kernels of the grouped products share: matrix products, 4-bit
+// codes as halves, offsets beyond a buffer.  Internal linkage.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -13,9 +13,10 @@
 namespace pm {
 namespace {
 
-// An offset beyond any buffer (all are below 2 GiB), with any immediate added.
-constexpr uint32_t kNowhere = 0x80000000u;
-constexpr int kRawBuffer = 0x00020000;
+// An offset beyond any buffer of less than 2 GiB, with any immediate added, and
+// one beyond any buffer.
+constexpr uint32_t kNowhere = 0x80000000u, kOutside = 0xFFFFFFF0u;
+constexpr int kRawBuffer = 0x00020000;          // raw buffer, 32-bit data format
 // How scales are read and applied: groups of 32, 64 or 128 inputs in aligned
 // vectors, or (kAnyGroup) one by one for every 32 inputs.
 enum { kNoGroup = 0, kGroup32 = 32, kGroup64 = 64, kGroup128 = 128, kAnyGroup = 1 };

@@ -46,6 +46,7 @@
 
 #include "pm_convert.h"
 #include "pm_device.h"
+#include "pm_grouped_codes.h"
 #include "pm_grouped_rows.h"
 #include "pm_routed.h"
 
@@ -55,22 +56,8 @@ namespace {
 
 constexpr int kTileN = 256, kTileK = 64;
 constexpr int kTileThreads = 512, kTileWaves = 8;
-constexpr uint32_t kOutside = 0xFFFFFFF0u;      // an offset beyond any buffer
-constexpr int kBufferFlags = 0x00020000;        // raw buffer, 32-bit data format
 
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef __attribute__((address_space(3))) void lds_void;
-
-template <int WT>
-__device__ inline f32x4 mfma16(const u32x4& a, const u32x4& b, const f32x4& c) {
-    if constexpr (WT == PM_F16)
-        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a),
-                                                      __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
-    else
-        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
-                                                       __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
-}
 
 // BM rows by 256 weight rows, S stages of 64 inputs in LDS.
 template <int WT, int YT, bool GLU, int BM, int S>
@@ -174,13 +161,13 @@ __global__ __launch_bounds__(kTileThreads, 2) void tile_kernel(const GroupedCall
                                      C.cols) * 2;
         return __builtin_amdgcn_make_buffer_rsrc(
             uni_ptr(const_cast<char*>(p)), 0, uni(int(uint32_t(min(n, size_t(kOutside))))),
-            kBufferFlags);
+            kRawBuffer);
     };
     auto w_buffer = [&](const Where& w) {
         const char* p = static_cast<const char*>(C.w) + size_t(w.e) * wbytes;
         return __builtin_amdgcn_make_buffer_rsrc(uni_ptr(const_cast<char*>(p)), 0,
                                                  uni(w.n == 0 ? 0 : int(uint32_t(wbytes))),
-                                                 kBufferFlags);
+                                                 kRawBuffer);
     };
 
     // (stages past the last input hold zeros; a tile has at least S)
@@ -233,7 +220,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void tile_kernel(const GroupedCall
 #pragma unroll
         for (int i = 0; i < MB; ++i)
 #pragma unroll
-            for (int j = 0; j < NB; ++j) acc[i][j] = mfma16<WT>(fb[h][j], fa[h][i], acc[i][j]);
+            for (int j = 0; j < NB; ++j) acc[i][j] = mfma_x_w<WT == PM_BF16>(fb[h][j], fa[h][i], acc[i][j]);
     };
     read_half(0, 0);
 

@@ -53,7 +53,6 @@ constexpr int kThreads4 = 512;
 // Rows of x per tile, blocks held in LDS.
 constexpr int tile4_rows(bool x32) { return x32 ? 64 : 128; }
 constexpr int tile4_stages(bool x32) { return x32 ? 2 : 3; }
-constexpr uint32_t kOutside = 0xFFFFFFF0u;      // an offset beyond any buffer
 
 typedef __attribute__((address_space(3))) void lds_void;
 
