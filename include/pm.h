@@ -427,9 +427,9 @@ pm_status pm_route_topk_device(int n_tokens, int n_experts, int top_k, const voi
  *   An expert without rows is not read, and NaN in rows of x that no i maps
  *   to reach no output.
  * Alignment: weights, d_x and each row of x 16 bytes (ldx a multiple of 16
- * bytes), d_y its element.  y may not overlap any input (PM_ERR_ARG).  One
- * matrix has fewer than 2^30 rows and weights (PM_ERR_SHAPE).  cols == 0 gives
- * zeros. */
+ * bytes), d_y its element.  The bytes from y's first element to its last may
+ * not hold any of an input's (PM_ERR_ARG).  One matrix has fewer than 2^30 rows
+ * and weights (PM_ERR_SHAPE).  cols == 0 gives zeros. */
 #define PM_GROUPED_MAX_EXPERTS 4096
 typedef struct { int32_t n_experts, rows, cols; } pm_grouped_shape;
 typedef struct {
