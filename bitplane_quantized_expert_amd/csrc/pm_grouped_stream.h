@@ -38,7 +38,7 @@
 // take their operands from there.
 //
 // Measured: 80 rows over 512 experts, 2048 x 4096 fp16 with gate and up: 218 to
-// 230 us, 5.4 to 5.7 TB/s (of 6.2 that a plain elementwise kernel reaches).  4-bit:
+// 232 us, 5.4 to 5.7 TB/s (of 6.2 that a plain elementwise kernel reaches).  4-bit:
 // 640 rows over 512 experts, 4096 x 1024 with zero points, bf16: 164 to 170 us,
 // 4.9 TB/s; 10 rows of fp32, 2048 x 4096 with gate and up: 20 us for 43 MB, of
 // which the stream takes 9 (a fifth more than equal shares: 128 row tiles of a

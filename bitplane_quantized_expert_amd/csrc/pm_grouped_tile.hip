@@ -32,7 +32,7 @@
 // bound the call, and the third stage covers more of memory's latency.
 //
 // Measured: 65536 rows over 32 uneven experts, 2048 x 4096 bf16 with gate and
-// up: 930 to 940 us, 1.2 PFLOP/s, the matrix cores 67 % busy (a large library
+// up: 896 to 940 us, 1.2 PFLOP/s, the matrix cores 67 % busy (a large library
 // product reaches 1.5 at these sizes; with all stages served by L2 this kernel
 // reached 1.35).  Two stages without the half-stage pipeline gave 0.99 PFLOP/s,
 // stages of 32 inputs 1.05 to 1.18, two workgroups of 128 x 256 per compute
