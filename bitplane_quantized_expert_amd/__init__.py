@@ -44,6 +44,10 @@ PM_ROUTE_MAX_EXPERTS = 4096
 PM_ROUTE_MAX_TOPK = 64
 PM_GROUPED_MAX_EXPERTS = 4096
 PM_ROUTED_MAX_USES = 0x7FFF0000
+PM_ROUTE_MAX_GROUPS = 64
+PM_SCORE_SIGMOID = 0
+PM_SCORE_SOFTMAX = 1
+PM_ROUTE_RENORM = 1
 
 _STATUS = {0: "PM_OK", -1: "PM_ERR_ARG", -2: "PM_ERR_SHAPE", -3: "PM_ERR_PREFIX",
            -4: "PM_ERR_NOT_RESIDENT", -5: "PM_ERR_OOM", -6: "PM_ERR_HIP", -7: "PM_ERR_STATE"}
@@ -73,6 +77,17 @@ class pm_grouped_rows(ctypes.Structure):
                 ("d_offsets", ctypes.c_void_p), ("d_order", ctypes.c_void_p)]
 
 
+class pm_route_rule(ctypes.Structure):
+    """How pm_route_scored_device scores and chooses; made once per model."""
+    _fields_ = [("score", ctypes.c_int32), ("n_groups", ctypes.c_int32),
+                ("top_groups", ctypes.c_int32), ("group_best", ctypes.c_int32),
+                ("flags", ctypes.c_uint32), ("scale", ctypes.c_float)]
+
+    def __init__(self, score=PM_SCORE_SIGMOID, n_groups=1, top_groups=1, group_best=1, flags=0,
+                 scale=1.0):
+        super().__init__(score, n_groups, top_groups, group_best, flags, scale)
+
+
 _c = ctypes
 _P = ctypes.c_void_p
 _I = ctypes.c_int
@@ -82,6 +97,7 @@ _MS = pm_matrix_shape
 _ES = pm_expert_shape
 _GS = pm_grouped_shape
 _GR = pm_grouped_rows
+_RR = pm_route_rule
 _L = ctypes.c_int64
 
 # name -> (restype, argtypes)
@@ -129,8 +145,11 @@ SIGNATURES = {
     "pm_gemv_fp16_batch": (_I, [_I, _P, _P, _P, _P, _P]),
     "pm_route_workspace_bytes": (_Z, [_I, _I, _I]),
     "pm_route_topk_device": (_I, [_I, _I, _I, _P, _I, _L, _P, _P, _P, _P, _P, _Z, _P]),
+    "pm_route_scored_device": (_I, [_I, _I, _I, _RR, _P, _I, _L, _P, _P, _P, _P, _P, _P, _Z, _P]),
     "pm_grouped_gemm": (_I, [_GS, _I, _P, _GR, _P, _L, _P, _I, _L, _U32, _P]),
     "pm_grouped_gemm_w4": (_I, [_GS, _I, _P, _P, _P, _GR, _P, _I, _L, _P, _I, _L, _U32, _P]),
+    "pm_grouped_gemm_fp8": (_I, [_GS, _P, _P, _GR, _P, _P, _L, _P, _I, _L, _U32, _P]),
+    "pm_encode_fp8_device": (_I, [_I, _MS, _I, _P, _I, _L, _P, _L, _P, _P]),
     "pm_encode_w4_device": (_I, [_MS, _P, _I, _P, _P, _P, _P]),
     "pm_combine_uses": (_I, [_I, _I, _I, _P, _I, _L, _P, _P, _I, _L, _P]),
 }
@@ -348,16 +367,16 @@ def pm_allocate_bits(ids, w, err_profiles, budget):
 # takes 3 to 10 us, so the checks of the calls that a step makes are written out
 # in line, each property of a tensor read once.
 _types = {}
-_int32 = _uint8 = None
+_int32 = _uint8 = _e4m3 = None
 
 
 def _current_device():
     """The current HIP device, which the kernels run on (loads torch at the
     first call and puts its device query in place of this function)."""
-    global _current_device, _int32, _uint8
+    global _current_device, _int32, _uint8, _e4m3
     import torch
     _types.update({torch.float32: PM_F32, torch.float16: PM_F16, torch.bfloat16: PM_BF16})
-    _int32, _uint8 = torch.int32, torch.uint8
+    _int32, _uint8, _e4m3 = torch.int32, torch.uint8, torch.float8_e4m3fn
     _current_device = torch.cuda.current_device if torch.cuda.is_available() else lambda: -2
     return _current_device()
 
@@ -435,6 +454,59 @@ def pm_route_topk_device(d_logits, top_k, d_ids, d_w, d_offsets=None, d_order=No
     return _check(lib().pm_route_topk_device(
         n, e, top_k, d_logits.data_ptr(), t, strides[0] if n > 1 else e, d_ids.data_ptr(),
         d_w.data_ptr(), offsets, order, ws, ws_bytes, _stream(stream)))
+
+
+def pm_route_scored_device(rule, d_logits, d_bias, top_k, d_ids, d_w, d_offsets=None,
+                           d_order=None, d_ws=None, stream=None):
+    """rule a pm_route_rule; d_bias float32 [n_experts] or None; the others as in
+    pm_route_topk_device.  stream=None is the null stream, not torch's current
+    one."""
+    shape, strides = d_logits.shape, d_logits.stride()
+    if len(shape) != 2 or (shape[1] > 1 and strides[1] != 1):
+        raise ValueError(f"logits: rows of adjacent elements, not {tuple(shape)} with strides "
+                         f"{strides}")
+    n, e = shape
+    dev = _current_device()
+    if d_logits.get_device() != dev or d_ids.get_device() != dev or d_w.get_device() != dev or \
+            (d_offsets is not None and d_offsets.get_device() != dev) or \
+            (d_order is not None and d_order.get_device() != dev) or \
+            (d_ws is not None and d_ws.get_device() != dev) or \
+            (d_bias is not None and d_bias.get_device() != dev):
+        _on_device(d_logits, d_ids, d_w, d_offsets, d_order, d_ws, d_bias)
+    uses = n * top_k
+    t = _types.get(d_logits.dtype)
+    if t is None:
+        _bad_type(d_logits, "logits")
+    if d_ids.dtype is not _int32 or d_ids.numel() < uses or not d_ids.is_contiguous():
+        _bad_vec(d_ids, "int32", uses, "ids")
+    if _types.get(d_w.dtype) != PM_F32 or d_w.numel() < uses or not d_w.is_contiguous():
+        _bad_vec(d_w, "float32", uses, "w")
+    offsets = order = ws = bias = None
+    ws_bytes = 0
+    if d_offsets is not None:
+        if d_offsets.dtype is not _int32 or d_offsets.numel() <= e or \
+                not d_offsets.is_contiguous():
+            _bad_vec(d_offsets, "int32", e + 1, "offsets")
+        offsets = d_offsets.data_ptr()
+    if d_order is not None:
+        if d_order.dtype is not _int32 or d_order.numel() < uses or not d_order.is_contiguous():
+            _bad_vec(d_order, "int32", uses, "order")
+        order = d_order.data_ptr()
+    if d_ws is not None:
+        if not d_ws.is_contiguous():
+            raise ValueError("workspace: contiguous")
+        ws = d_ws.data_ptr()
+        ws_bytes = d_ws.nbytes
+    if d_bias is not None:
+        if _types.get(d_bias.dtype) != PM_F32 or d_bias.numel() != e or \
+                not d_bias.is_contiguous():
+            raise ValueError(f"bias: contiguous float32 of {e} elements, not {d_bias.numel()} of "
+                             f"{d_bias.dtype}")
+        bias = d_bias.data_ptr()
+    # (one row, or none, has no distance to the next)
+    return _check(lib().pm_route_scored_device(
+        n, e, top_k, rule, d_logits.data_ptr(), t, strides[0] if n > 1 else e, bias,
+        d_ids.data_ptr(), d_w.data_ptr(), offsets, order, ws, ws_bytes, _stream(stream)))
 
 
 def _grouped_args(dev, d_w, n_experts, rows, cols, d_x, d_y, d_offsets, d_order, top_k, flags):
@@ -520,6 +592,81 @@ def pm_grouped_gemm_w4(d_q, d_scales, d_zeros, group, d_x, d_y, d_offsets, d_ord
     return _check(lib().pm_grouped_gemm_w4(s, group, d_q.data_ptr(), d_scales.data_ptr(), zeros, r,
                                            d_x.data_ptr(), xt, ldx, d_y.data_ptr(), yt, ldy,
                                            flags, _stream(stream)))
+
+
+def pm_grouped_gemm_fp8(d_w, d_wscales, d_x, d_xscales, d_y, d_offsets, d_order=None, top_k=1,
+                        flags=0, stream=None):
+    """d_w [n_experts][rows][cols] and d_x rows of cols: float8_e4m3fn (or uint8
+    codes); d_wscales float32 [n_experts][ceil(rows/128)][ceil(cols/128)],
+    d_xscales float32 [rows of x][ceil(cols/128)], contiguous; d_y rows of
+    float32, float16 or bfloat16.  stream=None is the null stream, not torch's
+    current one."""
+    shape = d_w.shape
+    if len(shape) != 3 or not d_w.is_contiguous():
+        raise ValueError("w: contiguous [n_experts][rows][cols]")
+    e, rows, cols = shape
+    dev = _current_device()
+    wt, xt, yt = d_w.dtype, d_x.dtype, _types.get(d_y.dtype)
+    if (wt is not _e4m3 and wt is not _uint8) or (xt is not _e4m3 and xt is not _uint8):
+        raise ValueError(f"w and x: float8_e4m3fn or uint8, not {wt} and {xt}")
+    if yt is None:
+        _bad_type(d_y, "y")
+    s, r, ldx, ldy = _grouped_args(dev, d_w, e, rows, cols, d_x, d_y, d_offsets, d_order, top_k,
+                                   flags)
+    blocks = (cols + 127) // 128
+    nw = e * ((rows + 127) // 128) * blocks
+    nx = ((r.n_rows + top_k - 1) // top_k if flags & PM_GROUPED_GATHER else r.n_rows) * blocks
+    if _types.get(d_wscales.dtype) != PM_F32 or d_wscales.numel() < nw or \
+            not d_wscales.is_contiguous():
+        _bad_vec(d_wscales, "float32", nw, "scales of w")
+    if _types.get(d_xscales.dtype) != PM_F32 or d_xscales.numel() < nx or \
+            not d_xscales.is_contiguous():
+        _bad_vec(d_xscales, "float32", nx, "scales of x")
+    if d_wscales.get_device() != dev or d_xscales.get_device() != dev:
+        _on_device(d_w, d_wscales, d_xscales)
+    return _check(lib().pm_grouped_gemm_fp8(s, d_w.data_ptr(), d_wscales.data_ptr(), r,
+                                            d_x.data_ptr(), d_xscales.data_ptr(), ldx,
+                                            d_y.data_ptr(), yt, ldy, flags, _stream(stream)))
+
+
+def pm_encode_fp8_device(d_x, d_q, d_scales, block_rows=1, stream=None):
+    """d_x [rows][cols] or [n][rows][cols] (float32, float16 or bfloat16) -> d_q of
+    the same shape, float8_e4m3fn (or uint8 codes), and d_scales float32
+    [n][ceil(rows/block_rows)][ceil(cols/128)], contiguous; block_rows 1
+    (activations) or 128 (weights).  Rows of x and q may be further apart than
+    cols, the same distance throughout.  stream=None is the null stream, not
+    torch's current one."""
+    xs, qs, sx, sq = d_x.shape, d_q.shape, d_x.stride(), d_q.stride()
+    dev = _current_device()
+    if d_x.get_device() != dev or d_q.get_device() != dev or d_scales.get_device() != dev:
+        _on_device(d_x, d_q, d_scales)
+    t = _types.get(d_x.dtype)
+    if t is None:
+        _bad_type(d_x, "x")
+    if d_q.dtype is not _e4m3 and d_q.dtype is not _uint8:
+        raise ValueError(f"q: float8_e4m3fn or uint8, not {d_q.dtype}")
+    if len(xs) == 2:
+        n, (rows, cols) = 1, xs
+    elif len(xs) == 3:
+        n, rows, cols = xs
+    else:
+        raise ValueError("x: [rows][cols] or [n][rows][cols]")
+    if qs != xs:
+        raise ValueError(f"q of {tuple(qs)} for x of {tuple(xs)}")
+    # (one row, or none, has no distance to the next)
+    many = rows > 1
+    ldx, ldq = (sx[-2], sq[-2]) if many else (sx[0], sq[0]) if n > 1 else (cols, cols)
+    if cols > 1 and (sx[-1] != 1 or sq[-1] != 1) or \
+            (n > 1 and many and (sx[0] != rows * ldx or sq[0] != rows * ldq)):
+        raise ValueError(f"x and q: rows of adjacent elements at one distance, not strides {sx} "
+                         f"and {sq}")
+    n_scales = n * (-(-rows // block_rows) if block_rows > 0 else 0) * ((cols + 127) // 128)
+    if _types.get(d_scales.dtype) != PM_F32 or d_scales.numel() < n_scales or \
+            not d_scales.is_contiguous():
+        _bad_vec(d_scales, "float32", n_scales, "scales")
+    return _check(lib().pm_encode_fp8_device(n, pm_matrix_shape(rows, cols, 128), block_rows,
+                                             d_x.data_ptr(), t, ldx, d_q.data_ptr(), ldq,
+                                             d_scales.data_ptr(), _stream(stream)))
 
 
 def pm_encode_w4_device(d_w, group, d_q, d_scales, d_zeros=None, stream=None):

@@ -86,11 +86,11 @@ extern "C" size_t pm_route_workspace_bytes(int n_tokens, int n_experts, int top_
     return (size_t(nb) * ((n_experts + 7) & ~7) * sizeof(uint16_t) + 15) & ~size_t(15);
 }
 
-extern "C" pm_status pm_route_topk_device(int n_tokens, int n_experts, int top_k,
-                                          const void* d_logits, int logits_type, int64_t ld,
-                                          int32_t* d_ids, float* d_w, int32_t* d_offsets,
-                                          int32_t* d_order, void* d_ws, size_t ws_bytes,
-                                          void* stream) {
+// Checks of both routers, and the parts of the call that they share.
+static pm_status check_route(int n_tokens, int n_experts, int top_k, const void* d_logits,
+                             int logits_type, int64_t ld, const float* d_bias, int32_t* d_ids,
+                             float* d_w, int32_t* d_offsets, int32_t* d_order, void* d_ws,
+                             size_t ws_bytes, RouteCall* call) {
     if (n_tokens < 0 || n_experts < 1 || top_k < 1 || top_k > n_experts)
         return failf(PM_ERR_ARG, "route: n_tokens=%d n_experts=%d top_k=%d", n_tokens, n_experts,
                      top_k);
@@ -108,7 +108,8 @@ extern "C" pm_status pm_route_topk_device(int n_tokens, int n_experts, int top_k
     if (n_tokens > 0 && (!d_logits || !d_ids || !d_w))
         return failf(PM_ERR_ARG, "route: null device pointer");
     if (!aligned(d_logits, type_bytes(logits_type)) || !aligned(d_ids, 4) || !aligned(d_w, 4) ||
-        !aligned(d_offsets, 4) || !aligned(d_order, 4) || !aligned(d_ws, 16))
+        !aligned(d_offsets, 4) || !aligned(d_order, 4) || !aligned(d_ws, 16) ||
+        !aligned(d_bias, 4))
         return failf(PM_ERR_ARG, "route: misaligned device pointer");
     const size_t need = d_offsets ? pm_route_workspace_bytes(n_tokens, n_experts, top_k) : 0;
     if (need && (!d_ws || ws_bytes < need))
@@ -116,18 +117,20 @@ extern "C" pm_status pm_route_topk_device(int n_tokens, int n_experts, int top_k
                      need);
     const size_t uses = size_t(n_tokens) * top_k;
     const size_t in = span(size_t(n_tokens), ld, size_t(n_experts), logits_type);
+    const size_t in_bias = d_bias ? 4 * size_t(n_experts) : 0;
     const struct { const void* p; size_t n; } out[5] = {
         {d_ids, 4 * uses}, {d_w, 4 * uses}, {d_offsets, d_offsets ? 4 * (size_t(n_experts) + 1) : 0},
         {d_order, d_order ? 4 * uses : 0}, {d_ws, need}};
     for (int a = 0; a < 5; ++a) {
         if (overlap(out[a].p, out[a].n, d_logits, in))
             return failf(PM_ERR_ARG, "route: an output overlaps the logits");
+        if (overlap(out[a].p, out[a].n, d_bias, in_bias))
+            return failf(PM_ERR_ARG, "route: an output overlaps the bias");
         for (int b = 0; b < a; ++b)
             if (overlap(out[a].p, out[a].n, out[b].p, out[b].n))
                 return failf(PM_ERR_ARG, "route: outputs or workspace overlap");
     }
-    if (n_tokens == 0 && !d_offsets) return PM_OK;
-    RouteCall C{};
+    RouteCall& C = *call;
     C.logits = d_logits;
     C.ld = ld;
     C.ids = d_ids;
@@ -141,7 +144,52 @@ extern "C" pm_status pm_route_topk_device(int n_tokens, int n_experts, int top_k
     C.top_k = top_k;
     C.type = logits_type;
     route_blocks(n_tokens, &C.block_tokens, &C.n_blocks);
+    return PM_OK;
+}
+
+extern "C" pm_status pm_route_topk_device(int n_tokens, int n_experts, int top_k,
+                                          const void* d_logits, int logits_type, int64_t ld,
+                                          int32_t* d_ids, float* d_w, int32_t* d_offsets,
+                                          int32_t* d_order, void* d_ws, size_t ws_bytes,
+                                          void* stream) {
+    RouteCall C{};
+    pm_status st = check_route(n_tokens, n_experts, top_k, d_logits, logits_type, ld, nullptr,
+                               d_ids, d_w, d_offsets, d_order, d_ws, ws_bytes, &C);
+    if (st) return st;
+    if (n_tokens == 0 && !d_offsets) return PM_OK;
     return launched(launch_route(C, (hipStream_t)stream), "route");
+}
+
+extern "C" pm_status pm_route_scored_device(int n_tokens, int n_experts, int top_k,
+                                            pm_route_rule rule, const void* d_logits,
+                                            int logits_type, int64_t ld, const float* d_bias,
+                                            int32_t* d_ids, float* d_w, int32_t* d_offsets,
+                                            int32_t* d_order, void* d_ws, size_t ws_bytes,
+                                            void* stream) {
+    RouteCall C{};
+    pm_status st = check_route(n_tokens, n_experts, top_k, d_logits, logits_type, ld, d_bias,
+                               d_ids, d_w, d_offsets, d_order, d_ws, ws_bytes, &C);
+    if (st) return st;
+    if (rule.score != PM_SCORE_SIGMOID && rule.score != PM_SCORE_SOFTMAX)
+        return failf(PM_ERR_ARG, "route: score %d", rule.score);
+    if (rule.flags & ~uint32_t(PM_ROUTE_RENORM))
+        return failf(PM_ERR_ARG, "route: flags 0x%x", rule.flags);
+    if (rule.group_best < 1 || rule.group_best > 2)
+        return failf(PM_ERR_ARG, "route: group_best=%d", rule.group_best);
+    if (rule.n_groups < 1 || rule.top_groups < 1 || rule.top_groups > rule.n_groups)
+        return failf(PM_ERR_ARG, "route: %d of %d groups", rule.top_groups, rule.n_groups);
+    if (rule.n_groups > PM_ROUTE_MAX_GROUPS || n_experts % rule.n_groups)
+        return failf(PM_ERR_SHAPE, "route: %d groups of %d experts: at most %d, of one size",
+                     rule.n_groups, n_experts, PM_ROUTE_MAX_GROUPS);
+    if (int64_t(top_k) * rule.n_groups > int64_t(rule.top_groups) * n_experts)
+        return failf(PM_ERR_ARG, "route: top_k=%d of %d groups of %d", top_k, rule.top_groups,
+                     n_experts / rule.n_groups);
+    if (!(rule.scale >= -3.402823466e38f && rule.scale <= 3.402823466e38f))
+        return failf(PM_ERR_ARG, "route: scale %g", double(rule.scale));
+    if (n_tokens == 0 && !d_offsets) return PM_OK;
+    C.bias = d_bias;
+    C.rule = rule;
+    return launched(launch_route_scored(C, (hipStream_t)stream), "scored route");
 }
 
 // ---------------------------------------------------------------- grouped products
@@ -162,7 +210,7 @@ static pm_status check_grouped(pm_grouped_shape s, pm_grouped_rows r, const void
         return failf(PM_ERR_SHAPE, "grouped: gate and up of %d rows together", s.rows);
     if (r.n_rows < 0 || r.top_k < 1 || !uses_ok(r.n_rows))
         return failf(PM_ERR_ARG, "grouped: n_rows=%d top_k=%d", r.n_rows, r.top_k);
-    if (y_type != PM_F32 && y_type != x_type)
+    if (x_type == kE4M3 ? !type_ok(y_type) : y_type != PM_F32 && y_type != x_type)
         return failf(PM_ERR_ARG, "grouped: x of type %d, y of type %d", x_type, y_type);
     const int out = flags & PM_GROUPED_SWIGLU ? s.rows / 2 : s.rows;
     if (ldx < s.cols || ldx >= kMaxLd || ldy < out || ldy >= kMaxLd)
@@ -258,6 +306,69 @@ extern "C" pm_status pm_grouped_gemm_w4(pm_grouped_shape s, int group, const uin
     C.zeros = d_zeros;
     C.group = group;
     return launched(launch_grouped(C, kW4, (hipStream_t)stream), "grouped 4-bit product");
+}
+
+extern "C" pm_status pm_grouped_gemm_fp8(pm_grouped_shape s, const uint8_t* d_w,
+                                         const float* d_wscales, pm_grouped_rows r,
+                                         const uint8_t* d_x, const float* d_xscales, int64_t ldx,
+                                         void* d_y, int y_type, int64_t ldy, uint32_t flags,
+                                         void* stream) {
+    if (s.cols % 16)
+        return failf(PM_ERR_SHAPE, "grouped: %d inputs, not a multiple of 16", s.cols);
+    pm_status st = check_grouped(s, r, d_x, kE4M3, ldx, d_y, y_type, ldy, flags);
+    if (st) return st;
+    if (r.n_rows == 0 || s.rows == 0) return PM_OK;
+    if (s.cols > 0 && (!d_w || !d_wscales || !d_xscales || !aligned(d_w, 16) ||
+                       !aligned(d_wscales, 4) || !aligned(d_xscales, 4)))
+        return failf(PM_ERR_ARG, "grouped: codes or scales null or misaligned");
+    const size_t blocks = (size_t(s.cols) + 127) / 128;
+    const size_t x_rows = flags & PM_GROUPED_GATHER ? size_t(r.n_rows - 1) / r.top_k + 1 : r.n_rows;
+    const int out = flags & PM_GROUPED_SWIGLU ? s.rows / 2 : s.rows;
+    if (in_weights(s, r, d_w, size_t(s.rows) * s.cols, d_y, y_type, ldy, flags) ||
+        in_weights(s, r, d_wscales, 4 * ((size_t(s.rows) + 127) / 128) * blocks, d_y, y_type, ldy,
+                   flags) ||
+        overlap(d_xscales, 4 * x_rows * blocks, d_y, span(r.n_rows, ldy, out, y_type)))
+        return failf(PM_ERR_ARG, "grouped: y overlaps the codes or scales");
+    GroupedCall C = grouped_call(s, r, d_x, kE4M3, ldx, d_y, y_type, ldy, flags);
+    C.w = d_w;
+    C.wscales8 = d_wscales;
+    C.xscales8 = d_xscales;
+    C.w_type = kE4M3;
+    return launched(launch_grouped8(C, (hipStream_t)stream), "grouped 8-bit product");
+}
+
+// ---------------------------------------------------------------- 8-bit encoder
+extern "C" pm_status pm_encode_fp8_device(int n, pm_matrix_shape s, int block_rows,
+                                          const void* d_x, int type, int64_t ldx, uint8_t* d_q,
+                                          int64_t ldq, float* d_scales, void* stream) {
+    if (s.rows < 0 || s.cols < 0 || s.cols % 16 || s.group != 128)
+        return failf(PM_ERR_SHAPE, "encode: rows=%d cols=%d group=%d: need rows>=0, cols a "
+                     "multiple of 16, group 128", s.rows, s.cols, s.group);
+    if (n < 0 || !uses_ok(int64_t(n) * s.rows))
+        return failf(PM_ERR_ARG, "encode: %d matrices of %d rows", n, s.rows);
+    if (block_rows != 1 && block_rows != 128)
+        return failf(PM_ERR_ARG, "encode: blocks of %d rows, not 1 or 128", block_rows);
+    if (!type_ok(type)) return failf(PM_ERR_ARG, "encode: values of type %d", type);
+    if (ldx < s.cols || ldx >= kMaxLd || ldq < s.cols || ldq >= kMaxLd)
+        return failf(PM_ERR_ARG, "encode: row distances %lld, %lld for %d inputs", (long long)ldx,
+                     (long long)ldq, s.cols);
+    if (n == 0 || s.rows == 0 || s.cols == 0) return PM_OK;
+    if (!d_x || !d_q || !d_scales) return failf(PM_ERR_ARG, "encode: null device pointer");
+    if (!aligned(d_x, 16) || !aligned(d_q, 16) || !aligned(d_scales, 4) ||
+        (size_t(ldx) * type_bytes(type)) % 16 || ldq % 16)
+        return failf(PM_ERR_ARG, "encode: misaligned device pointer or rows");
+    const size_t rows = size_t(n) * s.rows;
+    const size_t blocks = size_t(n) * ((s.rows + int64_t(block_rows) - 1) / block_rows) *
+                          ((size_t(s.cols) + 127) / 128);
+    const struct { const void* p; size_t n; } buf[3] = {
+        {d_x, span(rows, ldx, s.cols, type)}, {d_q, span(rows, ldq, s.cols, kE4M3)},
+        {d_scales, 4 * blocks}};
+    for (int a = 1; a < 3; ++a)
+        for (int b = 0; b < a; ++b)
+            if (overlap(buf[a].p, buf[a].n, buf[b].p, buf[b].n))
+                return failf(PM_ERR_ARG, "encode: buffers overlap");
+    return launched(launch_encode8(n, s.rows, s.cols, block_rows, d_x, type, ldx, d_q, ldq,
+                                   d_scales, (hipStream_t)stream), "8-bit encoder");
 }
 
 // ---------------------------------------------------------------- 4-bit encoder

@@ -13,7 +13,9 @@
 
 namespace pm {
 
-inline size_t type_bytes(int t) { return t == PM_F32 ? 4 : 2; }
+// The type of 8-bit codes, beside PM_F32, PM_F16 and PM_BF16.
+constexpr int kE4M3 = 3;
+inline size_t type_bytes(int t) { return t == PM_F32 ? 4 : t == kE4M3 ? 1 : 2; }
 
 // ---------------------------------------------------------------- router
 struct RouteCall {
@@ -27,10 +29,13 @@ struct RouteCall {
     int32_t hist_stride;           // n_experts, rounded up to 8
     int32_t n_tokens, n_experts, top_k, type;
     int32_t block_tokens, n_blocks;   // tokens per histogram block, blocks
+    const float* bias;             // scored router: [n_experts] or null, and
+    pm_route_rule rule;            // how experts are scored and chosen
 };
 // Tokens of one histogram block and the number of blocks.
 void route_blocks(int n_tokens, int* block_tokens, int* n_blocks);
 hipError_t launch_route(const RouteCall& C, hipStream_t st);
+hipError_t launch_route_scored(const RouteCall& C, hipStream_t st);   // pm_scored.hip
 
 // ---------------------------------------------------------------- grouped products
 enum { kW16 = 0, kW4 = 1 };
@@ -47,6 +52,8 @@ struct GroupedCall {
     int32_t n_rows, top_k;
     int32_t w_type, x_type, y_type;   // w_type: PM_F16 / PM_BF16 (16-bit weights)
     uint32_t flags;
+    const float* wscales8;         // 8-bit: one per 128 x 128 weights
+    const float* xscales8;         // 8-bit: one per row and 128 inputs
 };
 // Experts of one call (the kernels keep a table of them in LDS).
 constexpr int kMaxGroupedExperts = PM_GROUPED_MAX_EXPERTS;
@@ -66,6 +73,9 @@ hipError_t launch_grouped_stream16(const GroupedCall& C, hipStream_t st);
 hipError_t launch_grouped_stream4(const GroupedCall& C, hipStream_t st);
 hipError_t launch_grouped_stream4f(const GroupedCall& C, hipStream_t st);
 
+// 8-bit weights and activations: the choice of the kernel (pm_fp8.hip).
+hipError_t launch_grouped8(const GroupedCall& C, hipStream_t st);
+
 // Compute units of the current device.
 int compute_units();
 // Lets a kernel take up to `bytes` of dynamic LDS on the current device; `done`
@@ -73,7 +83,9 @@ int compute_units();
 constexpr int kTileMaxLds = 160 * 1024 - 1024;
 hipError_t allow_lds(const void* kernel, int bytes, std::atomic<uint64_t>* done);
 
-// ---------------------------------------------------------------- 4-bit encoder, combine
+// ---------------------------------------------------------------- encoders, combine
+hipError_t launch_encode8(int n, int rows, int cols, int block_rows, const void* x, int type,
+                          int64_t ldx, uint8_t* q, int64_t ldq, float* scales, hipStream_t st);
 hipError_t launch_encode_w4(size_t n_groups, int group, const void* w, int type, uint8_t* q,
                             uint16_t* scales, uint8_t* zeros, hipStream_t st);
 hipError_t launch_combine_uses(int n_tokens, int top_k, int hidden, const void* z, int z_type,

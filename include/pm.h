@@ -371,6 +371,9 @@ pm_status pm_moe_token_forward(pm_store* s, int layer, int n_tokens, int top_k,
  *   pm_grouped_gemm        down with PM_GROUPED_SCATTER: one row per use;
  *   pm_combine_uses        y[t] = sum_j w[t][j] * row (t, j).
  * pm_grouped_gemm_w4 takes the place of pm_grouped_gemm for 4-bit experts.
+ * pm_route_scored_device takes the place of pm_route_topk_device where every
+ * expert has a score of its own.  8-bit experts: pm_encode_fp8_device of the
+ * activations before each pm_grouped_gemm_fp8.
  * Sums run in fp32 in a fixed order (no atomics); each output is rounded
  * once, to nearest even, to its type.  A call has at most PM_ROUTED_MAX_USES
  * uses (else PM_ERR_ARG).  Calls are ordered by `stream` alone (null: the null
@@ -406,6 +409,44 @@ pm_status pm_route_topk_device(int n_tokens, int n_experts, int top_k, const voi
                                int logits_type, int64_t ld, int32_t* d_ids, float* d_w,
                                int32_t* d_offsets, int32_t* d_order, void* d_ws,
                                size_t ws_bytes, void* stream);
+
+/* Router by scores: every expert e of a token gets a score in fp64 from its
+ * logit l_e,
+ *     s_e = 1 / (1 + e^-l_e)         (PM_SCORE_SIGMOID)   or
+ *     s_e = e^l_e / sum_f e^l_f      (PM_SCORE_SOFTMAX, over all experts),
+ * and a rank c_e = s_e + bias_e (d_bias fp32 [n_experts], null: c_e = s_e).
+ * The experts are n_groups equal runs of adjacent ones; a group counts the sum
+ * of its group_best (1 or 2) largest c, and the top_groups groups that count
+ * most stay (ties to the lower group; n_groups = top_groups = 1: all experts).
+ * Of these, the top_k largest c are selected, largest first, ties to the lower
+ * id.  The bias only selects: the weight of a selected expert is s_e, under
+ * PM_ROUTE_RENORM over the sum of the selected s, times `scale`; computed in
+ * fp64 and rounded to fp32.
+ * An expert whose logit or bias is -inf or NaN is never selected and counts in
+ * no group (a logit that is takes no part in the softmax either); a group of
+ * fewer than group_best others counts those, and one of none does not stay.  A
+ * token with fewer than top_k experts left has id -1 and weight 0 in its last
+ * slots.  Among +inf logits a softmax is shared equally, as in
+ * pm_route_topk_device; where the selected s add up to 0, PM_ROUTE_RENORM gives
+ * weights of 0.
+ * Everything else - the outputs, the uses sorted by expert, the workspace, the
+ * limits - is as in pm_route_topk_device.  PM_ERR_SHAPE: n_experts not a multiple
+ * of n_groups, or more than PM_ROUTE_MAX_GROUPS groups.  PM_ERR_ARG: a score,
+ * flag or group_best other than those above, top_groups outside 1 .. n_groups,
+ * a scale that is not finite, top_k above the experts of top_groups groups. */
+#define PM_ROUTE_MAX_GROUPS 64
+enum { PM_SCORE_SIGMOID = 0, PM_SCORE_SOFTMAX = 1 };
+enum { PM_ROUTE_RENORM = 1u };
+typedef struct {
+    int32_t score, n_groups, top_groups, group_best;
+    uint32_t flags;
+    float scale;
+} pm_route_rule;
+pm_status pm_route_scored_device(int n_tokens, int n_experts, int top_k, pm_route_rule rule,
+                                 const void* d_logits, int logits_type, int64_t ld,
+                                 const float* d_bias, int32_t* d_ids, float* d_w,
+                                 int32_t* d_offsets, int32_t* d_order, void* d_ws,
+                                 size_t ws_bytes, void* stream);
 
 /* Products grouped by expert.  W[e] is rows x cols; sorted row i belongs to
  * expert e when d_offsets[e] <= i < d_offsets[e+1]:
@@ -460,6 +501,42 @@ pm_status pm_grouped_gemm_w4(pm_grouped_shape s, int group, const uint8_t* d_q,
                              const uint16_t* d_scales, const uint8_t* d_zeros,
                              pm_grouped_rows r, const void* d_x, int x_type, int64_t ldx,
                              void* d_y, int y_type, int64_t ldy, uint32_t flags, void* stream);
+/* 8-bit weights and activations: codes are e4m3 (4 bits of exponent, bias 7, 3 of
+ * mantissa, largest 448, no infinities, NaN 0x7F and 0xFF), with one fp32 scale
+ * for each block of 128 inputs: of 128 x 128 weights and of 128 inputs of one
+ * row of x.
+ *     p[o] = sum_b sw[e][o/128][b] * sx[xr][b] * sum_{i in block b} w[e][o][i] x[xr][i]
+ *   d_w uint8 [n_experts][rows][cols], d_wscales fp32
+ *   [n_experts][ceil(rows/128)][ceil(cols/128)]; under PM_GROUPED_SWIGLU the
+ *   blocks of rows are those of the whole matrix, gate and up together.
+ *   d_x uint8 rows of cols, ldx apart, d_xscales fp32 [rows of x][ceil(cols/128)].
+ * cols % 16 == 0 (PM_ERR_SHAPE).  y is fp32, fp16 or bf16.
+ * The sums are taken in fp32 of exact products, with one exception: where y is
+ * bf16 and the call has many rows, the matrix cores multiply the codes as they
+ * are, and of any 8 adjacent products each is cut off at 2^-13 of the largest
+ * one's power of two (8 exponents of e4m3 below the mantissa's 6 bits), before
+ * they are added.  What that loses is at most 7 * 2^-13 of the largest product
+ * (products of codes below 2^-6 count as those of 2^-6), less than bf16's own
+ * half step of 2^-9 where that product is the result.
+ * A block's factor sw * sx is formed in fp32: beyond fp32's range it is
+ * infinite, and below 2^-126 it loses bits. */
+pm_status pm_grouped_gemm_fp8(pm_grouped_shape s, const uint8_t* d_w, const float* d_wscales,
+                              pm_grouped_rows r, const uint8_t* d_x, const float* d_xscales,
+                              int64_t ldx, void* d_y, int y_type, int64_t ldy, uint32_t flags,
+                              void* stream);
+/* Encoder of the 8-bit format: n matrices of s.rows rows of d_x (`type`, fp32,
+ * fp16 or bf16), row i of matrix m at (m * s.rows + i) * ldx.  A block is
+ * s.group = 128 inputs of block_rows rows, 1 (activations) or 128 (weights);
+ * the last blocks of a row and of a matrix hold what is left.  Per block, in fp32:
+ *     scale = max(max|x| / 448, 2^-126),   q = e4m3(x / scale), to nearest even.
+ * NaN and infinities get the code of NaN and do not count in the maximum.
+ *   d_q uint8, rows ldq apart; d_scales fp32
+ *   [n][ceil(rows/block_rows)][ceil(cols/128)].
+ * cols % 16 == 0 (PM_ERR_SHAPE).  d_x, d_q and their rows are 16-byte aligned;
+ * no buffer may overlap another (PM_ERR_ARG).  n * s.rows <= PM_ROUTED_MAX_USES. */
+pm_status pm_encode_fp8_device(int n, pm_matrix_shape s, int block_rows, const void* d_x, int type,
+                               int64_t ldx, uint8_t* d_q, int64_t ldq, float* d_scales,
+                               void* stream);
 /* Encoder of the 4-bit format from weights d_w [rows][cols] of `type`, per
  * group, in fp32: without d_zeros scale = fp16(max|w| / 7) and
  * q = clamp(rint(w / scale), -8, 7) + 8; with d_zeros, lo = min(w, 0) and
