@@ -5,6 +5,7 @@
 
 #include "pm_convert.h"
 #include "pm_device.h"
+#include "pm_fp8.h"
 #include "pm_grouped_codes.h"
 #include "pm_grouped_rows.h"
 #include "pm_routed.h"
@@ -14,16 +15,6 @@ namespace pm {
 namespace {
 
 constexpr int kRows8 = 16, kOut8 = 64;
-
-// 8 codes as halves.
-__device__ inline u32x4 codes_f16(uint32_t a, uint32_t b) {
-    u32x4 r;
-    r[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(a, 1.0f, false));
-    r[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(a, 1.0f, true));
-    r[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b, 1.0f, false));
-    r[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b, 1.0f, true));
-    return r;
-}
 
 // 16 rows of x by 64 outputs (32 of gate and up) per workgroup, 16 weight rows
 // a wave.
@@ -110,6 +101,15 @@ hipError_t run_plain8(const GroupedCall& C, hipStream_t st) {
 }  // namespace
 
 hipError_t launch_grouped8(const GroupedCall& C, hipStream_t st) {
+    const int64_t groups = std::min(C.n_experts, C.n_rows);
+    const int64_t x_rows = C.flags & PM_GROUPED_GATHER ? (C.n_rows - 1) / C.top_k + 1 : 256;
+    const bool far = x_rows * C.ldx + C.cols >= 0xFFFFFFF0ll;
+    if (C.n_rows >= 8 * groups && !far && C.cols > 0) {
+        const int64_t tiles256 = (C.n_rows / 256) * int64_t((C.rows + 255) / 256);
+        const bool big =
+            (C.n_rows >= 224 * groups && tiles256 >= 2 * compute_units()) || !fp8_tiles128_fit(C);
+        return launch_fp8_tiles(C, big ? 256 : 128, st);
+    }
     switch (C.y_type) {
     case PM_F32: return run_plain8<PM_F32>(C, st);
     case PM_F16: return run_plain8<PM_F16>(C, st);

@@ -347,6 +347,17 @@ def test_grouped8_inputs(C, y_ty, counts):
     run_grouped8(counts, 96, C, y_ty, 1, SCATTER, seed=C)
 
 
+@pytest.mark.parametrize("R,C", [(4096, 144), (4120, 400), (3000, 16), (4096, 2048)])
+def test_grouped8_large_tiles(R, C):
+    """Groups of many rows and more tiles of 256 x 256 than twice the compute
+    units, the last round not full; weight rows whose gate and up begin inside
+    a block of 128."""
+    for counts in ([4500, 4200], [2300, 257, 0, 6200, 255]):
+        for flags in (0, GATHER | SWIGLU, SCATTER):
+            report(f"fp8 large tiles {R} x {C} {counts} flags {flags}")
+            run_grouped8(counts, R, C, "bf16", 2, flags, seed=R + C, pad=flags & 1)
+
+
 def test_grouped8_many_experts():
     """512 and 4096 experts, most without rows; more rows than offsets end at."""
     g = np.random.default_rng(3)
