@@ -31,7 +31,7 @@ TARGETS = [
       os.path.join(PKG, "csrc", "pm_grouped_stream4.hip"),
       os.path.join(PKG, "csrc", "pm_grouped_stream4f.hip"), os.path.join(PKG, "csrc", "pm_combine.hip"),
       os.path.join(PKG, "csrc", "pm_scored.hip"), os.path.join(PKG, "csrc", "pm_fp8.hip"),
-      os.path.join(PKG, "csrc", "pm_fp8_tile.hip"),
+      os.path.join(PKG, "csrc", "pm_fp8_tile.hip"), os.path.join(PKG, "csrc", "pm_fp8_stream.hip"),
       os.path.join(PKG, "csrc", "pm_fp8_encode.hip")]),
     (os.path.join(ROOT, "synth", "libpmsynth.so"),
      [os.path.join(ROOT, "synth", "synth_device.hip")]),

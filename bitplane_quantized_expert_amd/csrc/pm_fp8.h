@@ -18,6 +18,8 @@ hipError_t launch_fp8_tiles(const GroupedCall& C, int rows, hipStream_t st);
 // Whether the table of experts lies in LDS beside the three stages of 128-row
 // tiles (beside those of 256 rows, and beside two stages, it always does).
 bool fp8_tiles128_fit(const GroupedCall& C);
+// Weights streamed past 16 rows of activations (pm_fp8_stream.hip); any sizes.
+hipError_t launch_fp8_stream(const GroupedCall& C, hipStream_t st);
 
 namespace {
 
