@@ -527,8 +527,9 @@ pm_status pm_grouped_gemm_fp8(pm_grouped_shape s, const uint8_t* d_w, const floa
 /* Encoder of the 8-bit format: n matrices of s.rows rows of d_x (`type`, fp32,
  * fp16 or bf16), row i of matrix m at (m * s.rows + i) * ldx.  A block is
  * s.group = 128 inputs of block_rows rows, 1 (activations) or 128 (weights);
- * the last blocks of a row and of a matrix hold what is left.  Per block, in fp32:
- *     scale = max(max|x| / 448, 2^-126),   q = e4m3(x / scale), to nearest even.
+ * the last blocks of a row and of a matrix hold what is left.  Per block:
+ *     scale = max(max|x| / 448, 2^-126) in fp32,
+ *     q = x / scale, rounded once, to the nearest (even) e4m3 value.
  * NaN and infinities get the code of NaN and do not count in the maximum.
  *   d_q uint8, rows ldq apart; d_scales fp32
  *   [n][ceil(rows/block_rows)][ceil(cols/128)].

@@ -70,8 +70,9 @@ def round_e4m3(v):
 
 def encode_plain(x, block_rows):
     """Values of the codes (fp64, NaN where x is not finite) and fp32 scales of
-    x [n][rows][cols]: quotients of fp32 numbers taken in fp64 and rounded to
-    fp32 (53 bits are enough that this equals the fp32 division)."""
+    x [n][rows][cols].  Quotients of fp32 numbers in fp64: their 53 bits tell
+    every quotient from the borders of two codes (which differ from it by 2^-29
+    of it at least, or not at all), and round to fp32 as the exact ones do."""
     x = x.double().cpu().numpy()
     n, r, c = x.shape
     rb, cb = -(-r // block_rows), -(-c // BLOCK)
@@ -85,7 +86,7 @@ def encode_plain(x, block_rows):
             s = np.maximum((top / 448.0).astype(np.float32), np.float32(2.0 ** -126))
             scales[:, i, j] = s
             d = (np.where(fin, v, 0.0) / s.astype(np.float64)[:, None, None])
-            d = round_e4m3(d.astype(np.float32).astype(np.float64))
+            d = round_e4m3(d)
             q[:, i * block_rows:(i + 1) * block_rows, j * BLOCK:(j + 1) * BLOCK] = \
                 np.where(fin, d, np.nan)
     return q, scales
