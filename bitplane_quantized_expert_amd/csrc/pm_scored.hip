@@ -1,7 +1,18 @@
 // Router by scores: sigmoid or softmax of every logit, a bias that only
-// selects, the best groups of experts, top-k among them (include/pm.h).  All
-// scores are fp64.
+// selects, the best groups of experts, top-k among them (include/pm.h).
+//
+// The rule's scores and ranks are fp64, and which expert is selected may hang on
+// their last bits; but an exponential and a division in fp64 for each of a token's
+// experts would take several times as long as all the rest.  So a wave ranks its
+// token's experts in fp32 first, with a bound on what these ranks are off by:
+// groups that stay or fall by more than it, and the few experts that the exact
+// ranks may place among the top_k.  These get their exact scores, one lane each
+// (16 lanes a token where they suffice), which the weights need in any case, and
+// the number of exact ranks above a lane's own is its place.  Where fp32 leaves
+// a choice open, the wave ranks the token again, in fp64.
 #include <hip/hip_runtime.h>
+
+#include <type_traits>
 
 #include "pm_route_sort.h"
 
@@ -9,380 +20,571 @@ namespace pm {
 
 namespace {
 
-constexpr int scored_waves(int vpt) { return vpt > 16 ? 4 : vpt > 8 ? 8 : kRouteWaves; }
+// Waves of a workgroup that selects: each has a token's ranks in LDS, 74 KB
+// together, and up to 64 logits per lane in registers.
+constexpr int scored_waves(int vpt) { return vpt > 32 ? 2 : vpt > 16 ? 4 : vpt > 8 ? 8 : kRouteWaves; }
 
-template <class T>
-__device__ inline T wave_best(T v) {
-    for (int d = 1; d < kWave; d <<= 1) {
-        const T o = __shfl_xor(v, d);
-        v = o > v ? o : v;
+// ---------------------------------------------------------------- across the wave
+// v and its value in lane i ^ D, in either order, for D = 1, 2, and for D = 4, 8,
+// 16, 32 where lanes that differ in lower bits only hold the same.
+struct Pair {
+    uint32_t a, b;
+};
+template <int D>
+__device__ inline Pair both(uint32_t v) {
+    if constexpr (D == 16) {
+        const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+        return {uint32_t(r[0]), uint32_t(r[1])};
+    } else if constexpr (D == 32) {
+        const auto r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+        return {uint32_t(r[0]), uint32_t(r[1])};
+    } else {
+        // quad_perm [1,0,3,2], [2,3,0,1], row_half_mirror, row_mirror
+        constexpr int ctrl = D == 1 ? 0xB1 : D == 2 ? 0x4E : D == 4 ? 0x141 : 0x140;
+        return {v, uint32_t(__builtin_amdgcn_update_dpp(0, int(v), ctrl, 0xF, 0xF, false))};
     }
-    return v;
+}
+template <int D>
+__device__ inline void both(uint32_t v, uint32_t* a, uint32_t* b) {
+    const Pair p = both<D>(v);
+    *a = p.a;
+    *b = p.b;
+}
+template <int D>
+__device__ inline void both(uint64_t v, uint64_t* a, uint64_t* b) {
+    const Pair lo = both<D>(uint32_t(v)), hi = both<D>(uint32_t(v >> 32));
+    *a = uint64_t(hi.a) << 32 | lo.a;
+    *b = uint64_t(hi.b) << 32 | lo.b;
+}
+// f(1), f(2), .. f(2^(log - 1)) with constant arguments.
+template <class F>
+__device__ inline void doublings(int log, F&& f) {
+    if (log > 0) f(std::integral_constant<int, 1>{});
+    if (log > 1) f(std::integral_constant<int, 2>{});
+    if (log > 2) f(std::integral_constant<int, 4>{});
+    if (log > 3) f(std::integral_constant<int, 8>{});
+    if (log > 4) f(std::integral_constant<int, 16>{});
+    if (log > 5) f(std::integral_constant<int, 32>{});
 }
 
-// The selection of one token by one wave.
-template <int VPT, int TYPE>
-__device__ inline void scored_token(const RouteCall& C, int t, int lane, int* id_out, float* w_out) {
-    const pm_route_rule& r = C.rule;
-    const int64_t base = int64_t(t) * C.ld;
-    const bool softmax = r.score == PM_SCORE_SOFTMAX;
-    const Logits<VPT> l = load_logits<VPT, TYPE>(C, t, lane);
-    double c[VPT];
-    float top = -INFINITY;
-#pragma unroll
-    for (int v = 0; v < VPT; ++v)
-        if (v * kWave + lane < C.n_experts && l.v[v] > top) top = l.v[v];
-    top = wave_best(top);
-    double sum = 0.0;
-    if (softmax) {
-#pragma unroll
-        for (int v = 0; v < VPT; ++v)
-            if (v * kWave + lane < C.n_experts && l.v[v] > -INFINITY)
-                sum += l.v[v] == top ? 1.0 : exp(double(l.v[v]) - double(top));
-        for (int d = 1; d < kWave; d <<= 1) sum += __shfl_xor(sum, d);
-    }
-    auto score = [&](float x) {
-        if (softmax) return (x == top ? 1.0 : exp(double(x) - double(top))) / sum;
-        return 1.0 / (1.0 + exp(-double(x)));
-    };
-#pragma unroll
-    for (int v = 0; v < VPT; ++v) {
-        const int e = v * kWave + lane;
-        c[v] = -INFINITY;
-        if (e < C.n_experts && l.v[v] > -INFINITY) {
-            const double b = C.bias ? double(C.bias[e]) : 0.0;
-            if (b > -INFINITY) c[v] = score(l.v[v]) + b;
-        }
-    }
-    if (r.n_groups > 1) {
-        const int size = C.n_experts / r.n_groups;
-        double mine = -INFINITY;                            // lane g: what group g counts
-        for (int g = 0; g < r.n_groups; ++g) {
-            double a = -INFINITY, b = -INFINITY;            // its two largest
-#pragma unroll
-            for (int v = 0; v < VPT; ++v) {
-                const int e = v * kWave + lane;
-                if (e >= g * size && e < (g + 1) * size) {
-                    b = fmax(b, fmin(a, c[v]));
-                    a = fmax(a, c[v]);
-                }
-            }
-            for (int d = 1; d < kWave; d <<= 1) {
-                const double oa = __shfl_xor(a, d), ob = __shfl_xor(b, d);
-                b = fmax(fmax(b, ob), fmin(a, oa));
-                a = fmax(a, oa);
-            }
-            if (lane == g) mine = r.group_best == 2 && b > -INFINITY ? a + b : a;
-        }
-        int better = 0;
-        for (int g = 0; g < r.n_groups; ++g) {
-            const double o = __shfl(mine, g);
-            better += o > mine || (o == mine && g < lane);
-        }
-        const uint64_t keep = __ballot(mine > -INFINITY && better < r.top_groups);
-#pragma unroll
-        for (int v = 0; v < VPT; ++v)
-            if (!((keep >> min((v * kWave + lane) / size, 63)) & 1)) c[v] = -INFINITY;
-    }
-    int id = -1;
-    for (int j = 0; j < C.top_k; ++j) {
-        double a = -INFINITY;
-        int at = 0x7FFFFFFF;
-#pragma unroll
-        for (int v = 0; v < VPT; ++v)
-            if (c[v] > a) {
-                a = c[v];
-                at = v * kWave + lane;
-            }
-        const double best = wave_best(a);
-        if (!(best > -INFINITY)) break;
-        int first = a == best ? at : 0x7FFFFFFF;
-        for (int d = 1; d < kWave; d <<= 1) first = min(first, __shfl_xor(first, d));
-#pragma unroll
-        for (int v = 0; v < VPT; ++v)
-            if (v * kWave + lane == first) c[v] = -INFINITY;
-        if (lane == j) id = first;
-    }
-    double s = 0.0;
-    if (id >= 0) s = score(load_f32<TYPE>(C.logits, base + id));
-    double all = s;
-    for (int d = 1; d < kWave; d <<= 1) all += __shfl_xor(all, d);
-    if (r.flags & PM_ROUTE_RENORM) s = all > 0.0 ? s / all : 0.0;
-    *id_out = id;
-    *w_out = float(s * double(r.scale));
+__device__ inline double wave_sum_f64(double v) {
+    v = row16_sum_f64(v);
+    uint64_t a, b;
+    both<16>(__builtin_bit_cast(uint64_t, v), &a, &b);
+    v = __builtin_bit_cast(double, a) + __builtin_bit_cast(double, b);
+    both<32>(__builtin_bit_cast(uint64_t, v), &a, &b);
+    return __builtin_bit_cast(double, a) + __builtin_bit_cast(double, b);
 }
 
-// Orders like the numbers; 0 for -inf and NaN.
-__device__ inline uint32_t rank_key(float c) {
-    if (!(c > -INFINITY)) return 0;
-    const uint32_t b = __float_as_uint(c + 0.0f);
-    return b ^ (b >> 31 ? 0xFFFFFFFFu : 0x80000000u);
+// ---------------------------------------------------------------- ranks
+// A rank as an integer that orders like it, 0 for -inf and NaN (never selected)
+// and where it does not count.  (The sum as a value: the compiler may not branch
+// round it)
+__device__ inline uint32_t rank_key(float c, bool counts = true) {
+    const uint32_t b = __float_as_uint(c + 0.0f);           // -0 counts as 0
+    uint32_t k = b ^ (uint32_t(int(b) >> 31) | 0x80000000u);
+    asm("" : "+v"(k));
+    return counts && c > -INFINITY ? k : 0u;
+}
+__device__ inline uint64_t rank_key(double c, bool counts = true) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, c + 0.0);
+    const uint64_t k = b ^ (uint64_t(int64_t(b) >> 63) | 1ull << 63);
+    return counts && c > -INFINITY ? k : 0ull;
 }
 __device__ inline float rank_value(uint32_t k) {
     return __uint_as_float(k ^ (k >> 31 ? 0x80000000u : 0xFFFFFFFFu));
 }
-__device__ inline float value_at(float v, int lane) {
+__device__ inline double rank_value(uint64_t k) {
+    return __builtin_bit_cast(double, k ^ (k >> 63 ? 1ull << 63 : ~0ull));
+}
+__device__ inline uint32_t top32(uint32_t k) { return k; }
+__device__ inline uint32_t top32(uint64_t k) { return uint32_t(k >> 32); }
+
+__device__ inline float lane_value(float v, int lane) {
     return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), lane));
 }
+__device__ inline double lane_value(double v, int lane) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    return __builtin_bit_cast(
+        double, uint64_t(uint32_t(__builtin_amdgcn_readlane(int(b >> 32), lane))) << 32 |
+                    uint32_t(__builtin_amdgcn_readlane(int(b), lane)));
+}
 
-// Ranks in fp32 and what they may be off by.  The score: e^-l from v_exp_f32 has an
-// error of |l| 2^-22 of it at most, 1 / (1 + e) and e / sum by v_rcp_f32 a few 2^-24
-// more; so 2^-20 of 1, and 2^-16 of the score itself.  The sum with a bias is
-// rounded to 2^-24 of it.  Twice that and more:
+// What a rank in fp32 may be off by, doubled and more.  The score: e^-l from
+// v_exp_f32 has an error of |l| 2^-22 of it at most, 1 / (1 + e) and e / sum by
+// v_rcp_f32 a few 2^-24 more; so 2^-20 of 1, and 2^-16 of the score itself.  The
+// sum with a bias is rounded to 2^-24 of it.
 __device__ inline float rank_slack(float v, bool bias) {
     return bias ? 0x1p-18f + fabsf(v) * 0x1p-21f : fminf(0x1p-18f, v * 0x1p-14f);
 }
 
-template <int VPT>
+// K: uint32_t (ranks in fp32) or uint64_t (exact).
+template <int VPT, class K>
 struct Ranks {
-    float c[VPT];                                   // in fp32; -inf: not selected
+    K key[VPT];
 };
 
-// The list of the experts with the largest ranks in fp32, sorted across the
-// lanes, ties by lower id: every expert that the exact ranks may select among
-// `held`, or *unsure.
-template <int VPT>
-__device__ inline void rank_list(const RouteCall& C, const Ranks<VPT>& r, int lane, int held,
-                                 uint32_t* key_out, int* id_out, bool* unsure) {
-    uint32_t key[VPT];
+// A bound that the top_k largest keys meet, as their top halves: at least top_k
+// of the lanes' own largest do, just top_k if any value tells so many apart.
+template <int VPT, class K>
+__device__ inline uint32_t rank_bound(const Ranks<VPT, K>& r, int top_k) {
+    uint32_t m = top32(r.key[0]);
 #pragma unroll
-    for (int v = 0; v < VPT; ++v) key[v] = rank_key(r.c[v]);
-    uint32_t m = key[0];
-#pragma unroll
-    for (int v = 1; v < VPT; ++v) m = max(m, key[v]);
-    // a bound that top_k lanes meet: the largest, or any that just top_k meet
-    uint32_t bound = 0;
-    for (uint32_t bit = 1u << 31; bit; bit >>= 1) {
-        const uint32_t c = bound | bit;
+    for (int v = 1; v < VPT; ++v) m = max(m, top32(r.key[v]));
+    uint32_t hi = m, lo = m;
+    doublings(6, [&](auto d) {
+        const Pair h = both<d>(hi), l = both<d>(lo);
+        hi = max(h.a, h.b);
+        lo = min(l.a, l.b);
+    });
+    hi = uni(int(hi));
+    lo = uni(int(lo));
+    // lo is met by top_k lanes at least, hi + 1 by none
+    while (lo < hi) {
+        const uint32_t c = lo + ((hi - lo) >> 1) + 1;
         const int n = __popcll(__ballot(m >= c));
-        if (n >= C.top_k) bound = c;
-        if (n == C.top_k) break;
+        if (n >= top_k) lo = c;
+        if (n == top_k) break;
+        if (n < top_k) hi = c - 1;
     }
-    const bool bias = C.bias != nullptr;
-    if (bound) {
-        const float v = rank_value(bound);
-        bound = rank_key(v - rank_slack(v, bias));
-    }
-    bound = bound ? bound : 1u;
+    return lo;
+}
+
+// The experts with the largest exact ranks, sorted across the lanes, ties by lower
+// id: lane j gets the id of place j (-1: none).
+template <int VPT>
+__device__ inline int rank_list(const RouteCall& C, const Ranks<VPT, uint64_t>& r, int lane) {
+    const uint32_t bound = max(rank_bound(r, C.top_k), 1u);
     // list across the lanes, descending: (key, ~expert), 0 for none
-    uint32_t mine = 0, low = 0;
-    int found = 0;
+    uint64_t mine = 0;
+    uint32_t low = 0;
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
-        uint64_t hit = __ballot(key[v] >= bound);
-        found += __popcll(hit);
+        uint64_t hit = __ballot(top32(r.key[v]) >= bound);
         while (hit) {
             const int l = __builtin_ctzll(hit);
             hit &= hit - 1;
-            const uint32_t k = __builtin_amdgcn_readlane(key[v], l);
+            const uint64_t k = uint64_t(uint32_t(__builtin_amdgcn_readlane(int(r.key[v] >> 32), l))) << 32 |
+                               uint32_t(__builtin_amdgcn_readlane(int(r.key[v]), l));
             const uint32_t ne = ~uint32_t(v * kWave + l);
             // lanes that come after it move up by one, the first takes it
-            const bool after = (uint64_t(mine) << 32 | low) < (uint64_t(k) << 32 | ne);
+            const bool after = mine < k || (mine == k && low < ne);
             const uint64_t mask = __ballot(after);
             if (mask == 0) continue;
             const int first = __builtin_ctzll(mask);
+            const uint32_t hi_up = __shfl_up(uint32_t(mine >> 32), 1), lo_up = __shfl_up(uint32_t(mine), 1);
+            const uint32_t low_up = __shfl_up(low, 1);
             if (after) {
-                mine = __builtin_amdgcn_update_dpp(int(mine), int(mine), 0x138, 0xF, 0xF, false);
-                low = __builtin_amdgcn_update_dpp(int(low), int(low), 0x138, 0xF, 0xF, false);
+                mine = uint64_t(hi_up) << 32 | lo_up;
+                low = low_up;
             }
-            mine = lane == first ? k : mine;
-            low = lane == first ? ne : low;
+            if (lane == first) {
+                mine = k;
+                low = ne;
+            }
         }
     }
-    *unsure = false;
-    if (found > held) {
-        const float last = value_at(rank_value(mine), C.top_k - 1);
-        *unsure = !(value_at(rank_value(mine), held - 1) < last - rank_slack(last, bias));
-    }
-    *key_out = mine;
-    *id_out = mine ? int(~low) : -1;
+    return mine && lane < C.top_k ? int(~low) : -1;
 }
 
-// Takes the experts of the groups that do not stay out of the ranks; false where
-// fp32 does not tell which do.  `space`: the wave's LDS, padded_at(E) floats.
-__device__ inline int padded_at(int e) { return e + (e >> 3); }
+// ---------------------------------------------------------------- groups
+// How the experts of a lane fall into groups, the same for every token: 2^log
+// lanes look at a group, and of[v] is the first of them for expert v * 64 + lane.
 template <int VPT>
-__device__ inline bool rank_groups(const RouteCall& C, Ranks<VPT>& r, int lane, float* space) {
-    const pm_route_rule& rule = C.rule;
-    const int n = rule.n_groups, size = C.n_experts / n;
+struct Groups {
+    int log, size;
+    int of[VPT];
+};
+template <int VPT>
+__device__ inline Groups<VPT> find_groups(const RouteCall& C, int lane) {
+    Groups<VPT> g;
+    g.log = C.rule.n_groups > 1 ? 6 - (32 - __builtin_clz(C.rule.n_groups - 1)) : 0;
+    g.size = C.n_experts / C.rule.n_groups;
 #pragma unroll
-    for (int v = 0; v < VPT; ++v) {
-        const int e = v * kWave + lane;
-        if (e < C.n_experts) space[padded_at(e)] = r.c[v];
-    }
+    for (int v = 0; v < VPT; ++v)
+        g.of[v] = C.rule.n_groups > 1 ? min(v * kWave + lane, C.n_experts - 1) / g.size << g.log : 0;
+    return g;
+}
+
+// Places apart in LDS of experts that the lanes of several groups read at once.
+__device__ inline int padded_at(int e) { return e + (e >> 3); }
+constexpr int padded_size(int vpt) { return vpt * (kWave + kWave / 8); }
+
+// Takes the experts of the groups that do not stay out of the ranks; false where
+// ranks in fp32 do not tell which do.  `space`: the wave's LDS, padded_size(VPT)
+// keys.
+template <int VPT, class K>
+__device__ inline bool rank_groups(const RouteCall& C, const Groups<VPT>& groups,
+                                   Ranks<VPT, K>& r, int lane, K* space) {
+    typedef typename std::conditional<sizeof(K) == 8, double, float>::type Value;
+    const pm_route_rule& rule = C.rule;
+    const int n = rule.n_groups, size = groups.size, log = groups.log;
+    K* const own = space + padded_at(lane);
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) own[v * padded_at(kWave)] = r.key[v];
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    // 2^log lanes per group
-    const int log = 6 - (32 - __builtin_clz(n - 1));
     const int g = lane >> log, j = lane & ((1 << log) - 1);
-    float a = -INFINITY, b = -INFINITY;                     // its two largest
-    if (g < n)
-        for (int i = j; i < size; i += 1 << log) {
-            const float c = space[padded_at(g * size + i)];
-            b = fmaxf(b, fminf(a, c));
-            a = fmaxf(a, c);
+    K a = 0, b = 0;                                         // its two largest
+    int base = min(g, n - 1) * size;
+    asm volatile("" : "+v"(base));                          // (addresses are not kept)
+    for (int i0 = j; i0 - j < size; i0 += 8 << log) {
+        K k[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) k[i] = space[padded_at(base + min(i0 + (i << log), size - 1))];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const K c = i0 + (i << log) < size ? k[i] : K(0);
+            b = max(b, min(a, c));
+            a = max(a, c);
         }
-    for (int d = 1; d < 1 << log; d <<= 1) {
-        const float oa = __shfl_xor(a, d), ob = __shfl_xor(b, d);
-        b = fmaxf(fmaxf(b, ob), fminf(a, oa));
-        a = fmaxf(a, oa);
     }
-    const float mine = rule.group_best == 2 && b > -INFINITY ? a + b : a;
-    const float slack = 4.0f * (0x1p-18f + fabsf(mine) * 0x1p-21f);
-    // groups that count more for certain, and those that may
-    int more = 0, maybe = 0;
-    for (int k = 0; k < n; ++k) {
-        const float o = value_at(mine, k << log);
-        more += o > mine + slack;
-        maybe += k != g && !(o < mine - slack);
+    asm volatile("" ::: "memory");                          // (read before the next token's)
+    doublings(log, [&](auto d) {
+        K a0, a1, b0, b1;
+        both<d>(a, &a0, &a1);
+        both<d>(b, &b0, &b1);
+        a = max(a0, a1);
+        b = max(min(a0, a1), max(b0, b1));
+    });
+    const bool real = g < n && a != 0;
+    Value mine = real ? rank_value(a) : Value(-INFINITY);
+    if (rule.group_best == 2 && b != 0) mine += rank_value(b);
+    bool stays;
+    if constexpr (sizeof(K) == 8) {
+        int more = 0;
+        for (int k = 0; k < n; ++k) {
+            const double o = lane_value(mine, k << log);
+            more += o > mine || (o == mine && k < g);
+        }
+        stays = real && more < rule.top_groups;
+    } else {
+        // groups that count more for certain, and those that may
+        const float slack = 4.0f * (0x1p-18f + fabsf(mine) * 0x1p-21f);
+        int more = 0, maybe = -1;
+        for (int k = 0; k < n; ++k) {
+            const float o = lane_value(mine, k << log);
+            more += o > mine + slack;
+            maybe += !(o < mine - slack);
+        }
+        stays = real && maybe < rule.top_groups;
+        if (__ballot(real && !stays && more < rule.top_groups)) return false;
     }
-    const bool real = g < n && mine > -INFINITY;
-    const bool stays = real && maybe < rule.top_groups;
-    if (__ballot(real && !stays && more < rule.top_groups)) return false;
     const uint64_t keep = __ballot(stays);                  // bit of a group: its first lane's
 #pragma unroll
-    for (int v = 0; v < VPT; ++v) {
-        const int of = min(v * kWave + lane, C.n_experts - 1) / size;
-        if (!((keep >> (of << log)) & 1)) r.c[v] = -INFINITY;
-    }
+    for (int v = 0; v < VPT; ++v) r.key[v] = (keep >> groups.of[v]) & 1 ? r.key[v] : K(0);
     return true;
 }
 
-template <int VPT, int TYPE>
+// ---------------------------------------------------------------- scores
+// A softmax's largest logit, and its sum.
+struct Softmax {
+    float top;
+    double sum;
+};
+__device__ inline double softmax_part(float l, float top) {
+    return l == top ? 1.0 : exp(double(l) - double(top));
+}
+__device__ inline double exact_score(bool softmax, const Softmax& s, float l) {
+    return softmax ? softmax_part(l, s.top) / s.sum : 1.0 / (1.0 + exp(-double(l)));
+}
+
+// A token's logits as they are loaded: every 64th from logit `lane` on (0 past the
+// last).
+template <int VPT>
+struct RawLogits {
+    uint32_t d[VPT];
+};
+template <int VPT>
+__device__ inline RawLogits<VPT> load_raw(const RouteCall& C, int t, int lane) {
+    RawLogits<VPT> l;
+    const int log = C.type == PM_F32 ? 2 : 1;
+    const auto row = __builtin_amdgcn_make_buffer_rsrc(
+        uni_ptr(const_cast<char*>(static_cast<const char*>(C.logits)) + (int64_t(t) * C.ld << log)),
+        0, C.n_experts << log, 0x00020000);
+    if (C.type == PM_F32) {
+#pragma unroll
+        for (int v = 0; v < VPT; ++v)
+            l.d[v] = __builtin_amdgcn_raw_buffer_load_b32(row, lane * 4, v * kWave * 4, 0);
+    } else {
+#pragma unroll
+        for (int v = 0; v < VPT; ++v)
+            l.d[v] = uint16_t(__builtin_amdgcn_raw_buffer_load_b16(row, lane * 2, v * kWave * 2, 0));
+    }
+    return l;
+}
+template <int VPT>
+__device__ inline Logits<VPT> widen(const RouteCall& C, const RawLogits<VPT>& r) {
+    Logits<VPT> l;
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) l.v[v] = __uint_as_float(r.d[v]);
+    if (C.type == PM_BF16) {
+#pragma unroll
+        for (int v = 0; v < VPT; ++v) l.v[v] = __uint_as_float(r.d[v] << 16);
+    } else if (C.type == PM_F16) {
+#pragma unroll
+        for (int v = 0; v < VPT; ++v) l.v[v] = __half2float(__ushort_as_half(uint16_t(r.d[v])));
+    }
+    return l;
+}
+__device__ inline float logit(const RouteCall& C, int t, int e) {
+    const int64_t at = int64_t(t) * C.ld + e;
+    if (C.type == PM_F32) return load_f32<PM_F32>(C.logits, at);
+    return C.type == PM_F16 ? load_f32<PM_F16>(C.logits, at) : load_f32<PM_BF16>(C.logits, at);
+}
+
+// An expert that the exact ranks may select, with what its rank takes.
+struct Candidate {
+    int32_t id;
+    float logit, bias;
+};
+
+// The number of lanes with a larger (key, ~id) among those that share a token: 16
+// lanes, or all 64 of which `found` hold one.
+__device__ inline int place_of16(uint64_t key, uint32_t low) {
+    int n = 0;
+    auto turn = [&](auto by) {
+        constexpr int ctrl = 0x120 + decltype(by)::value;  // row_ror
+        const uint32_t h = __builtin_amdgcn_update_dpp(0, int(key >> 32), ctrl, 0xF, 0xF, false);
+        const uint32_t l = __builtin_amdgcn_update_dpp(0, int(key), ctrl, 0xF, 0xF, false);
+        const uint32_t o = __builtin_amdgcn_update_dpp(0, int(low), ctrl, 0xF, 0xF, false);
+        const uint64_t k = uint64_t(h) << 32 | l;
+        n += k > key || (k == key && o > low);
+    };
+    turn(std::integral_constant<int, 1>{});
+    turn(std::integral_constant<int, 2>{});
+    turn(std::integral_constant<int, 3>{});
+    turn(std::integral_constant<int, 4>{});
+    turn(std::integral_constant<int, 5>{});
+    turn(std::integral_constant<int, 6>{});
+    turn(std::integral_constant<int, 7>{});
+    turn(std::integral_constant<int, 8>{});
+    turn(std::integral_constant<int, 9>{});
+    turn(std::integral_constant<int, 10>{});
+    turn(std::integral_constant<int, 11>{});
+    turn(std::integral_constant<int, 12>{});
+    turn(std::integral_constant<int, 13>{});
+    turn(std::integral_constant<int, 14>{});
+    turn(std::integral_constant<int, 15>{});
+    return n;
+}
+__device__ inline int place_of64(uint64_t key, uint32_t low, int found) {
+    int n = 0;
+    for (int i = 0; i < found; ++i) {
+        const uint64_t k = uint64_t(uint32_t(__builtin_amdgcn_readlane(int(key >> 32), i))) << 32 |
+                           uint32_t(__builtin_amdgcn_readlane(int(key), i));
+        const uint32_t o = __builtin_amdgcn_readlane(low, i);
+        n += k > key || (k == key && o > low);
+    }
+    return n;
+}
+
+template <int VPT, bool SOFTMAX>
 struct ScoredRouter {
     static constexpr int kWaves = scored_waves(VPT);
+    struct Space {
+        uint64_t key[padded_size(VPT)];
+        Candidate listed[kWave];
+    };
+
     template <class F>
     __device__ static inline void tokens(const RouteCall& C, int t0, int t1, int step, int lane,
                                          F&& f) {
-        __shared__ float space[kWaves][VPT * kWave + VPT * 8];
-        if (t0 >= t1) return;
+        __shared__ Space spaces[kWaves];
+        Space* const space = &spaces[threadIdx.x >> 6];
+        // 64 tokens in fp32, then those among them that it leaves open (apart, as
+        // the registers of the two are not the same)
+        for (; t0 < t1; t0 += kWave * step) {
+            uint64_t redo = rank_tokens(C, t0, min(t1 - t0, kWave * step) + t0, step, lane, space, f);
+            for (; redo; redo &= redo - 1) {
+                const int t = t0 + __builtin_ctzll(redo) * step;
+                float w;
+                int own = lane;
+                asm volatile("" : "+v"(own));               // (nothing of it is kept)
+                const int e = rank_again(C, t, own, space, &w);
+                if (lane < C.top_k) {
+                    const int64_t u = int64_t(t) * C.top_k + lane;
+                    C.ids[u] = e;
+                    C.w[u] = w;
+                    if (e >= 0) f(u, e);
+                }
+            }
+        }
+    }
+
+private:
+    // Up to 64 tokens; returns those that are left, a bit each.
+    template <class F>
+    __device__ static inline uint64_t rank_tokens(const RouteCall& C, int t0, int t1, int step,
+                                                  int lane, Space* space, F&& f) {
+        uint64_t left = 0;
         const pm_route_rule& rule = C.rule;
-        const bool softmax = rule.score == PM_SCORE_SOFTMAX;
+        const bool biased = C.bias != nullptr;
+        const Groups<VPT> groups = find_groups<VPT>(C, lane);
+        // -inf: never selected.  (Neither is an expert of a NaN: no rank is one)
         float bias[VPT];
 #pragma unroll
         for (int v = 0; v < VPT; ++v) {
             const int e = v * kWave + lane;
-            bias[v] = e < C.n_experts ? (C.bias ? C.bias[e] : 0.0f) : -INFINITY;
+            bias[v] = e < C.n_experts ? (biased ? C.bias[e] : 0.0f) : -INFINITY;
         }
         // up to 4 tokens share the exact scores where 16 lanes hold a token's
-        // slots and a few ranks behind them
+        // candidates
         const int held = C.top_k <= 12 ? 16 : kWave, group = kWave / held;
         const int slot = lane & (held - 1);
-        Logits<VPT> next = load_logits<VPT, TYPE>(C, t0, lane);
+        RawLogits<VPT> next = load_raw<VPT>(C, t0, lane);
         for (int t = t0; t < t1; t += group * step) {
-            int id = -1, tok = -1;
-            float top = 0.0f;                               // softmax: the largest logit,
-            double sum = 1.0;                               // and the sum
-            uint64_t redo = 0;                              // tokens that fp32 leaves open
+            int tok = -1, found = 0;
+            Softmax soft{0.0f, 1.0};
+            uint32_t redo = 0;                              // of these
             for (int s = 0; s < group && t + s * step < t1; ++s) {
-                const Logits<VPT> now = next;
+                const Logits<VPT> now = widen(C, next);
                 // the next token's logits are on their way meanwhile
-                next = load_logits<VPT, TYPE>(C, min(t + (s + 1) * step, t1 - 1), lane);
-                Ranks<VPT> r;
-                float big = -INFINITY;
-                double all = 0.0;
-                if (softmax) {
+                next = load_raw<VPT>(C, min(t + (s + 1) * step, t1 - 1), lane);
+                Softmax all{-INFINITY, 0.0};
+                Ranks<VPT, uint32_t> r;
+                if constexpr (SOFTMAX) {
+                    double x[VPT];
+                    all = softmax_of(C, now, lane, x);
+                    const float part = __builtin_amdgcn_rcpf(float(all.sum));
 #pragma unroll
                     for (int v = 0; v < VPT; ++v)
-                        if (v * kWave + lane < C.n_experts) big = fmaxf(big, now.v[v]);
-                    big = wave_best(big);
-                    double x[VPT];
-#pragma unroll
-                    for (int v = 0; v < VPT; ++v) {
-                        const bool seen = v * kWave + lane < C.n_experts && now.v[v] > -INFINITY;
-                        x[v] = !seen ? 0.0
-                                     : now.v[v] == big ? 1.0 : exp(double(now.v[v]) - double(big));
-                        all += x[v];
-                    }
-                    for (int d = 1; d < kWave; d <<= 1) all += __shfl_xor(all, d);
-                    const float part = __builtin_amdgcn_rcpf(float(all));
-#pragma unroll
-                    for (int v = 0; v < VPT; ++v) r.c[v] = float(x[v]) * part;
+                        r.key[v] = rank_key(float(x[v]) * part + bias[v], now.v[v] > -INFINITY);
                 } else {
 #pragma unroll
-                    for (int v = 0; v < VPT; ++v)
-                        r.c[v] = __builtin_amdgcn_rcpf(
+                    for (int v = 0; v < VPT; ++v) {
+                        const float x = __builtin_amdgcn_rcpf(
                             1.0f + __builtin_amdgcn_exp2f(now.v[v] * -1.44269504f));
+                        r.key[v] = rank_key(x + bias[v], now.v[v] > -INFINITY);
+                    }
                 }
+                bool sure = true;
+                if (rule.n_groups > 1)
+                    sure = rank_groups<VPT>(C, groups, r, lane,
+                                            reinterpret_cast<uint32_t*>(space->key));
+                // all that may be among the top_k, into this token's lanes
+                uint32_t bound = rank_bound(r, C.top_k);
+                if (bound) {
+                    const float v = rank_value(bound);
+                    bound = rank_key(v - rank_slack(v, biased));
+                }
+                bound = max(bound, 1u);
+                int n = 0;
 #pragma unroll
                 for (int v = 0; v < VPT; ++v) {
-                    // (a NaN among logit and bias leaves no rank, either)
-                    r.c[v] = now.v[v] > -INFINITY ? r.c[v] + bias[v] : -INFINITY;
+                    const bool hit = r.key[v] >= bound;
+                    const uint64_t hits = __ballot(hit);
+                    const int at = n + __builtin_amdgcn_mbcnt_hi(
+                                           uint32_t(hits >> 32),
+                                           __builtin_amdgcn_mbcnt_lo(uint32_t(hits), 0));
+                    if (hit && at < held)
+                        space->listed[s * held + at] = {v * kWave + lane, now.v[v], bias[v]};
+                    n += __popcll(hits);
                 }
-                bool unsure = false;
-                if (rule.n_groups > 1)
-                    unsure = !rank_groups<VPT>(C, r, lane, space[threadIdx.x >> 6]);
-                uint32_t k = 0;
-                int i = -1;
-                if (!unsure) rank_list<VPT>(C, r, lane, held, &k, &i, &unsure);
-                if (unsure) redo |= uint64_t(1) << s;
-                const int is = __shfl(i, slot);
-                if (lane / held != s) continue;
-                id = is;
-                tok = t + s * step;
-                top = big;
-                sum = all;
+                if (!sure || n > held) redo |= 1u << s;
+                if (lane / held == s) {
+                    tok = t + s * step;
+                    found = n;
+                    soft = all;
+                }
             }
-            // exact scores, and whether the exact ranks are in this order
-            double x = 0.0, c = -INFINITY;
-            if (id >= 0) {
-                const float l = load_f32<TYPE>(C.logits, int64_t(tok) * C.ld + id);
-                if (softmax)
-                    x = (l == top ? 1.0 : exp(double(l) - double(top))) / sum;
-                else
-                    x = 1.0 / (1.0 + exp(-double(l)));
-                c = x + (C.bias ? double(C.bias[id]) : 0.0);
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            // exact scores and ranks, and the place of each
+            int id = -1;
+            double x = 0.0;
+            uint64_t key = 0;
+            if (slot < found) {
+                const Candidate c = space->listed[lane];
+                id = c.id;
+                x = exact_score(SOFTMAX, soft, c.logit);
+                key = rank_key(x + double(c.bias));
             }
-            const double after = __shfl_down(c, 1);
-            const int id_after = __shfl_down(id, 1);
-            const bool order = slot == held - 1 || id_after < 0 || c > after ||
-                               (c == after && id < id_after);
-            const uint64_t wrong = __ballot(!order);
-            for (int s = 0; s < group; ++s)
-                if ((wrong >> (s * held)) & (held == kWave ? ~0ull : 0xFFFFull))
-                    redo |= uint64_t(1) << s;
-            if (slot >= C.top_k) {
-                id = -1;
-                x = 0.0;
-            }
+            asm volatile("" ::: "memory");                  // (read before the next tokens')
+            const int place = held == kWave ? place_of64(key, ~uint32_t(id), uni(found))
+                                            : place_of16(key, ~uint32_t(id));
+            const bool chosen = id >= 0 && place < C.top_k;
+            if (!chosen) x = 0.0;
             if (rule.flags & PM_ROUTE_RENORM) {
-                double all = row16_sum_f64(x);
-                if (held == kWave) {
-                    all += __shfl_xor(all, 16);
-                    all += __shfl_xor(all, 32);
-                }
+                const double all = held == kWave ? wave_sum_f64(x) : row16_sum_f64(x);
                 x = all > 0.0 ? x / all : 0.0;
             }
-            if (tok >= 0 && slot < C.top_k && !((redo >> (lane / held)) & 1)) {
-                const int64_t u = int64_t(tok) * C.top_k + slot;
-                C.ids[u] = id;
-                C.w[u] = id >= 0 ? float(x * double(rule.scale)) : 0.0f;
-                if (id >= 0) f(u, id);
-            }
-            while (redo) {
-                const int s = __builtin_ctzll(redo);
-                redo &= redo - 1;
-                if (t + s * step >= t1) continue;
-                int i;
-                float w;
-                scored_token<VPT, TYPE>(C, t + s * step, lane, &i, &w);
-                if (lane < C.top_k) {
-                    const int64_t u = int64_t(t + s * step) * C.top_k + lane;
-                    C.ids[u] = i;
-                    C.w[u] = i >= 0 ? w : 0.0f;
-                    if (i >= 0) f(u, i);
+            if (tok >= 0 && !((redo >> (lane / held)) & 1)) {
+                const int64_t u = int64_t(tok) * C.top_k;
+                if (chosen) {
+                    C.ids[u + place] = id;
+                    C.w[u + place] = float(x * double(rule.scale));
+                    f(u + place, id);
+                }
+                // slots left over
+                if (slot >= found && slot < C.top_k) {
+                    C.ids[u + slot] = -1;
+                    C.w[u + slot] = 0.0f;
                 }
             }
+            left |= uint64_t(redo) << ((t - t0) / step);
         }
+        return left;
+    }
+
+    __device__ static inline Softmax softmax_of(const RouteCall& C, const Logits<VPT>& l, int lane,
+                                                double* x) {
+        Softmax all{-INFINITY, 0.0};
+        uint32_t big = 0;
+#pragma unroll
+        for (int v = 0; v < VPT; ++v)
+            if (v * kWave + lane < C.n_experts) big = max(big, rank_key(l.v[v]));
+        doublings(6, [&](auto d) {
+            const Pair p = both<d>(big);
+            big = max(p.a, p.b);
+        });
+        if (big) all.top = rank_value(big);
+#pragma unroll
+        for (int v = 0; v < VPT; ++v) {
+            const bool seen = v * kWave + lane < C.n_experts && l.v[v] > -INFINITY;
+            x[v] = seen ? softmax_part(l.v[v], all.top) : 0.0;
+            all.sum += x[v];
+            if (VPT > 4) __builtin_amdgcn_sched_barrier(0);           // (registers)
+        }
+        all.sum = wave_sum_f64(all.sum);
+        return all;
+    }
+
+    // A token by its exact ranks: the expert (-1: none) and weight of slot `lane`.
+    __device__ static inline int rank_again(const RouteCall& C, int t, int lane, Space* space,
+                                            float* w) {
+        const Logits<VPT> l = widen(C, load_raw<VPT>(C, t, lane));
+        const Groups<VPT> groups = find_groups<VPT>(C, lane);
+        Softmax soft{0.0f, 1.0};
+        Ranks<VPT, uint64_t> r;
+        if constexpr (SOFTMAX) {
+            double x[VPT];
+            soft = softmax_of(C, l, lane, x);
+        }
+#pragma unroll
+        for (int v = 0; v < VPT; ++v) {
+            const int e = v * kWave + lane;
+            const float b = e < C.n_experts ? (C.bias ? C.bias[e] : 0.0f) : -INFINITY;
+            r.key[v] = rank_key(exact_score(SOFTMAX, soft, l.v[v]) + double(b),
+                                l.v[v] > -INFINITY && b > -INFINITY);
+            if (VPT > 4) __builtin_amdgcn_sched_barrier(0);           // (registers)
+        }
+        if (C.rule.n_groups > 1) rank_groups<VPT>(C, groups, r, lane, space->key);
+        const int id = rank_list<VPT>(C, r, lane);
+        double x = 0.0;
+        if (id >= 0)
+            x = exact_score(SOFTMAX, soft, logit(C, t, id));
+        if (C.rule.flags & PM_ROUTE_RENORM) {
+            const double all = wave_sum_f64(x);
+            x = all > 0.0 ? x / all : 0.0;
+        }
+        *w = id >= 0 ? float(x * double(C.rule.scale)) : 0.0f;
+        return id;
     }
 };
 
 template <int VPT>
 hipError_t launch_scored(const RouteCall& C, hipStream_t st) {
-    switch (C.type) {
-    case PM_F32: return launch_routed<ScoredRouter<VPT, PM_F32>>(C, st);
-    case PM_F16: return launch_routed<ScoredRouter<VPT, PM_F16>>(C, st);
-    default: return launch_routed<ScoredRouter<VPT, PM_BF16>>(C, st);
-    }
+    return C.rule.score == PM_SCORE_SOFTMAX ? launch_routed<ScoredRouter<VPT, true>>(C, st)
+                                            : launch_routed<ScoredRouter<VPT, false>>(C, st);
 }
 
 }  // namespace
