@@ -81,13 +81,13 @@ __device__ inline double wave_sum_f64(double v) {
 // and where it does not count.  (The sum as a value: the compiler may not branch
 // round it)
 __device__ inline uint32_t rank_key(float c, bool counts = true) {
-    const uint32_t b = __float_as_uint(c + 0.0f);           // -0 counts as 0
+    const uint32_t b = __float_as_uint(c);                  // (a sum with a score is not -0)
     uint32_t k = b ^ (uint32_t(int(b) >> 31) | 0x80000000u);
     asm("" : "+v"(k));
     return counts && c > -INFINITY ? k : 0u;
 }
 __device__ inline uint64_t rank_key(double c, bool counts = true) {
-    const uint64_t b = __builtin_bit_cast(uint64_t, c + 0.0);
+    const uint64_t b = __builtin_bit_cast(uint64_t, c);
     const uint64_t k = b ^ (uint64_t(int64_t(b) >> 63) | 1ull << 63);
     return counts && c > -INFINITY ? k : 0ull;
 }
@@ -166,7 +166,7 @@ __device__ inline int rank_list(const RouteCall& C, const Ranks<VPT, uint64_t>& 
             hit &= hit - 1;
             const uint64_t k = uint64_t(uint32_t(__builtin_amdgcn_readlane(int(r.key[v] >> 32), l))) << 32 |
                                uint32_t(__builtin_amdgcn_readlane(int(r.key[v]), l));
-            const uint32_t ne = ~uint32_t(v * kWave + l);
+            const uint32_t ne = ~uint32_t(l * VPT + v);
             // lanes that come after it move up by one, the first takes it
             const bool after = mine < k || (mine == k && low < ne);
             const uint64_t mask = __ballot(after);
@@ -188,21 +188,22 @@ __device__ inline int rank_list(const RouteCall& C, const Ranks<VPT, uint64_t>& 
 }
 
 // ---------------------------------------------------------------- groups
-// How the experts of a lane fall into groups, the same for every token: 2^log
-// lanes look at a group, and of[v] is the first of them for expert v * 64 + lane.
-template <int VPT>
+// How the experts fall into groups.  2^log lanes look at a group; a lane's own
+// experts are all of their group where the groups are as many as a power of two
+// and the lanes hold as many experts each.
 struct Groups {
     int log, size;
-    int of[VPT];
+    uint32_t part;                                  // ceil(2^32 / size), size > 1
+    bool whole;
 };
 template <int VPT>
-__device__ inline Groups<VPT> find_groups(const RouteCall& C, int lane) {
-    Groups<VPT> g;
-    g.log = C.rule.n_groups > 1 ? 6 - (32 - __builtin_clz(C.rule.n_groups - 1)) : 0;
-    g.size = C.n_experts / C.rule.n_groups;
-#pragma unroll
-    for (int v = 0; v < VPT; ++v)
-        g.of[v] = C.rule.n_groups > 1 ? min(v * kWave + lane, C.n_experts - 1) / g.size << g.log : 0;
+__device__ inline Groups find_groups(const RouteCall& C) {
+    Groups g;
+    const uint32_t n = C.rule.n_groups;
+    g.log = n > 1 ? 6 - (32 - __builtin_clz(n - 1)) : 0;
+    g.size = C.n_experts / int(n);
+    g.part = 0xFFFFFFFFu / uint32_t(g.size) + 1;
+    g.whole = C.n_experts == VPT * kWave && (n & (n - 1)) == 0;
     return g;
 }
 
@@ -214,31 +215,38 @@ constexpr int padded_size(int vpt) { return vpt * (kWave + kWave / 8); }
 // ranks in fp32 do not tell which do.  `space`: the wave's LDS, padded_size(VPT)
 // keys.
 template <int VPT, class K>
-__device__ inline bool rank_groups(const RouteCall& C, const Groups<VPT>& groups,
-                                   Ranks<VPT, K>& r, int lane, K* space) {
+__device__ inline bool rank_groups(const RouteCall& C, const Groups& groups, Ranks<VPT, K>& r,
+                                   int lane, K* space) {
     typedef typename std::conditional<sizeof(K) == 8, double, float>::type Value;
     const pm_route_rule& rule = C.rule;
     const int n = rule.n_groups, size = groups.size, log = groups.log;
-    K* const own = space + padded_at(lane);
-#pragma unroll
-    for (int v = 0; v < VPT; ++v) own[v * padded_at(kWave)] = r.key[v];
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     const int g = lane >> log, j = lane & ((1 << log) - 1);
     K a = 0, b = 0;                                         // its two largest
-    int base = min(g, n - 1) * size;
-    asm volatile("" : "+v"(base));                          // (addresses are not kept)
-    for (int i0 = j; i0 - j < size; i0 += 8 << log) {
-        K k[8];
+    auto take = [&](K c) {
+        b = max(b, min(a, c));
+        a = max(a, c);
+    };
+    if (groups.whole) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) k[i] = space[padded_at(base + min(i0 + (i << log), size - 1))];
+        for (int v = 0; v < VPT; ++v) take(r.key[v]);
+    } else {
+        int first = lane * VPT;
+        asm volatile("" : "+v"(first));                     // (addresses are not kept)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const K c = i0 + (i << log) < size ? k[i] : K(0);
-            b = max(b, min(a, c));
-            a = max(a, c);
+        for (int v = 0; v < VPT; ++v) space[padded_at(first + v)] = r.key[v];
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        int base = min(g, n - 1) * size;
+        asm volatile("" : "+v"(base));
+        for (int i0 = j; i0 - j < size; i0 += 8 << log) {
+            K k[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                k[i] = space[padded_at(base + min(i0 + (i << log), size - 1))];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) take(i0 + (i << log) < size ? k[i] : K(0));
         }
+        asm volatile("" ::: "memory");                      // (read before the next token's)
     }
-    asm volatile("" ::: "memory");                          // (read before the next token's)
     doublings(log, [&](auto d) {
         K a0, a1, b0, b1;
         both<d>(a, &a0, &a1);
@@ -270,8 +278,19 @@ __device__ inline bool rank_groups(const RouteCall& C, const Groups<VPT>& groups
         if (__ballot(real && !stays && more < rule.top_groups)) return false;
     }
     const uint64_t keep = __ballot(stays);                  // bit of a group: its first lane's
+    if (groups.whole) {
 #pragma unroll
-    for (int v = 0; v < VPT; ++v) r.key[v] = (keep >> groups.of[v]) & 1 ? r.key[v] : K(0);
+        for (int v = 0; v < VPT; ++v) r.key[v] = stays ? r.key[v] : K(0);
+    } else {
+        int first = lane * VPT;
+        asm volatile("" : "+v"(first));
+#pragma unroll
+        for (int v = 0; v < VPT; ++v) {
+            const uint32_t e = uint32_t(min(first + v, C.n_experts - 1));
+            const uint32_t of = size == 1 ? e : __umulhi(e, groups.part);
+            r.key[v] = (keep >> (of << log)) & 1 ? r.key[v] : K(0);
+        }
+    }
     return true;
 }
 
@@ -288,41 +307,69 @@ __device__ inline double exact_score(bool softmax, const Softmax& s, float l) {
     return softmax ? softmax_part(l, s.top) / s.sum : 1.0 / (1.0 + exp(-double(l)));
 }
 
-// A token's logits as they are loaded: every 64th from logit `lane` on (0 past the
-// last).
+// The logits of a token: a lane has VPT adjacent ones.  As they are loaded: one a
+// word, or (16-bit ones of VPT * 64 experts) two.  0 past the last.
 template <int VPT>
 struct RawLogits {
     uint32_t d[VPT];
 };
 template <int VPT>
+__device__ inline bool in_pairs(const RouteCall& C) {
+    return VPT > 1 && C.type != PM_F32 && C.n_experts == VPT * kWave;
+}
+template <int VPT>
 __device__ inline RawLogits<VPT> load_raw(const RouteCall& C, int t, int lane) {
     RawLogits<VPT> l;
     const int log = C.type == PM_F32 ? 2 : 1;
-    const auto row = __builtin_amdgcn_make_buffer_rsrc(
-        uni_ptr(const_cast<char*>(static_cast<const char*>(C.logits)) + (int64_t(t) * C.ld << log)),
-        0, C.n_experts << log, 0x00020000);
-    if (C.type == PM_F32) {
-#pragma unroll
-        for (int v = 0; v < VPT; ++v)
-            l.d[v] = __builtin_amdgcn_raw_buffer_load_b32(row, lane * 4, v * kWave * 4, 0);
+    char* const row =
+        const_cast<char*>(static_cast<const char*>(C.logits)) + (int64_t(t) * C.ld << log);
+    if (C.n_experts == VPT * kWave && C.type == PM_F32) {
+        __builtin_memcpy(l.d, __builtin_assume_aligned(row + lane * VPT * 4, 4), VPT * 4);
+    } else if (in_pairs<VPT>(C)) {
+        // (rows need no alignment beyond their element's)
+        __builtin_memcpy(l.d, row + lane * VPT * 2, VPT * 2);
     } else {
+        const auto buf = __builtin_amdgcn_make_buffer_rsrc(uni_ptr(row), 0, C.n_experts << log,
+                                                           0x00020000);
+        if (C.type == PM_F32) {
 #pragma unroll
-        for (int v = 0; v < VPT; ++v)
-            l.d[v] = uint16_t(__builtin_amdgcn_raw_buffer_load_b16(row, lane * 2, v * kWave * 2, 0));
+            for (int v = 0; v < VPT; ++v)
+                l.d[v] = __builtin_amdgcn_raw_buffer_load_b32(buf, (lane * VPT + v) * 4, 0, 0);
+        } else {
+#pragma unroll
+            for (int v = 0; v < VPT; ++v)
+                l.d[v] = uint16_t(
+                    __builtin_amdgcn_raw_buffer_load_b16(buf, (lane * VPT + v) * 2, 0, 0));
+        }
     }
     return l;
 }
 template <int VPT>
-__device__ inline Logits<VPT> widen(const RouteCall& C, const RawLogits<VPT>& r) {
-    Logits<VPT> l;
+struct Widened {
+    float v[VPT];
+};
+template <int VPT>
+__device__ inline Widened<VPT> widen(const RouteCall& C, const RawLogits<VPT>& r) {
+    Widened<VPT> l;
+    if (C.type == PM_F32) {
 #pragma unroll
-    for (int v = 0; v < VPT; ++v) l.v[v] = __uint_as_float(r.d[v]);
+        for (int v = 0; v < VPT; ++v) l.v[v] = __uint_as_float(r.d[v]);
+        return l;
+    }
+    uint32_t h[VPT];
+    if (in_pairs<VPT>(C)) {
+#pragma unroll
+        for (int v = 0; v < VPT; ++v) h[v] = v & 1 ? r.d[v >> 1] >> 16 : r.d[v >> 1] & 0xFFFFu;
+    } else {
+#pragma unroll
+        for (int v = 0; v < VPT; ++v) h[v] = r.d[v];
+    }
     if (C.type == PM_BF16) {
 #pragma unroll
-        for (int v = 0; v < VPT; ++v) l.v[v] = __uint_as_float(r.d[v] << 16);
-    } else if (C.type == PM_F16) {
+        for (int v = 0; v < VPT; ++v) l.v[v] = __uint_as_float(h[v] << 16);
+    } else {
 #pragma unroll
-        for (int v = 0; v < VPT; ++v) l.v[v] = __half2float(__ushort_as_half(uint16_t(r.d[v])));
+        for (int v = 0; v < VPT; ++v) l.v[v] = __half2float(__ushort_as_half(uint16_t(h[v])));
     }
     return l;
 }
@@ -419,12 +466,12 @@ private:
         uint64_t left = 0;
         const pm_route_rule& rule = C.rule;
         const bool biased = C.bias != nullptr;
-        const Groups<VPT> groups = find_groups<VPT>(C, lane);
+        const Groups groups = find_groups<VPT>(C);
         // -inf: never selected.  (Neither is an expert of a NaN: no rank is one)
         float bias[VPT];
 #pragma unroll
         for (int v = 0; v < VPT; ++v) {
-            const int e = v * kWave + lane;
+            const int e = lane * VPT + v;
             bias[v] = e < C.n_experts ? (biased ? C.bias[e] : 0.0f) : -INFINITY;
         }
         // up to 4 tokens share the exact scores where 16 lanes hold a token's
@@ -437,7 +484,7 @@ private:
             Softmax soft{0.0f, 1.0};
             uint32_t redo = 0;                              // of these
             for (int s = 0; s < group && t + s * step < t1; ++s) {
-                const Logits<VPT> now = widen(C, next);
+                const Widened<VPT> now = widen(C, next);
                 // the next token's logits are on their way meanwhile
                 next = load_raw<VPT>(C, min(t + (s + 1) * step, t1 - 1), lane);
                 Softmax all{-INFINITY, 0.0};
@@ -473,11 +520,12 @@ private:
                 for (int v = 0; v < VPT; ++v) {
                     const bool hit = r.key[v] >= bound;
                     const uint64_t hits = __ballot(hit);
+                    if (hits == 0) continue;
                     const int at = n + __builtin_amdgcn_mbcnt_hi(
                                            uint32_t(hits >> 32),
                                            __builtin_amdgcn_mbcnt_lo(uint32_t(hits), 0));
                     if (hit && at < held)
-                        space->listed[s * held + at] = {v * kWave + lane, now.v[v], bias[v]};
+                        space->listed[s * held + at] = {lane * VPT + v, now.v[v], bias[v]};
                     n += __popcll(hits);
                 }
                 if (!sure || n > held) redo |= 1u << s;
@@ -525,13 +573,13 @@ private:
         return left;
     }
 
-    __device__ static inline Softmax softmax_of(const RouteCall& C, const Logits<VPT>& l, int lane,
+    __device__ static inline Softmax softmax_of(const RouteCall& C, const Widened<VPT>& l, int lane,
                                                 double* x) {
         Softmax all{-INFINITY, 0.0};
         uint32_t big = 0;
 #pragma unroll
         for (int v = 0; v < VPT; ++v)
-            if (v * kWave + lane < C.n_experts) big = max(big, rank_key(l.v[v]));
+            if (lane * VPT + v < C.n_experts) big = max(big, rank_key(l.v[v]));
         doublings(6, [&](auto d) {
             const Pair p = both<d>(big);
             big = max(p.a, p.b);
@@ -539,7 +587,7 @@ private:
         if (big) all.top = rank_value(big);
 #pragma unroll
         for (int v = 0; v < VPT; ++v) {
-            const bool seen = v * kWave + lane < C.n_experts && l.v[v] > -INFINITY;
+            const bool seen = lane * VPT + v < C.n_experts && l.v[v] > -INFINITY;
             x[v] = seen ? softmax_part(l.v[v], all.top) : 0.0;
             all.sum += x[v];
             if (VPT > 4) __builtin_amdgcn_sched_barrier(0);           // (registers)
@@ -551,8 +599,8 @@ private:
     // A token by its exact ranks: the expert (-1: none) and weight of slot `lane`.
     __device__ static inline int rank_again(const RouteCall& C, int t, int lane, Space* space,
                                             float* w) {
-        const Logits<VPT> l = widen(C, load_raw<VPT>(C, t, lane));
-        const Groups<VPT> groups = find_groups<VPT>(C, lane);
+        const Widened<VPT> l = widen(C, load_raw<VPT>(C, t, lane));
+        const Groups groups = find_groups<VPT>(C);
         Softmax soft{0.0f, 1.0};
         Ranks<VPT, uint64_t> r;
         if constexpr (SOFTMAX) {
@@ -561,7 +609,7 @@ private:
         }
 #pragma unroll
         for (int v = 0; v < VPT; ++v) {
-            const int e = v * kWave + lane;
+            const int e = lane * VPT + v;
             const float b = e < C.n_experts ? (C.bias ? C.bias[e] : 0.0f) : -INFINITY;
             r.key[v] = rank_key(exact_score(SOFTMAX, soft, l.v[v]) + double(b),
                                 l.v[v] > -INFINITY && b > -INFINITY);
