@@ -33,6 +33,9 @@ namespace pm {
 
 namespace {
 
+#ifndef XS
+#define XS 2
+#endif
 constexpr int kTileN = 256, kTileK = 128;
 constexpr int kTileThreads = 512, kTileWaves = 8;
 constexpr int kScaleBytes = kTileThreads * 4;        // of a stage: a lane of every wave
@@ -44,6 +47,12 @@ typedef __attribute__((address_space(3))) void lds_void;
 // (kGluSplit: the up matrix begins inside a block of 128 rows).
 enum { kPlain = 0, kGlu = 1, kGluSplit = 2 };
 
+// silu_up to within 2^-16 and |g| 2^-22 of itself: what bf16 results need, whose
+// rounding is 2^-9.  (The exact one takes a twelfth of the kernel's time)
+__device__ inline float silu_up_fast(float g, float u) {
+    return g * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.44269504f)) * u;
+}
+
 // BM rows by 256 weight rows, S stages of 128 inputs in LDS.
 template <int YT, int MODE, int BM, int S>
 __global__ __launch_bounds__(kTileThreads, 2) void fp8_tile_kernel(const GroupedCall C, int nt) {
@@ -54,6 +63,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void fp8_tile_kernel(const Grouped
     constexpr int LA = BM / 64, LB = kTileN / 64, L = LA + LB + 1;  // a wave's loads per stage
     constexpr int WM = BM / 2;                    // rows of a wave: 2 x 4 waves
     constexpr int MB = WM / 16, NB = 4, NP = MB * NB;
+    constexpr int kApart = (NP - NB) / (2 * (L - NB));        // products between two loads
     extern __shared__ __attribute__((aligned(1024))) char smem[];
     int* const ymap = reinterpret_cast<int*>(smem + S * kStage);          // [2][BM]
     int* const before = ymap + 2 * BM;                                    // [E + 1]
@@ -199,29 +209,32 @@ __global__ __launch_bounds__(kTileThreads, 2) void fp8_tile_kernel(const Grouped
     set_rows(cur, u, 0, pa, pb, &ps);
     auto ra = x_buffer(cur), rb = w_buffer(cur), rs = s_buffer(cur);
     int kk = 0;
-    auto issue = [&](int stage) {
-        char* base = smem + stage * kStage + wv * 1024;
+    // load k of the L of stage kk into `stage`: the scales, the rows of x, of W
+    auto issue = [&](int stage, auto which) {
+        constexpr int k = decltype(which)::value;
+        char* base = smem + stage * kStage;
         const bool in = kk * kTileK + piece * 16 < C.cols;
         const int ko = kk * kTileK;
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(
-            rs, (lds_void*)(smem + stage * kStage + kCodes + wv * 256), 4,
-            kk < blocks ? ps : kOutside, kk * 4, 0, 0);
-#pragma unroll
-        for (int i = 0; i < LA; ++i)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void*)(base + i * 8192), 16,
-                                                     in ? pa[i] : kOutside, ko, 0, 0);
-#pragma unroll
-        for (int i = 0; i < LB; ++i)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_void*)(base + kStageA + i * 8192), 16,
-                                                     in ? pb[i] : kOutside, ko, 0, 0);
+        if constexpr (k == 0)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void*)(base + kCodes + wv * 256), 4,
+                                                     kk < blocks ? ps : kOutside, kk * 4, 0, 0);
+        else if constexpr (k <= LA)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                ra, (lds_void*)(base + wv * 1024 + (k - 1) * 8192), 16, in ? pa[k - 1] : kOutside,
+                ko, 0, 0);
+        else
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                rb, (lds_void*)(base + kStageA + wv * 1024 + (k - 1 - LA) * 8192), 16,
+                in ? pb[k - 1 - LA] : kOutside, ko, 0, 0);
     };
-#pragma unroll
-    for (int i = 0; i < S; ++i) {
-        issue(i);
-        ++kk;
-    }
+    // the last stage's loads are under way but for those that go out between the
+    // products of the first
+    for_each<S>([&](auto i) {
+        for_each<(i < S - 1 ? L : NB)>([&](auto k) { issue(i, k); });
+        if (i < S - 1) ++kk;
+    });
     // stage 0 is needed now
-    asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"((S - 1) * L) : "memory");
+    asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"((S - 2) * L + NB) : "memory");
 
     const int off0 = i16 * 128 + ((q ^ (i16 & 7)) * 16);
     const int off1 = i16 * 128 + (((4 + q) ^ (i16 & 7)) * 16);
@@ -331,21 +344,32 @@ __global__ __launch_bounds__(kTileThreads, 2) void fp8_tile_kernel(const Grouped
                     __builtin_amdgcn_sched_barrier(0);
                 };
                 __builtin_amdgcn_sched_barrier(0);
+                // the rest of the loads of the stage before: a few products apart, as
+                // a compute unit takes one in 16 cycles
+                const int before_st = st == 0 ? S - 1 : st - 1;
                 if constexpr (ACT) {
                     for_each<NP - NB>([&](auto k) {
                         step(k, false);
                         constexpr int i = k / NB;
+                        if constexpr (k % kApart == kApart - 1 && k / kApart < L - NB)
+                            issue(before_st, std::integral_constant<int, NB + k / kApart>{});
                         // (behind the first products: a wait for operands in LDS
                         // is one for these, too)
                         if (k == NB - 1) next_scales(min(t + 1, blocks - 1));
                         if (k % NB == NB - 1 && i + 2 < MB) fa[i & 1] = read_a(st, i + 2);
                     });
+                } else {
+                    for_each<L - NB>([&](auto k) {
+                        issue(before_st, std::integral_constant<int, NB + k>{});
+                    });
                 }
+                ++kk;
                 __builtin_amdgcn_sched_barrier(0);
                 // the next stage has arrived, and every wave has read all of this one
                 asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((S - 2) * L)
                              : "memory");
                 __builtin_amdgcn_sched_barrier(0);
+                // (the loads from here on are of the next stage, or the next tile)
                 if (t == T - S) {
                     set_rows(nxt, u, parity ^ 1, pa, pb, &ps);
                     ra = x_buffer(nxt);
@@ -354,16 +378,18 @@ __global__ __launch_bounds__(kTileThreads, 2) void fp8_tile_kernel(const Grouped
                     kk = 0;
                 }
                 __builtin_amdgcn_sched_barrier(0);
-                issue(st);
-                ++kk;
                 if constexpr (ACT) {
                     fa[MB & 1] = read_a(after, 0);
                     for_each<NB>([&](auto k) {
                         step(std::integral_constant<int, NP - NB + k>{}, true);
+                        issue(st, k);
                     });
                     fa[(MB - 1) & 1] = read_a(after, 1);
                     read_s(after);
-                } else if (t == T - 1) {
+                } else {
+                    for_each<NB>([&](auto k) { issue(st, k); });
+                }
+                if (!ACT && t == T - 1) {
                     // the next tile may need this wave
                     fa[0] = read_a(after, 0);
                     fa[1] = read_a(after, 1);
@@ -391,7 +417,9 @@ __global__ __launch_bounds__(kTileThreads, 2) void fp8_tile_kernel(const Grouped
                     for (int j = 0; j < 4; j += 2) {
                         float v[4];
 #pragma unroll
-                        for (int r = 0; r < 4; ++r) v[r] = silu_up(acc[i][j][r], acc[i][j + 1][r]);
+                        for (int r = 0; r < 4; ++r)
+                            v[r] = NATIVE ? silu_up_fast(acc[i][j][r], acc[i][j + 1][r])
+                                          : silu_up(acc[i][j][r], acc[i][j + 1][r]);
                         store4<YT>(C.y, at + o + 2 * j, out - o - 2 * j, v);
                     }
                 } else {
@@ -450,8 +478,8 @@ hipError_t launch_fp8_tiles(const GroupedCall& C, int rows, hipStream_t st) {
     if (C.y_type == PM_BF16)
         return rows == 256 ? run_tiles8_mode<PM_BF16, 256, 2>(C, st)
                            : run_tiles8_mode<PM_BF16, 128, 3>(C, st);
-    return C.y_type == PM_F16 ? run_tiles8_mode<PM_F16, 128, 2>(C, st)
-                              : run_tiles8_mode<PM_F32, 128, 2>(C, st);
+    return C.y_type == PM_F16 ? run_tiles8_mode<PM_F16, 128, XS>(C, st)
+                              : run_tiles8_mode<PM_F32, 128, XS>(C, st);
 }
 
 }  // namespace pm
