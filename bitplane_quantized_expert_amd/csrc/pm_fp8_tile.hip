@@ -33,14 +33,29 @@ namespace pm {
 
 namespace {
 
-#ifndef XS
-#define XS 2
-#endif
 constexpr int kTileN = 256, kTileK = 128;
 constexpr int kTileThreads = 512, kTileWaves = 8;
 constexpr int kScaleBytes = kTileThreads * 4;        // of a stage: a lane of every wave
 
 typedef __attribute__((address_space(3))) void lds_void;
+
+// N adjacent outputs of row y + at, those below `left`, 16 bytes at a time.
+template <int YT, int N>
+__device__ inline void store_row(void* y, int64_t at, int left, const float* v) {
+    constexpr int B = YT == PM_F32 ? 4 : 2, P = 16 / B;
+    if (left >= N) {
+#pragma unroll
+        for (int k = 0; k < N; k += P) {
+            alignas(16) char o[16];
+#pragma unroll
+            for (int r = 0; r < P; ++r) store_f32<YT>(o, r, v[k + r]);
+            __builtin_memcpy(static_cast<char*>(y) + (at + k) * B, o, 16);
+        }
+        return;
+    }
+#pragma unroll
+    for (int k = 0; k < N; k += 4) store4<YT>(y, at + k, left - k, v + k);
+}
 
 // How the scales of the weight rows of a wave fall: one for all (kPlain), one
 // for gate and one for up rows (kGlu), or up rows on both sides of a border
@@ -234,7 +249,9 @@ __global__ __launch_bounds__(kTileThreads, 2) void fp8_tile_kernel(const Grouped
         if (i < S - 1) ++kk;
     });
     // stage 0 is needed now
-    asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"((S - 2) * L + NB) : "memory");
+    // three stages: and stage 1 in the first step
+    asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(S > 2 ? (S - 3) * L + NB : NB)
+                 : "memory");
 
     const int off0 = i16 * 128 + ((q ^ (i16 & 7)) * 16);
     const int off1 = i16 * 128 + (((4 + q) ^ (i16 & 7)) * 16);
@@ -366,8 +383,13 @@ __global__ __launch_bounds__(kTileThreads, 2) void fp8_tile_kernel(const Grouped
                 ++kk;
                 __builtin_amdgcn_sched_barrier(0);
                 // the next stage has arrived, and every wave has read all of this one
-                asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((S - 2) * L)
-                             : "memory");
+                // (with three stages the first step's has been waited for before the
+                // last tile's stores went out: loads and stores complete in order)
+                if (S > 2 && t == 0)
+                    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+                else
+                    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((S - 2) * L)
+                                 : "memory");
                 __builtin_amdgcn_sched_barrier(0);
                 // (the loads from here on are of the next stage, or the next tile)
                 if (t == T - S) {
@@ -400,6 +422,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void fp8_tile_kernel(const Grouped
                 __builtin_amdgcn_sched_barrier(0);
                 st = after;
             }
+            if (S > 2) asm volatile("s_waitcnt vmcnt(%0)" ::"n"((S - 3) * L + NB) : "memory");
         };
         if (act) {
             steps(std::true_type{});
@@ -411,25 +434,20 @@ __global__ __launch_bounds__(kTileThreads, 2) void fp8_tile_kernel(const Grouped
                 const int yr = rows[i * 16];
                 if (yr < 0) continue;
                 const int64_t at = int64_t(yr) * C.ldy;
-                if constexpr (GLU) {
-                    const int o = cur.o0 + wn * 32 + q * 8;
+                // this lane's adjacent outputs: 8 of gate and up, else 16
+                float v[GLU ? 8 : 16];
 #pragma unroll
-                    for (int j = 0; j < 4; j += 2) {
-                        float v[4];
+                for (int j = 0; j < 4; j += GLU ? 2 : 1)
 #pragma unroll
-                        for (int r = 0; r < 4; ++r)
-                            v[r] = NATIVE ? silu_up_fast(acc[i][j][r], acc[i][j + 1][r])
-                                          : silu_up(acc[i][j][r], acc[i][j + 1][r]);
-                        store4<YT>(C.y, at + o + 2 * j, out - o - 2 * j, v);
+                    for (int r = 0; r < 4; ++r) {
+                        if constexpr (GLU)
+                            v[2 * j + r] = NATIVE ? silu_up_fast(acc[i][j][r], acc[i][j + 1][r])
+                                                  : silu_up(acc[i][j][r], acc[i][j + 1][r]);
+                        else
+                            v[4 * j + r] = acc[i][j][r];
                     }
-                } else {
-                    const int o = cur.o0 + wn * 64 + q * 16;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float v[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
-                        store4<YT>(C.y, at + o + 4 * j, out - o - 4 * j, v);
-                    }
-                }
+                const int o = cur.o0 + (GLU ? wn * 32 + q * 8 : wn * 64 + q * 16);
+                store_row<YT, GLU ? 8 : 16>(C.y, at + o, out - o, v);
             }
         } else {
             steps(std::false_type{});
@@ -470,6 +488,12 @@ hipError_t run_tiles8_mode(const GroupedCall& C, hipStream_t st) {
     return run_tiles8<YT, kGluSplit, BM, S>(C, st);
 }
 
+template <int YT>
+hipError_t run_exact(const GroupedCall& C, hipStream_t st) {
+    return tile_lds(C, 128, 3) <= kTileMaxLds ? run_tiles8_mode<YT, 128, 3>(C, st)
+                                              : run_tiles8_mode<YT, 128, 2>(C, st);
+}
+
 }  // namespace
 
 bool fp8_tiles128_fit(const GroupedCall& C) { return tile_lds(C, 128, 3) <= kTileMaxLds; }
@@ -478,8 +502,8 @@ hipError_t launch_fp8_tiles(const GroupedCall& C, int rows, hipStream_t st) {
     if (C.y_type == PM_BF16)
         return rows == 256 ? run_tiles8_mode<PM_BF16, 256, 2>(C, st)
                            : run_tiles8_mode<PM_BF16, 128, 3>(C, st);
-    return C.y_type == PM_F16 ? run_tiles8_mode<PM_F16, 128, XS>(C, st)
-                              : run_tiles8_mode<PM_F32, 128, XS>(C, st);
+    return C.y_type == PM_F16 ? run_exact<PM_F16>(C, st)
+                              : run_exact<PM_F32>(C, st);
 }
 
 }  // namespace pm
