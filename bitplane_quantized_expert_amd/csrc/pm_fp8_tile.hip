@@ -113,7 +113,8 @@ __global__ __launch_bounds__(kTileThreads, 2) void fp8_tile_kernel(const Grouped
         if (i < n_tiles) {
             const int mt = i / nt;
             const int e = tile_expert(C, before, mt);
-            const RowRange g = group_rows(C, e);
+            // (by scalar loads: a wait for vector loads is one for the stages, too)
+            const RowRange g = group_rows_uniform(C, e);
             const int64_t skip = int64_t(mt - before[e]) * BM;
             const bool ok = skip >= 0 && skip < g.n;      // (not so only for bad offsets)
             w.e = uni(e);
@@ -135,17 +136,20 @@ __global__ __launch_bounds__(kTileThreads, 2) void fp8_tile_kernel(const Grouped
     const int p_row = wv < BM / 64 ? (wv * 64 + lane) / WM * WM + (lane & (MB - 1)) * 16 +
                                          ((wv * 64 + lane) % WM) / MB
                                    : BM;
-    auto use_rows = [&](const Where& w, int* u) {
+    // the uses of this lane's rows and of that of its scale, as they are loaded
+    auto load_uses = [&](const Where& w, int* raw) {
 #pragma unroll
-        for (int i = 0; i < LA; ++i) {
-            const int r = (i * kTileWaves + wv) * 8 + r8;
-            u[i] = r < w.n ? use_of(C, w.row0 + r) : -1;
+        for (int i = 0; i <= LA; ++i) {
+            const int r = i < LA ? (i * kTileWaves + wv) * 8 + r8 : p_row;
+            raw[i] = r < w.n ? w.row0 + r : -1;
+            if (C.order && raw[i] >= 0) raw[i] = C.order[raw[i]];
         }
-        u[LA] = p_row < w.n ? use_of(C, w.row0 + p_row) : -1;
     };
-    // offsets of this lane's rows of x, of their scales and of W per stage
-    auto set_rows = [&](const Where& w, const int* u, int parity, uint32_t* pa, uint32_t* pb,
-                        uint32_t* ps) {
+    // offsets of this lane's rows of x and of their scales, and of W per stage
+    auto set_x = [&](const Where& w, const int* raw, int parity, uint32_t* pa, uint32_t* ps) {
+        int u[LA + 1];
+#pragma unroll
+        for (int i = 0; i <= LA; ++i) u[i] = raw[i] < C.n_rows ? max(raw[i], -1) : -1;
 #pragma unroll
         for (int i = 0; i < LA; ++i) {
             const int r = (i * kTileWaves + wv) * 8 + r8;
@@ -157,6 +161,8 @@ __global__ __launch_bounds__(kTileThreads, 2) void fp8_tile_kernel(const Grouped
         }
         const uint32_t sr = gather ? uint32_t(u[LA]) / uint32_t(C.top_k) : uint32_t(p_row);
         *ps = u[LA] >= 0 ? sr * uint32_t(blocks) * 4 : kOutside;
+    };
+    auto set_w = [&](const Where& w, uint32_t* pb) {
 #pragma unroll
         for (int i = 0; i < LB; ++i) {
             const int r = (i * kTileWaves + wv) * 8 + r8;
@@ -220,8 +226,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void fp8_tile_kernel(const Grouped
     int u[LA + 1];
     Where cur = locate(place), nxt;
     if (cur.n == 0) return;
-    use_rows(cur, u);
-    set_rows(cur, u, 0, pa, pb, &ps);
+    set_w(cur, pb);
     auto ra = x_buffer(cur), rb = w_buffer(cur), rs = s_buffer(cur);
     int kk = 0;
     // load k of the L of stage kk into `stage`: the scales, the rows of x, of W
@@ -242,16 +247,19 @@ __global__ __launch_bounds__(kTileThreads, 2) void fp8_tile_kernel(const Grouped
                 rb, (lds_void*)(base + kStageA + wv * 1024 + (k - 1 - LA) * 8192), 16,
                 in ? pb[k - 1 - LA] : kOutside, ko, 0, 0);
     };
-    // the last stage's loads are under way but for those that go out between the
-    // products of the first
-    for_each<S>([&](auto i) {
-        for_each<(i < S - 1 ? L : NB)>([&](auto k) { issue(i, k); });
-        if (i < S - 1) ++kk;
+    // the first stages, that of W in the first while the uses are on their way; the
+    // last loads of the last go out between the products of the first
+    load_uses(cur, u);
+    asm volatile("" ::: "memory");
+    for_each<LB>([&](auto k) { issue(0, std::integral_constant<int, 1 + LA + k>{}); });
+    set_x(cur, u, 0, pa, &ps);
+    for_each<1 + LA>([&](auto k) { issue(0, k); });
+    for_each<S - 1>([&](auto i) {
+        ++kk;
+        for_each<(i < S - 2 ? L : NB)>([&](auto k) { issue(i + 1, k); });
     });
-    // stage 0 is needed now
-    // three stages: and stage 1 in the first step
-    asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(S > 2 ? (S - 3) * L + NB : NB)
-                 : "memory");
+    // stage 0 is needed now; three stages: and stage 1 in the first step
+    asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(NB) : "memory");
 
     const int off0 = i16 * 128 + ((q ^ (i16 & 7)) * 16);
     const int off1 = i16 * 128 + (((4 + q) ^ (i16 & 7)) * 16);
@@ -284,7 +292,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void fp8_tile_kernel(const Grouped
     for (int tile = place; cur.n > 0; tile += gridDim.x) {
         // the next tile's place and uses, long before its first loads
         nxt = locate(tile + gridDim.x);
-        use_rows(nxt, u);
+        load_uses(nxt, u);
         const bool act = cur.n > wm * WM;
         const WScales wsc = w_scales(cur);
         // up rows past the border of a block of 128 rows, bit (j / 2) * 4 + r
@@ -393,7 +401,8 @@ __global__ __launch_bounds__(kTileThreads, 2) void fp8_tile_kernel(const Grouped
                 __builtin_amdgcn_sched_barrier(0);
                 // (the loads from here on are of the next stage, or the next tile)
                 if (t == T - S) {
-                    set_rows(nxt, u, parity ^ 1, pa, pb, &ps);
+                    set_x(nxt, u, parity ^ 1, pa, &ps);
+                    set_w(nxt, pb);
                     ra = x_buffer(nxt);
                     rb = w_buffer(nxt);
                     rs = s_buffer(nxt);
