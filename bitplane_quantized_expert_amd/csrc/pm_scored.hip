@@ -97,8 +97,12 @@ __device__ inline float rank_value(uint32_t k) {
 __device__ inline double rank_value(uint64_t k) {
     return __builtin_bit_cast(double, k ^ (k >> 63 ? 1ull << 63 : ~0ull));
 }
-__device__ inline uint32_t top32(uint32_t k) { return k; }
-__device__ inline uint32_t top32(uint64_t k) { return uint32_t(k >> 32); }
+
+// The lanes below this one among those of a ballot.
+__device__ inline int lanes_below(uint64_t lanes) {
+    return __builtin_amdgcn_mbcnt_hi(uint32_t(lanes >> 32),
+                                     __builtin_amdgcn_mbcnt_lo(uint32_t(lanes), 0));
+}
 
 __device__ inline float lane_value(float v, int lane) {
     return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), lane));
@@ -110,27 +114,31 @@ __device__ inline double lane_value(double v, int lane) {
                     uint32_t(__builtin_amdgcn_readlane(int(b), lane)));
 }
 
-// What a rank in fp32 may be off by, doubled and more.  The score: e^-l from
-// v_exp_f32 has an error of |l| 2^-22 of it at most, 1 / (1 + e) and e / sum by
-// v_rcp_f32 a few 2^-24 more; so 2^-20 of 1, and 2^-16 of the score itself.  The
-// sum with a bias is rounded to 2^-24 of it.
+// What a rank in fp32 may be off by, at least doubled.  A sigmoid 1 / (1 + e),
+// e = e^-l: the exponent of v_exp_f32 is rounded twice, e by an ulp, so that e has
+// an error of |l| 2^-23.7 + 2^-23 of it, which the score takes times s (1 - s):
+// 2^-24.5 together, as that is 1/4 at most and |l| times it 0.23.  The sum and
+// v_rcp_f32's ulp are 2^-23 + 2^-24 more, so the score is off by 2^-22 at most; a
+// softmax's e / sum, with five roundings of half an ulp, by 2^-21.6 of it.  The sum
+// with a bias is rounded to 2^-24 of it.
+__device__ inline float rank_error(float size) { return 0x1p-20f + size * 0x1p-23f; }
+
+// How far below a rank in fp32 another may be and still come before it.  Scores
+// without a bias tell small ones apart as well: they are off by 2^-17 of
+// themselves (|l| < 88 where they are not 0), or what is lost below 2^-126.
 __device__ inline float rank_slack(float v, bool bias) {
-    return bias ? 0x1p-18f + fabsf(v) * 0x1p-21f : fminf(0x1p-18f, v * 0x1p-14f);
+    const float slack = 2.0f * rank_error(fabsf(v));
+    return bias ? slack : fminf(slack, v * 0x1p-14f + 0x1p-124f);
 }
 
-// K: uint32_t (ranks in fp32) or uint64_t (exact).
-template <int VPT, class K>
-struct Ranks {
-    K key[VPT];
+template <int VPT>
+struct Ranks {                                      // in fp32
+    uint32_t key[VPT];
 };
 
-// A bound that the top_k largest keys meet, as their top halves: at least top_k
-// of the lanes' own largest do, just top_k if any value tells so many apart.
-template <int VPT, class K>
-__device__ inline uint32_t rank_bound(const Ranks<VPT, K>& r, int top_k) {
-    uint32_t m = top32(r.key[0]);
-#pragma unroll
-    for (int v = 1; v < VPT; ++v) m = max(m, top32(r.key[v]));
+// A bound that the top_k largest keys meet: at least top_k of the lanes' own
+// largest (m) do, just top_k if any value tells so many apart.
+__device__ inline uint32_t rank_bound(uint32_t m, int top_k) {
     uint32_t hi = m, lo = m;
     doublings(6, [&](auto d) {
         const Pair h = both<d>(hi), l = both<d>(lo);
@@ -150,43 +158,6 @@ __device__ inline uint32_t rank_bound(const Ranks<VPT, K>& r, int top_k) {
     return lo;
 }
 
-// The experts with the largest exact ranks, sorted across the lanes, ties by lower
-// id: lane j gets the id of place j (-1: none).
-template <int VPT>
-__device__ inline int rank_list(const RouteCall& C, const Ranks<VPT, uint64_t>& r, int lane) {
-    const uint32_t bound = max(rank_bound(r, C.top_k), 1u);
-    // list across the lanes, descending: (key, ~expert), 0 for none
-    uint64_t mine = 0;
-    uint32_t low = 0;
-#pragma unroll
-    for (int v = 0; v < VPT; ++v) {
-        uint64_t hit = __ballot(top32(r.key[v]) >= bound);
-        while (hit) {
-            const int l = __builtin_ctzll(hit);
-            hit &= hit - 1;
-            const uint64_t k = uint64_t(uint32_t(__builtin_amdgcn_readlane(int(r.key[v] >> 32), l))) << 32 |
-                               uint32_t(__builtin_amdgcn_readlane(int(r.key[v]), l));
-            const uint32_t ne = ~uint32_t(l * VPT + v);
-            // lanes that come after it move up by one, the first takes it
-            const bool after = mine < k || (mine == k && low < ne);
-            const uint64_t mask = __ballot(after);
-            if (mask == 0) continue;
-            const int first = __builtin_ctzll(mask);
-            const uint32_t hi_up = __shfl_up(uint32_t(mine >> 32), 1), lo_up = __shfl_up(uint32_t(mine), 1);
-            const uint32_t low_up = __shfl_up(low, 1);
-            if (after) {
-                mine = uint64_t(hi_up) << 32 | lo_up;
-                low = low_up;
-            }
-            if (lane == first) {
-                mine = k;
-                low = ne;
-            }
-        }
-    }
-    return mine && lane < C.top_k ? int(~low) : -1;
-}
-
 // ---------------------------------------------------------------- groups
 // How the experts fall into groups.  2^log lanes look at a group; a lane's own
 // experts are all of their group where the groups are as many as a power of two
@@ -195,6 +166,8 @@ struct Groups {
     int log, size;
     uint32_t part;                                  // ceil(2^32 / size), size > 1
     bool whole;
+
+    __device__ inline int of(int e) const { return size == 1 ? e : __umulhi(uint32_t(e), part); }
 };
 template <int VPT>
 __device__ inline Groups find_groups(const RouteCall& C) {
@@ -207,6 +180,26 @@ __device__ inline Groups find_groups(const RouteCall& C) {
     return g;
 }
 
+// The two largest keys of a group.
+template <class K>
+struct TwoLargest {
+    K a = 0, b = 0;
+
+    __device__ inline void take(K c) {
+        b = max(b, min(a, c));
+        a = max(a, c);
+    }
+    __device__ inline void join(int log) {          // those of 2^log lanes
+        doublings(log, [&](auto d) {
+            K a0, a1, b0, b1;
+            both<d>(a, &a0, &a1);
+            both<d>(b, &b0, &b1);
+            a = max(a0, a1);
+            b = max(min(a0, a1), max(b0, b1));
+        });
+    }
+};
+
 // Places apart in LDS of experts that the lanes of several groups read at once.
 __device__ inline int padded_at(int e) { return e + (e >> 3); }
 constexpr int padded_size(int vpt) { return vpt * (kWave + kWave / 8); }
@@ -214,21 +207,16 @@ constexpr int padded_size(int vpt) { return vpt * (kWave + kWave / 8); }
 // Takes the experts of the groups that do not stay out of the ranks; false where
 // ranks in fp32 do not tell which do.  `space`: the wave's LDS, padded_size(VPT)
 // keys.
-template <int VPT, class K>
-__device__ inline bool rank_groups(const RouteCall& C, const Groups& groups, Ranks<VPT, K>& r,
-                                   int lane, K* space) {
-    typedef typename std::conditional<sizeof(K) == 8, double, float>::type Value;
+template <int VPT>
+__device__ inline bool rank_groups(const RouteCall& C, const Groups& groups, Ranks<VPT>& r,
+                                   int lane, uint32_t* space) {
     const pm_route_rule& rule = C.rule;
     const int n = rule.n_groups, size = groups.size, log = groups.log;
     const int g = lane >> log, j = lane & ((1 << log) - 1);
-    K a = 0, b = 0;                                         // its two largest
-    auto take = [&](K c) {
-        b = max(b, min(a, c));
-        a = max(a, c);
-    };
+    TwoLargest<uint32_t> two;
     if (groups.whole) {
 #pragma unroll
-        for (int v = 0; v < VPT; ++v) take(r.key[v]);
+        for (int v = 0; v < VPT; ++v) two.take(r.key[v]);
     } else {
         int first = lane * VPT;
         asm volatile("" : "+v"(first));                     // (addresses are not kept)
@@ -238,57 +226,43 @@ __device__ inline bool rank_groups(const RouteCall& C, const Groups& groups, Ran
         int base = min(g, n - 1) * size;
         asm volatile("" : "+v"(base));
         for (int i0 = j; i0 - j < size; i0 += 8 << log) {
-            K k[8];
+            uint32_t k[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 k[i] = space[padded_at(base + min(i0 + (i << log), size - 1))];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) take(i0 + (i << log) < size ? k[i] : K(0));
+            for (int i = 0; i < 8; ++i) two.take(i0 + (i << log) < size ? k[i] : 0u);
         }
         asm volatile("" ::: "memory");                      // (read before the next token's)
     }
-    doublings(log, [&](auto d) {
-        K a0, a1, b0, b1;
-        both<d>(a, &a0, &a1);
-        both<d>(b, &b0, &b1);
-        a = max(a0, a1);
-        b = max(min(a0, a1), max(b0, b1));
-    });
-    const bool real = g < n && a != 0;
-    Value mine = real ? rank_value(a) : Value(-INFINITY);
-    if (rule.group_best == 2 && b != 0) mine += rank_value(b);
-    bool stays;
-    if constexpr (sizeof(K) == 8) {
-        int more = 0;
-        for (int k = 0; k < n; ++k) {
-            const double o = lane_value(mine, k << log);
-            more += o > mine || (o == mine && k < g);
-        }
-        stays = real && more < rule.top_groups;
-    } else {
-        // groups that count more for certain, and those that may
-        const float slack = 4.0f * (0x1p-18f + fabsf(mine) * 0x1p-21f);
-        int more = 0, maybe = -1;
-        for (int k = 0; k < n; ++k) {
-            const float o = lane_value(mine, k << log);
-            more += o > mine + slack;
-            maybe += !(o < mine - slack);
-        }
-        stays = real && maybe < rule.top_groups;
-        if (__ballot(real && !stays && more < rule.top_groups)) return false;
+    two.join(log);
+    const bool real = g < n && two.a != 0;
+    float mine = real ? rank_value(two.a) : -INFINITY, second = 0.0f;
+    if (rule.group_best == 2 && two.b != 0) second = rank_value(two.b);
+    // groups that count more for certain, and those that may: by the ends of what
+    // each may count (two ranks, and their sum)
+    const float off = 2.0f * rank_error(fabsf(mine) + fabsf(second));
+    mine += second;
+    const float low = real ? mine - off : mine, high = real ? mine + off : mine;
+    int more = 0, maybe = -1;
+    for (int k = 0; k < n; ++k) {
+        const float o = lane_value(low, k << log), p = lane_value(high, k << log);
+        more += o > high;
+        maybe += !(p < low);
     }
+    const bool stays = real && maybe < rule.top_groups;
+    if (__ballot(real && !stays && more < rule.top_groups)) return false;
     const uint64_t keep = __ballot(stays);                  // bit of a group: its first lane's
     if (groups.whole) {
 #pragma unroll
-        for (int v = 0; v < VPT; ++v) r.key[v] = stays ? r.key[v] : K(0);
+        for (int v = 0; v < VPT; ++v) r.key[v] = stays ? r.key[v] : 0u;
     } else {
         int first = lane * VPT;
         asm volatile("" : "+v"(first));
 #pragma unroll
         for (int v = 0; v < VPT; ++v) {
-            const uint32_t e = uint32_t(min(first + v, C.n_experts - 1));
-            const uint32_t of = size == 1 ? e : __umulhi(e, groups.part);
-            r.key[v] = (keep >> (of << log)) & 1 ? r.key[v] : K(0);
+            const int of = groups.of(min(first + v, C.n_experts - 1));
+            r.key[v] = (keep >> (of << log)) & 1 ? r.key[v] : 0u;
         }
     }
     return true;
@@ -444,16 +418,9 @@ struct ScoredRouter {
             uint64_t redo = rank_tokens(C, t0, min(t1 - t0, kWave * step) + t0, step, lane, space, f);
             for (; redo; redo &= redo - 1) {
                 const int t = t0 + __builtin_ctzll(redo) * step;
-                float w;
                 int own = lane;
                 asm volatile("" : "+v"(own));               // (nothing of it is kept)
-                const int e = rank_again(C, t, own, space, &w);
-                if (lane < C.top_k) {
-                    const int64_t u = int64_t(t) * C.top_k + lane;
-                    C.ids[u] = e;
-                    C.w[u] = w;
-                    if (e >= 0) f(u, e);
-                }
+                rank_again(C, t, own, space, f);
             }
         }
     }
@@ -488,7 +455,7 @@ private:
                 // the next token's logits are on their way meanwhile
                 next = load_raw<VPT>(C, min(t + (s + 1) * step, t1 - 1), lane);
                 Softmax all{-INFINITY, 0.0};
-                Ranks<VPT, uint32_t> r;
+                Ranks<VPT> r;
                 if constexpr (SOFTMAX) {
                     double x[VPT];
                     all = softmax_of(C, now, lane, x);
@@ -509,7 +476,10 @@ private:
                     sure = rank_groups<VPT>(C, groups, r, lane,
                                             reinterpret_cast<uint32_t*>(space->key));
                 // all that may be among the top_k, into this token's lanes
-                uint32_t bound = rank_bound(r, C.top_k);
+                uint32_t most = r.key[0];
+#pragma unroll
+                for (int v = 1; v < VPT; ++v) most = max(most, r.key[v]);
+                uint32_t bound = rank_bound(most, C.top_k);
                 if (bound) {
                     const float v = rank_value(bound);
                     bound = rank_key(v - rank_slack(v, biased));
@@ -521,9 +491,7 @@ private:
                     const bool hit = r.key[v] >= bound;
                     const uint64_t hits = __ballot(hit);
                     if (hits == 0) continue;
-                    const int at = n + __builtin_amdgcn_mbcnt_hi(
-                                           uint32_t(hits >> 32),
-                                           __builtin_amdgcn_mbcnt_lo(uint32_t(hits), 0));
+                    const int at = n + lanes_below(hits);
                     if (hit && at < held)
                         space->listed[s * held + at] = {lane * VPT + v, now.v[v], bias[v]};
                     n += __popcll(hits);
@@ -573,6 +541,15 @@ private:
         return left;
     }
 
+    // The largest logit, by the largest of the lanes' keys.
+    __device__ static inline float top_of(uint32_t big) {
+        doublings(6, [&](auto d) {
+            const Pair p = both<d>(big);
+            big = max(p.a, p.b);
+        });
+        return big ? rank_value(big) : -INFINITY;
+    }
+
     __device__ static inline Softmax softmax_of(const RouteCall& C, const Widened<VPT>& l, int lane,
                                                 double* x) {
         Softmax all{-INFINITY, 0.0};
@@ -580,11 +557,7 @@ private:
 #pragma unroll
         for (int v = 0; v < VPT; ++v)
             if (lane * VPT + v < C.n_experts) big = max(big, rank_key(l.v[v]));
-        doublings(6, [&](auto d) {
-            const Pair p = both<d>(big);
-            big = max(p.a, p.b);
-        });
-        if (big) all.top = rank_value(big);
+        all.top = top_of(big);
 #pragma unroll
         for (int v = 0; v < VPT; ++v) {
             const bool seen = lane * VPT + v < C.n_experts && l.v[v] > -INFINITY;
@@ -596,36 +569,161 @@ private:
         return all;
     }
 
-    // A token by its exact ranks: the expert (-1: none) and weight of slot `lane`.
-    __device__ static inline int rank_again(const RouteCall& C, int t, int lane, Space* space,
-                                            float* w) {
-        const Widened<VPT> l = widen(C, load_raw<VPT>(C, t, lane));
-        const Groups groups = find_groups<VPT>(C);
-        Softmax soft{0.0f, 1.0};
-        Ranks<VPT, uint64_t> r;
-        if constexpr (SOFTMAX) {
-            double x[VPT];
-            soft = softmax_of(C, l, lane, x);
-        }
+    // A token by its exact ranks.  One wave in some hundred comes here, and the
+    // rest may wait for it: its time is that of fetching the code, which loops over
+    // ranks in LDS keep short.  Expert v * 64 + lane is a lane's v-th.
+    template <class F>
+    __device__ static inline void rank_again(const RouteCall& C, int t, int lane, Space* space,
+                                             F&& f) {
+        constexpr int kAt = VPT < 8 ? VPT : 8;      // loads on their way together
+        const pm_route_rule& rule = C.rule;
+        uint64_t* const keys = space->key;
+        auto at = [&](int v) { return padded_at(v * kWave + lane); };
+        // logits and biases, as they are; NaN where there is no expert
+        uint32_t big = 0;
+#pragma unroll 1
+        for (int v0 = 0; v0 < VPT; v0 += kAt) {
+            float l[kAt], b[kAt];
 #pragma unroll
-        for (int v = 0; v < VPT; ++v) {
-            const int e = lane * VPT + v;
-            const float b = e < C.n_experts ? (C.bias ? C.bias[e] : 0.0f) : -INFINITY;
-            r.key[v] = rank_key(exact_score(SOFTMAX, soft, l.v[v]) + double(b),
-                                l.v[v] > -INFINITY && b > -INFINITY);
-            if (VPT > 4) __builtin_amdgcn_sched_barrier(0);           // (registers)
+            for (int i = 0; i < kAt; ++i) {
+                const int e = min((v0 + i) * kWave + lane, C.n_experts - 1);
+                l[i] = logit(C, t, e);
+                b[i] = C.bias ? C.bias[e] : 0.0f;
+            }
+#pragma unroll
+            for (int i = 0; i < kAt; ++i) {
+                if ((v0 + i) * kWave + lane >= C.n_experts) l[i] = NAN;
+                big = max(big, rank_key(l[i]));
+                keys[at(v0 + i)] = uint64_t(__float_as_uint(b[i])) << 32 | __float_as_uint(l[i]);
+            }
         }
-        if (C.rule.n_groups > 1) rank_groups<VPT>(C, groups, r, lane, space->key);
-        const int id = rank_list<VPT>(C, r, lane);
+        Softmax soft{-INFINITY, 0.0};
+        if constexpr (SOFTMAX) {
+            soft.top = top_of(big);
+#pragma unroll 1
+            for (int v = 0; v < VPT; ++v) {
+                const float l = __uint_as_float(uint32_t(keys[at(v)]));
+                if (l > -INFINITY) soft.sum += softmax_part(l, soft.top);
+            }
+            soft.sum = wave_sum_f64(soft.sum);
+        }
+#pragma unroll 1
+        for (int v = 0; v < VPT; ++v) {
+            const uint64_t k = keys[at(v)];
+            const float l = __uint_as_float(uint32_t(k)), b = __uint_as_float(uint32_t(k >> 32));
+            keys[at(v)] = rank_key(exact_score(SOFTMAX, soft, l) + double(b),
+                                   l > -INFINITY && b > -INFINITY);
+        }
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        if (rule.n_groups > 1) {
+            const Groups groups = find_groups<VPT>(C);
+            const int n = rule.n_groups, log = groups.log, g = lane >> log;
+            TwoLargest<uint64_t> two;
+#pragma unroll 1
+            for (int i = lane & ((1 << log) - 1); i < groups.size; i += 1 << log)
+                two.take(keys[padded_at(min(g, n - 1) * groups.size + i)]);
+            two.join(log);
+            const bool real = g < n && two.a != 0;
+            double mine = real ? rank_value(two.a) : -double(INFINITY);
+            if (rule.group_best == 2 && two.b != 0) mine += rank_value(two.b);
+            int more = 0;
+#pragma unroll 1
+            for (int k = 0; k < n; ++k) {
+                const double o = lane_value(mine, k << log);
+                more += o > mine || (o == mine && k < g);
+            }
+            const uint64_t keep = __ballot(real && more < rule.top_groups);
+#pragma unroll 1
+            for (int v = 0; v < VPT; ++v) {
+                const int of = groups.of(min(v * kWave + lane, C.n_experts - 1));
+                if (!((keep >> (of << log)) & 1)) keys[at(v)] = 0;
+            }
+        }
+        uint32_t most = 0;
+#pragma unroll 1
+        for (int v = 0; v < VPT; ++v) most = max(most, uint32_t(keys[at(v)] >> 32));
+        // those above `least`, and `equal` of those that equal it
+        uint64_t least = uint64_t(max(rank_bound(most, C.top_k), 1u)) << 32;
+        int n = list_above(least, kWave, lane, space);
+        if (n > kWave) {
+            // more than the list holds: the top_k-th largest itself
+            uint64_t lo = ~0ull, hi = 0;
+#pragma unroll 1
+            for (int v = 0; v < VPT; ++v) {
+                const uint64_t k = keys[at(v)];
+                hi = max(hi, k);
+                if (k >= least) lo = min(lo, k);
+            }
+            doublings(6, [&](auto d) {
+                uint64_t a, b;
+                both<d>(hi, &a, &b);
+                hi = max(a, b);
+                both<d>(lo, &a, &b);
+                lo = min(a, b);
+            });
+            lo = uni64(lo);
+            hi = uni64(hi);
+            while (lo < hi) {
+                const uint64_t c = lo + ((hi - lo) >> 1) + 1;
+                if (met_by(c, lane, space) >= C.top_k)
+                    lo = c;
+                else
+                    hi = c - 1;
+            }
+            n = list_above(lo, C.top_k - (lo == ~0ull ? 0 : met_by(lo + 1, lane, space)), lane,
+                           space);
+        }
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        int id = -1;
+        uint64_t key = 0;
         double x = 0.0;
-        if (id >= 0)
-            x = exact_score(SOFTMAX, soft, logit(C, t, id));
-        if (C.rule.flags & PM_ROUTE_RENORM) {
+        if (lane < n) {
+            id = space->listed[lane].id;
+            key = keys[padded_at(id)];
+        }
+        asm volatile("" ::: "memory");              // (read before the next token's)
+        const int place = place_of64(key, ~uint32_t(id), n);
+        if (place >= C.top_k) id = -1;
+        if (id >= 0) x = exact_score(SOFTMAX, soft, logit(C, t, id));
+        if (rule.flags & PM_ROUTE_RENORM) {
             const double all = wave_sum_f64(x);
             x = all > 0.0 ? x / all : 0.0;
         }
-        *w = id >= 0 ? float(x * double(C.rule.scale)) : 0.0f;
-        return id;
+        const int64_t u = int64_t(t) * C.top_k;
+        if (id >= 0) {
+            C.ids[u + place] = id;
+            C.w[u + place] = float(x * double(rule.scale));
+            f(u + place, id);
+        }
+        if (lane >= n && lane < C.top_k) {          // (left over)
+            C.ids[u + lane] = -1;
+            C.w[u + lane] = 0.0f;
+        }
+    }
+
+    // Lists the experts above `least`, and of those that equal it the first `equal`;
+    // returns how many, listed if they are no more than a wave's lanes.
+    __device__ static inline int list_above(uint64_t least, int equal, int lane, Space* space) {
+        int n = 0, same = 0;
+#pragma unroll 1
+        for (int v = 0; v < VPT; ++v) {
+            const uint64_t k = space->key[padded_at(v * kWave + lane)];
+            const uint64_t equals = __ballot(k == least);
+            const bool hit = k > least || (k == least && same + lanes_below(equals) < equal);
+            const uint64_t hits = __ballot(hit);
+            const int at = n + lanes_below(hits);
+            if (hit && at < kWave) space->listed[at].id = v * kWave + lane;
+            n += __popcll(hits);
+            same += __popcll(equals);
+        }
+        return n;
+    }
+    __device__ static inline int met_by(uint64_t least, int lane, Space* space) {
+        int n = 0;
+#pragma unroll 1
+        for (int v = 0; v < VPT; ++v)
+            n += __popcll(__ballot(space->key[padded_at(v * kWave + lane)] >= least));
+        return n;
     }
 };
 

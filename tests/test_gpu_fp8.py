@@ -151,6 +151,63 @@ def test_scored_route_near_ties():
                 check_scored(l, b, K, score=score, **groups)
 
 
+def test_scored_route_large_biases():
+    """Biases so large that fp32 sums, and the top halves of fp64 ones, hold
+    little of the scores; and such of both signs, which cancel in the sums of
+    a group's two best experts."""
+    report("scored route large biases")
+    g = rc.gen(21)
+    for E, K in ((96, 6), (512, 10), (1000, 64), (4096, 10)):
+        l = torch.randn(9, E, generator=g, device="cuda")
+        for big in (2.0 ** 10, 2.0 ** 20, -2.0 ** 20):
+            for score in SCORES:
+                check_scored(l, torch.full((E,), big, device="cuda"), K, f"{E} {big}", score=score)
+    for big in (1000.0, 60000.0):
+        bias = torch.full((64, 4), -big, device="cuda")
+        bias[:, 1] = big
+        l = torch.randn(100, 256, generator=g, device="cuda")
+        for top_groups in (3, 30):
+            check_scored(l, bias.view(-1), 8, f"{big} {top_groups}", score="sigmoid",
+                         n_groups=64, group_best=2, top_groups=top_groups)
+
+
+def test_scored_route_equal_rows():
+    """Rows whose experts all count the same, as a padded token's do: the lowest
+    ids.  And such rows with one better, one worse and one masked."""
+    report("scored route equal rows")
+    for E, K in ((8, 3), (72, 64), (100, 12), (512, 10), (520, 13), (4096, 64)):
+        l = torch.zeros(12, E, device="cuda")
+        l[1:5] = torch.tensor([-1.0, 3.5, 40.0, -90.0], device="cuda")[:, None]
+        l[5, E // 2] = 1.0
+        l[6, 1] = -1.0
+        l[7, 0] = -float("inf")
+        l[8, E // 3:] = -float("inf")
+        l[9, :3] = 2.0 ** -40                      # (a score of just over 1/2)
+        l[10, ::2] = 2.0 ** -40
+        for score in SCORES:
+            for bias in (None, torch.full((E,), 0.125, device="cuda")):
+                check_scored(l, bias, K, f"{E} {score}", score=score, renorm=True)
+                if E % 8 == 0 and K <= E // 2:
+                    check_scored(l, bias, K, f"{E} {score} groups", score=score, n_groups=8,
+                                 top_groups=4, group_best=2)
+
+
+def test_scored_route_smallest_scores():
+    """Sigmoids about the smallest normal fp32 number, a few steps of the logits'
+    type apart, and softmax scores as small beside one large."""
+    report("scored route smallest scores")
+    g = rc.gen(22)
+    at = torch.full((40, 128), -87.3365447, device="cuda")
+    l = (at.view(torch.int32) + torch.randint(-400, 400, at.shape, generator=g, device="cuda",
+                                              dtype=torch.int32)).view(torch.float32)
+    check_scored(l, None, 8, score="sigmoid")
+    check_scored(l * (1.0 + torch.rand(40, 1, generator=g, device="cuda") / 8), None, 12,
+                 score="sigmoid")
+    l = torch.cat([torch.zeros(40, 2, device="cuda"), l - 5 * torch.rand(
+        40, 128, generator=g, device="cuda")], dim=1)
+    check_scored(l, None, 8, "softmax", score="softmax", renorm=True)
+
+
 def test_scored_route_no_experts_but_the_biased():
     """A bias alone decides between scores of 0; their weights are 0, renormalised
     or not."""
