@@ -13,6 +13,12 @@
 // outputs of one row of x, so sx is one register per block and lane, sw (one for
 // four outputs that begin at a multiple of four rows) one value loaded with the
 // weights.
+//
+// 8 tokens of 512 experts, top-10, 2048 x 4096, gate and up: 116 to 120 us, 5.2 to 5.4
+// TB/s; 64 tokens, top-10, 4096 x 1024: 286, 5.4.  (A plain product of two large
+// vectors reaches 6.2.)  The matrix cores are 7 % busy; waves wait for memory.  Two
+// row tiles of 4 blocks in registers, one at work: four, with x converted anew for
+// each, spill and are slower.
 #include <hip/hip_runtime.h>
 
 #include "pm_fp8.h"
