@@ -12,14 +12,15 @@
 // a choice open, the wave ranks the token again, in fp64.
 //
 // Bound by the chain of dependent steps of a token (the bound by ballots, the
-// groups, the candidates), which four waves on a SIMD half hide (51 % of the waves'
+// groups, the candidates), which four waves on a SIMD half hide (59 % of the waves'
 // time is waiting): 16384 tokens of 512 experts, sigmoid, 10 of the best 4 of 8
-// groups, take 32 us (33.5 MB of logits, 5.4 at the memory's rate), 5 to 6 of them
-// for the few tokens that are ranked again.  With sorting, a second launch
-// (pm_route_sort.h): 41 us, without groups 30, with all ranks in fp64 117, and 100
-// where each token's experts all count the same and each is ranked again.  Experts
-// lie VPT adjacent ones to a lane: a row is read by one wide load, and groups of
-// whole lanes need no LDS (43 us where experts were dealt out in turn).
+// groups, take 28 us (33.5 MB of logits, 5.4 at the memory's rate).  A token that is
+// ranked again takes 6, which the kernel waits for; bounds as close as they are leave
+// that to less than one token of these calls on average.  With sorting, a second launch
+// (pm_route_sort.h): 38 us, with all ranks in fp64 117, and 102 where each token's
+// experts all count the same and each is ranked again.  Experts lie VPT adjacent
+// ones to a lane: a row is read by one wide load, and groups of whole lanes need no
+// LDS (2 us more where experts were dealt out in turn).
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
@@ -124,21 +125,21 @@ __device__ inline double lane_value(double v, int lane) {
                     uint32_t(__builtin_amdgcn_readlane(int(b), lane)));
 }
 
-// What a rank in fp32 may be off by, at least doubled.  A sigmoid 1 / (1 + e),
-// e = e^-l: the exponent of v_exp_f32 is rounded twice, e by an ulp, so that e has
-// an error of |l| 2^-23.7 + 2^-23 of it, which the score takes times s (1 - s):
-// 2^-24.5 together, as that is 1/4 at most and |l| times it 0.23.  The sum and
-// v_rcp_f32's ulp are 2^-23 + 2^-24 more, so the score is off by 2^-22 at most; a
-// softmax's e / sum, with five roundings of half an ulp, by 2^-21.6 of it.  The sum
-// with a bias is rounded to 2^-24 of it.
-__device__ inline float rank_error(float size) { return 0x1p-20f + size * 0x1p-23f; }
-
-// How far below a rank in fp32 another may be and still come before it.  Scores
-// without a bias tell small ones apart as well: they are off by 2^-17 of
-// themselves (|l| < 88 where they are not 0), or what is lost below 2^-126.
-__device__ inline float rank_slack(float v, bool bias) {
-    const float slack = 2.0f * rank_error(fabsf(v));
-    return bias ? slack : fminf(slack, v * 0x1p-14f + 0x1p-124f);
+// How far apart in fp32 two ranks (or two groups' sums of two) may be and still
+// be the other way round, where the larger of them, or the two of a group, are
+// `size`.  A sigmoid as rank_tokens forms it is off by less than 2^-23 (1.11e-7 at
+// most, found by trying every fp32 logit); a softmax's e / sum by 5 roundings of
+// 2^-24 of it (v_rcp_f32: two).  Either side has this error twice at most (two
+// ranks, or both of the ranks that are compared).  Sums with a bias, a group's sum,
+// and the difference from the bound are each rounded to 2^-24 of `size`.
+__device__ inline float rank_slack(bool softmax, float size) {
+    return (softmax ? 0x1.5p-21f : 0x1p-22f) + size * 0x1.9p-23f;
+}
+// The same without a bias, of ranks from v down: small scores are told apart as
+// well, as they are off by 2^-17.9 of themselves (|l| < 88 where they are not 0), or
+// what is lost below 2^-126.
+__device__ inline float score_slack(bool softmax, float v) {
+    return fminf(rank_slack(softmax, v), v * 0x1p-14f + 0x1p-124f);
 }
 
 template <int VPT>
@@ -164,6 +165,30 @@ __device__ inline uint32_t rank_bound(uint32_t m, int top_k) {
         if (n >= top_k) lo = c;
         if (n == top_k) break;
         if (n < top_k) hi = c - 1;
+    }
+    return lo;
+}
+
+// A higher bound, of those that all keys are counted for: top_k keys meet it, and
+// few more if any value tells so many apart.
+template <int VPT>
+__device__ inline uint32_t rank_bound_all(const Ranks<VPT>& r, uint32_t lo, uint32_t hi, int top_k,
+                                          int spare) {
+    doublings(6, [&](auto d) {
+        const Pair p = both<d>(hi);
+        hi = max(p.a, p.b);
+    });
+    hi = uni(int(hi));
+    while (lo < hi) {
+        const uint32_t c = lo + ((hi - lo) >> 1) + 1;
+        int n = 0;
+#pragma unroll
+        for (int v = 0; v < VPT; ++v) n += __popcll(__ballot(r.key[v] >= c));
+        if (n >= top_k) lo = c;
+        if (n < top_k)
+            hi = c - 1;
+        else if (n - top_k <= spare)
+            break;
     }
     return lo;
 }
@@ -217,7 +242,7 @@ constexpr int padded_size(int vpt) { return vpt * (kWave + kWave / 8); }
 // Takes the experts of the groups that do not stay out of the ranks; false where
 // ranks in fp32 do not tell which do.  `space`: the wave's LDS, padded_size(VPT)
 // keys.
-template <int VPT>
+template <int VPT, bool SOFTMAX>
 __device__ inline bool rank_groups(const RouteCall& C, const Groups& groups, Ranks<VPT>& r,
                                    int lane, uint32_t* space) {
     const pm_route_rule& rule = C.rule;
@@ -250,8 +275,8 @@ __device__ inline bool rank_groups(const RouteCall& C, const Groups& groups, Ran
     float mine = real ? rank_value(two.a) : -INFINITY, second = 0.0f;
     if (rule.group_best == 2 && two.b != 0) second = rank_value(two.b);
     // groups that count more for certain, and those that may: by the ends of what
-    // each may count (two ranks, and their sum)
-    const float off = 2.0f * rank_error(fabsf(mine) + fabsf(second));
+    // each may count
+    const float off = rank_slack(SOFTMAX, fabsf(mine) + fabsf(second));
     mine += second;
     const float low = real ? mine - off : mine, high = real ? mine + off : mine;
     int more = 0, maybe = -1;
@@ -483,28 +508,37 @@ private:
                 }
                 bool sure = true;
                 if (rule.n_groups > 1)
-                    sure = rank_groups<VPT>(C, groups, r, lane,
+                    sure = rank_groups<VPT, SOFTMAX>(C, groups, r, lane,
                                             reinterpret_cast<uint32_t*>(space->key));
                 // all that may be among the top_k, into this token's lanes
                 uint32_t most = r.key[0];
 #pragma unroll
                 for (int v = 1; v < VPT; ++v) most = max(most, r.key[v]);
-                uint32_t bound = rank_bound(most, C.top_k);
-                if (bound) {
-                    const float v = rank_value(bound);
-                    bound = rank_key(v - rank_slack(v, biased));
-                }
-                bound = max(bound, 1u);
-                int n = 0;
+                uint32_t least = rank_bound(most, C.top_k);
+                int n;
+#pragma unroll 1
+                for (bool again = false;; again = true) {
+                    uint32_t bound = 1;
+                    if (least) {
+                        const float v = rank_value(least);
+                        bound = max(rank_key(v - (biased ? rank_slack(SOFTMAX, fabsf(v))
+                                                         : score_slack(SOFTMAX, v))),
+                                    1u);
+                    }
+                    n = 0;
 #pragma unroll
-                for (int v = 0; v < VPT; ++v) {
-                    const bool hit = r.key[v] >= bound;
-                    const uint64_t hits = __ballot(hit);
-                    if (hits == 0) continue;
-                    const int at = n + lanes_below(hits);
-                    if (hit && at < held)
-                        space->listed[s * held + at] = {lane * VPT + v, now.v[v], bias[v]};
-                    n += __popcll(hits);
+                    for (int v = 0; v < VPT; ++v) {
+                        const bool hit = r.key[v] >= bound;
+                        const uint64_t hits = __ballot(hit);
+                        if (hits == 0) continue;
+                        const int at = n + lanes_below(hits);
+                        if (hit && at < held)
+                            space->listed[s * held + at] = {lane * VPT + v, now.v[v], bias[v]};
+                        n += __popcll(hits);
+                    }
+                    // (lanes that hold several of the largest let too many pass)
+                    if (n <= held || again || !sure) break;
+                    least = rank_bound_all(r, least, most, C.top_k, (held - C.top_k) / 2);
                 }
                 if (!sure || n > held) redo |= 1u << s;
                 if (lane / held == s) {

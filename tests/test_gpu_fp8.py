@@ -171,6 +171,24 @@ def test_scored_route_large_biases():
                          n_groups=64, group_best=2, top_groups=top_groups)
 
 
+def test_scored_route_adjacent_experts():
+    """The largest logits side by side, in few lanes, or all in one group."""
+    report("scored route adjacent experts")
+    g = rc.gen(23)
+    for E, K in ((64, 8), (128, 13), (512, 10), (512, 40), (1000, 10), (4096, 64)):
+        l = torch.randn(21, E, generator=g, device="cuda")
+        l[:7] = l[:7].sort(dim=1, descending=True).values
+        l[7:14] = l[7:14].sort(dim=1).values
+        l[14] = torch.arange(E, device="cuda").div(64, rounding_mode="floor")
+        bias = torch.randn(E, generator=g, device="cuda").mul_(0.01)
+        for score in SCORES:
+            for b in (None, bias):
+                check_scored(l, b, K, f"{E} {score}", score=score, renorm=True)
+                if E % 8 == 0 and K <= E // 8:
+                    check_scored(l, b, K, f"{E} {score} one group", score=score, n_groups=8,
+                                 top_groups=1, group_best=2)
+
+
 def test_scored_route_equal_rows():
     """Rows whose experts all count the same, as a padded token's do: the lowest
     ids.  And such rows with one better, one worse and one masked."""
