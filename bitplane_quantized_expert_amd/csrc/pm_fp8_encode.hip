@@ -255,7 +255,7 @@ template <int TYPE>
 hipError_t run_encode8(const EncodeCall& C, int n, int block_rows, hipStream_t st) {
     const int64_t blocks = int64_t(n) * C.row_blocks * C.blocks;
     if (block_rows == 1) {
-                const unsigned grid =
+        const unsigned grid =
             unsigned(std::min<int64_t>((blocks + 31) / 32, int64_t(compute_units()) * 32));
         hipLaunchKernelGGL((encode_rows_kernel<TYPE>), dim3(grid), dim3(256), 0, st, C, blocks);
     } else {

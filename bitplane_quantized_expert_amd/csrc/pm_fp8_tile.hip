@@ -19,8 +19,8 @@
 // Either way a block's sum meets the factor sw * sx in one fp32 fma per element.
 //
 // What bounds them, and how it is met:
-// - Many rows (65536 over 32 experts of 2048 x 4096, gate and up: 508 to 515 us, 2.13
-//   to 2.17 PFLOP/s, the matrix cores 62 % busy): 4 fmas and 4 factors an element
+// - Many rows (65536 over 32 experts of 2048 x 4096, gate and up: 504 to 515 us, 2.13
+//   to 2.18 PFLOP/s, the matrix cores 62 % busy): 4 fmas and 4 factors an element
 //   of a block beside its 32 cycles of product, all in one wave's order.  So each
 //   product is pinned where it is written, its sums are added two products later
 //   (no wait for the result), and the loads of a stage lie a few products apart;
@@ -33,7 +33,8 @@
 //   for the last tile's stores.
 // - Loads of weights past the caches gained 2 % there and lost more elsewhere, such
 //   stores of y lost everywhere, loads 1 product apart or 4 lost 1 to 3 %, and all
-//   stages' weights before any x at the start lost on small calls.
+//   stages' weights before any x at the start lost on small calls.  Priorities of
+//   waves (of one of a SIMD's two, or of both between barriers) changed nothing.
 // - Halves (fp32 and fp16 results): conversions and four times the products, 848
 //   TFLOP/s at 64 experts of 4096 x 2048 with 512 rows each.
 #include <hip/hip_runtime.h>
