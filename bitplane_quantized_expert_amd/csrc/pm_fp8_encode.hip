@@ -9,8 +9,13 @@
 // instructions a value would bound the kernel (24 in all took 42 us for 16384 x 4096
 // bf16 values, these 8 take 34).  With t = x / scale or up to 2^-20 of it more, and h = t cut off to
 // 12 bits, which every border between two codes has, the sign of the remainder
-// |x| - |h| scale (exact in one fma) says on which side of h the quotient lies, and
-// h moved there by one ulp of fp32 rounds as the quotient does.
+// |x| - |h| scale says on which side of h the quotient lies, and h moved there by
+// one ulp of fp32 rounds as the quotient does.  One fma gives that sign while the
+// remainder is a multiple of fp32's smallest number, 2^-149: h counts from
+// 2^-10 on (half the smallest code), so its last bit is 2^-21 or more, and that of
+// a scale of 2^-105 or more is 2^-128 or more.  Below 2^-100 x and scale are both
+// taken times 2^24, which changes no quotient: the last bits are 2^-125 and
+// 2^-146 then.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -128,11 +133,20 @@ __device__ inline float quotient(float x, float scale, float over) {
     return __uint_as_float(h + uint32_t(side));
 }
 
-// The codes of these.  FINITE: no x is an infinity or NaN.
-template <int TYPE, bool FINITE>
+// Whether a block of this largest |x| is an ordinary one: no infinities or NaN,
+// and its scale, largest / 448, is not below 2^-100 (or the block is all zeros).
+__device__ inline bool ordinary(uint32_t largest) {
+    constexpr uint32_t kLeast = (127u - 91u) << 23;      // of 2^-91 > 448 * 2^-100
+    return largest == 0 || largest - kLeast < 0x7F800000u - kLeast;
+}
+
+// The codes of these.  ORDINARY: of an ordinary block.
+template <int TYPE, bool ORDINARY>
 __device__ inline void store16(const EncodeCall& C, int64_t row, int col, int l,
                                const Raw16<TYPE>& x, float scale) {
     constexpr int kPer = Raw16<TYPE>::kPer;
+    const float lift = ORDINARY || scale >= 0x1p-100f ? 1.0f : 0x1p24f;
+    scale *= lift;
     const float over = __builtin_amdgcn_rcpf(scale) * (1.0f + 0x1p-21f);
     uint8_t* p = C.q + row * C.ldq;
 #pragma unroll
@@ -144,9 +158,10 @@ __device__ inline void store16(const EncodeCall& C, int64_t row, int col, int l,
             float v[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const float xi = value<TYPE>(x.d[k], 4 * h + i);
+                float xi = value<TYPE>(x.d[k], 4 * h + i);
+                if (!ORDINARY) xi *= lift;
                 v[i] = quotient(xi, scale, over);
-                if (!FINITE && !(fabsf(xi) < INFINITY)) v[i] = __uint_as_float(0x7FC00000u);
+                if (!ORDINARY && !(fabsf(xi) < INFINITY)) v[i] = __uint_as_float(0x7FC00000u);
             }
             const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[0], v[1], 0, false);
             w[h] = uint32_t(__builtin_amdgcn_cvt_pk_fp8_f32(v[2], v[3], lo, true));
@@ -174,7 +189,7 @@ __global__ __launch_bounds__(256) void encode_rows_kernel(const EncodeCall C, in
         const Raw16<TYPE> x = load16<TYPE>(C, row, col, l);
         const uint32_t big = row8_max(largest16<TYPE, false>(x));
         float scale;
-        if (__ballot(big >= 0x7F800000u) == 0) {
+        if (__ballot(!ordinary(big)) == 0) {
             scale = scale_of(big);
             store16<TYPE, true>(C, row, col, l, x, scale);
         } else {
@@ -230,8 +245,8 @@ __global__ __launch_bounds__(1024 / R) void encode_square_kernel(const EncodeCal
 #pragma unroll
         for (int i = 0; i < R; ++i) big = max(big, largest16<TYPE, false>(x[i]));
         big = block_max(big, wave_max[parity][0]);
-        const bool finite = big < 0x7F800000u;     // the same in every thread
-        if (!finite) {
+        const bool plain = ordinary(big);           // the same in every thread
+        if (!plain) {
             big = 0;
 #pragma unroll
             for (int i = 0; i < R; ++i) big = max(big, largest16<TYPE, true>(x[i]));
@@ -242,7 +257,7 @@ __global__ __launch_bounds__(1024 / R) void encode_square_kernel(const EncodeCal
         for (int i = 0; i < R; ++i) {
             if (row0 + i * kStep >= C.rows) continue;
             const int64_t row = m * C.rows + row0 + i * kStep;
-            if (finite)
+            if (plain)
                 store16<TYPE, true>(C, row, col, l, x[i], scale);
             else
                 store16<TYPE, false>(C, row, col, l, x[i], scale);
