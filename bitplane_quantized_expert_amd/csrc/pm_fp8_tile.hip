@@ -82,12 +82,6 @@ __device__ inline void store_row(void* y, int64_t at, int left, const float* v) 
 // (kGluSplit: the up matrix begins inside a block of 128 rows).
 enum { kPlain = 0, kGlu = 1, kGluSplit = 2 };
 
-// silu_up to within 2^-16 and |g| 2^-22 of itself: what bf16 results need, whose
-// rounding is 2^-9.  (The exact one takes a twelfth of the kernel's time)
-__device__ inline float silu_up_fast(float g, float u) {
-    return g * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.44269504f)) * u;
-}
-
 // BM rows by 256 weight rows, S stages of 128 inputs in LDS.
 template <int YT, int MODE, int BM, int S>
 __global__ __launch_bounds__(kTileThreads, 2) void fp8_tile_kernel(const GroupedCall C, int nt) {
@@ -470,8 +464,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void fp8_tile_kernel(const Grouped
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
                         if constexpr (GLU)
-                            v[2 * j + r] = NATIVE ? silu_up_fast(acc[i][j][r], acc[i][j + 1][r])
-                                                  : silu_up(acc[i][j][r], acc[i][j + 1][r]);
+                            v[2 * j + r] = silu_up(acc[i][j][r], acc[i][j + 1][r]);
                         else
                             v[4 * j + r] = acc[i][j][r];
                     }

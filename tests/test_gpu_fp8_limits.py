@@ -1,12 +1,13 @@
 """The 8-bit operators where their arithmetic is at its ends: quotients beside a
-midpoint at the smallest scales."""
+midpoint at the smallest scales, gates whose exponential is almost infinite."""
 import numpy as np
 import pytest
 import torch
 
+import bitplane_quantized_expert_amd as pm
 import fp8_cases as fc
 import routed_cases as rc
-from test_gpu_fp8 import check_encode, report
+from test_gpu_fp8 import SWIGLU, check_encode, report
 
 pytestmark = pytest.mark.gpu
 
@@ -52,3 +53,45 @@ def test_encode_smallest_scales(ty, block_rows):
     x = torch.cat([x, x.roll(block_rows, 0), torch.ones_like(x)], dim=1)
     x[-block_rows:, 300] = float("inf")
     check_encode(x.to(rc.TYPES[ty]).cuda(), block_rows)
+
+
+# ---------------------------------------------------------------- gates
+@pytest.mark.parametrize("R", [256, 80])
+@pytest.mark.parametrize("counts", [[2], [40, 9], [300]])
+@pytest.mark.parametrize("y_ty", ["f32", "bf16"])
+def test_grouped8_gates_at_the_ends(y_ty, counts, R):
+    """SiLU of gates from -88.7, whose exponential is about fp32's largest, to 88,
+    times up values that make the smallest results count.  One product per
+    output, so sums are exact, and only the roundings of SiLU are allowed:
+    16 steps of fp32, and that to the type of y."""
+    report(f"fp8 gates {counts} {R} {y_ty}")
+    E, C, h = len(counts), 128, R // 2
+    off, _ = rc.groups(counts, 0)
+    n = sum(counts)
+    g = rc.gen(n + R)
+    W = torch.zeros(E, R, C, device="cuda")
+    W[:, :h, 5] = torch.tensor([-88.0, -72.0, -8.0, -0.5, 0.0, 0.5, 9.0, 88.0],
+                               device="cuda")[torch.arange(h, device="cuda") % 8]
+    W[:, h:, 5] = torch.randint(1, 9, (h,), generator=g, device="cuda").float() * 2.0 ** -3
+    W = W.to(fc.F8)
+    ws = torch.ones(E, -(-R // 128), 1, device="cuda")
+    up = 1.0
+    if R == 256:                                   # (else gate and up share a block)
+        up = 2.0 ** 100
+        ws[:, 1] = up
+    x = torch.zeros(n, C, device="cuda")
+    x[:, 5] = 1.0
+    x = x.to(fc.F8)
+    xs = 0.985 + 0.023 * torch.rand(n, 1, generator=g, device="cuda")
+    y = torch.full((n, h), -7.0, dtype=rc.TYPES[y_ty], device="cuda")
+    pm.pm_grouped_gemm_fp8(W, ws, x, xs, y, off, None, 1, SWIGLU)
+    gate = (xs * W[0, :h, 5].float()).double()     # as fp32 rounds it
+    s = torch.where(gate < 0, gate * torch.exp(gate) / (1 + torch.exp(gate)),
+                    gate / (1 + torch.exp(-gate)))
+    p = s * (xs * up * W[0, h:, 5].float()).double()
+    # (an exponential beyond fp32's range may make the result 0)
+    free = gate < -88.72
+    lim = 16 * 2.0 ** -24 * p.abs() + rc.HALF_STEP[y.dtype] * p.abs() * (1 + 2.0 ** -19) + 2.0 ** -126
+    bad = ~((y.double() - p).abs() <= lim) & ~free
+    assert not bad.any(), (bad.nonzero()[0].tolist(), int(bad.sum()),
+                           sorted(set(gate[bad].tolist()))[:4])
