@@ -342,7 +342,13 @@ __global__ __launch_bounds__(kTileThreads, 2) void fp8_tile_kernel(const Grouped
             constexpr bool ACT = decltype(active)::value;
             for (int t = 0; t < T; ++t) {
                 const int after = st + 1 == S ? 0 : st + 1;
-                const float wa = na, wu0 = nu0, wu1 = nu1;
+                // (none for a stage past the last input: its sums are 0, and
+                // an infinite factor would make them NaN)
+                const int in = t < blocks ? -1 : 0;
+                auto kept = [&](float v) {
+                    return __builtin_bit_cast(float, uni(__builtin_bit_cast(int, v) & in));
+                };
+                const float wa = kept(na), wu0 = kept(nu0), wu1 = kept(nu1);
                 f32x4 wu[2];
                 if constexpr (MODE == kGluSplit) {
 #pragma unroll

@@ -1,5 +1,6 @@
 """The 8-bit operators where their arithmetic is at its ends: quotients beside a
-midpoint at the smallest scales, gates whose exponential is almost infinite."""
+midpoint at the smallest scales, gates whose exponential is almost infinite,
+infinite scales."""
 import numpy as np
 import pytest
 import torch
@@ -95,3 +96,40 @@ def test_grouped8_gates_at_the_ends(y_ty, counts, R):
     bad = ~((y.double() - p).abs() <= lim) & ~free
     assert not bad.any(), (bad.nonzero()[0].tolist(), int(bad.sum()),
                            sorted(set(gate[bad].tolist()))[:4])
+
+
+# ---------------------------------------------------------------- scales
+@pytest.mark.parametrize("y_ty", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("counts", [[3, 1], [40, 40], [300, 20]])
+@pytest.mark.parametrize("C", [16, 128, 144, 256, 272])
+def test_grouped8_infinite_scale(y_ty, counts, C):
+    """An infinite scale of weights, or of a row of x, makes its outputs infinite,
+    with the sign of the block's sum, however few blocks of inputs there are;
+    outputs of other rows and experts are as without it."""
+    report(f"fp8 infinite scale {counts} {C} {y_ty}")
+    R = 144
+    off, _ = rc.groups(counts, 0)
+    n = sum(counts)
+    W, ws = fc.make_weights(2, R, C, 3)
+    x, xs = fc.make_x(n, C, 4)
+    # one sign throughout: no sum is 0
+    W = W.view(torch.uint8).bitwise_and(0x77).bitwise_or(1).view(fc.F8)
+    x = x.contiguous().view(torch.uint8).bitwise_and(0x77).bitwise_or(1)
+    x[1] |= 0x80
+    x = x.view(fc.F8)
+    for last in (False, True):
+        b = -1 if last else 0
+        w2, x2 = ws.clone(), xs.clone()
+        w2[0, 0, b] = float("inf")
+        x2[2, b] = float("inf")
+        y = torch.full((n, R), -7.0, dtype=rc.TYPES[y_ty], device="cuda")
+        z = torch.full_like(y, -7.0)
+        pm.pm_grouped_gemm_fp8(W, w2, x, x2, y, off, None, 1, 0)
+        pm.pm_grouped_gemm_fp8(W, ws, x, xs, z, off, None, 1, 0)
+        inf = torch.zeros(n, R, dtype=torch.bool, device="cuda")
+        inf[:counts[0], :128] = True
+        inf[2] = True
+        sign = torch.ones(n, 1, device="cuda")
+        sign[1] = -1.0
+        want = torch.where(inf, float("inf") * sign, z.float())
+        assert torch.equal(y.float(), want), (last, (y.float() != want).nonzero()[0].tolist())
