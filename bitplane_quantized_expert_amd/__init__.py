@@ -40,6 +40,7 @@ PM_BF16 = 2
 PM_GROUPED_GATHER = 1
 PM_GROUPED_SCATTER = 2
 PM_GROUPED_SWIGLU = 4
+PM_GROUPED_FP32_SUMS = 16
 PM_ROUTE_MAX_EXPERTS = 4096
 PM_ROUTE_MAX_TOPK = 64
 PM_GROUPED_MAX_EXPERTS = 4096
@@ -599,7 +600,8 @@ def pm_grouped_gemm_fp8(d_w, d_wscales, d_x, d_xscales, d_y, d_offsets, d_order=
     """d_w [n_experts][rows][cols] and d_x rows of cols: float8_e4m3fn (or uint8
     codes); d_wscales float32 [n_experts][ceil(rows/128)][ceil(cols/128)],
     d_xscales float32 [rows of x][ceil(cols/128)], contiguous; d_y rows of
-    float32, float16 or bfloat16.  stream=None is the null stream, not torch's
+    float32, float16 or bfloat16 (whose sums may be cut off where flags lack
+    PM_GROUPED_FP32_SUMS, see pm.h).  stream=None is the null stream, not torch's
     current one."""
     shape = d_w.shape
     if len(shape) != 3 or not d_w.is_contiguous():

@@ -12,7 +12,11 @@
 
 namespace pm {
 
-// Tiles of 256 or 128 rows (bf16 results; others: 128) x 256 (pm_fp8_tile.hip);
+// Whether the tiles of a call multiply codes as they are, in sums that are cut off.
+inline bool fp8_cuts_off(const GroupedCall& C) {
+    return C.y_type == PM_BF16 && !(C.flags & PM_GROUPED_FP32_SUMS);
+}
+// Tiles of 256 or 128 rows (where sums are not cut off: 128) x 256 (pm_fp8_tile.hip);
 // the offsets of a tile's rows in x must fit 32 bits.
 hipError_t launch_fp8_tiles(const GroupedCall& C, int rows, hipStream_t st);
 // Whether the table of experts lies in LDS beside the three stages of 128-row

@@ -7,7 +7,8 @@ namespace pm {
 
 // Weights are streamed while a group has few rows.  Measured, us of the streamed
 // kernel against 128-row tiles at 1, 2, 4, 8, 12, 16 rows per group; bf16 results
-// (tiles of codes as they are), then fp32 (tiles of codes as halves):
+// (tiles of codes as they are), then fp32 (tiles of codes as halves, also those of
+// bf16 results with fp32 sums):
 //   128 experts, 256 inputs, 1024 outputs: 14/13 16/14 16/14 14/14 20/15 22/15;
 //                                          14/16 16/16 17/17 15/17 20/18 22/19
 //   64, 512, 4096:   21/21 28/26 30/27 33/28 40/28 52/29;  21/25 28/31 30/32 34/33 41/35 54/38
@@ -37,7 +38,7 @@ hipError_t launch_grouped8(const GroupedCall& C, hipStream_t st) {
     const int64_t groups = std::min(C.n_experts, C.n_rows), cus = compute_units();
     const int64_t x_rows = C.flags & PM_GROUPED_GATHER ? (C.n_rows - 1) / C.top_k + 1 : 256;
     const bool far = x_rows * C.ldx + C.cols >= 0xFFFFFFF0ll;
-    const bool glu = C.flags & PM_GROUPED_SWIGLU, bf16 = C.y_type == PM_BF16;
+    const bool glu = C.flags & PM_GROUPED_SWIGLU, bf16 = fp8_cuts_off(C);
     const int64_t out = glu ? C.rows / 2 : C.rows, per = glu ? 128 : 256;
     const bool one_each = groups * ((out + per - 1) / per) <= cus;
     int64_t from = std::min<int64_t>(C.cols / 320, 13);

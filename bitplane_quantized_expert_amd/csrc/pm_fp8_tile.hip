@@ -13,9 +13,13 @@
 // bf16 results: v_mfma_f32_16x16x128_f8f6f4 takes a whole block of 16 x 16 in one
 // instruction (32 cycles), from codes as they are.  Its sums of 8 adjacent
 // products are cut off 13 bits below the largest one's power of two (measured:
-// every one of 13 million random groups equals that model), which bf16's own
-// rounding covers; include/pm.h has the bound.  Other results: the codes become
-// halves in registers, exactly, and four v_mfma_f32_16x16x32_f16 take a block.
+// every one of 13 million random groups equals that model; v_mfma_f32_16x16x32_fp8
+// and the 32x32x64 form do the same), 1.5e-5 of results on normal data beside
+// the 1.7e-3 of bf16's own rounding; include/pm.h has the bound.  Other results,
+// and bf16 ones under PM_GROUPED_FP32_SUMS: the codes become halves in registers,
+// exactly, and four v_mfma_f32_16x16x32_f16 take a block (65536 rows over 32 experts
+// of 2048 x 4096, gate and up: 1038 us with fp32 sums beside 540; 40960 over 512 of
+// 4096 x 1024: 600 beside 513).
 // Either way a block's sum meets the factor sw * sx in one fp32 fma per element.
 //
 // What bounds them, and how it is met:
@@ -82,11 +86,12 @@ __device__ inline void store_row(void* y, int64_t at, int left, const float* v) 
 // (kGluSplit: the up matrix begins inside a block of 128 rows).
 enum { kPlain = 0, kGlu = 1, kGluSplit = 2 };
 
-// BM rows by 256 weight rows, S stages of 128 inputs in LDS.
-template <int YT, int MODE, int BM, int S>
+// BM rows by 256 weight rows, S stages of 128 inputs in LDS.  NATIVE: codes
+// multiplied as they are.
+template <int YT, bool NATIVE, int MODE, int BM, int S>
 __global__ __launch_bounds__(kTileThreads, 2) void fp8_tile_kernel(const GroupedCall C, int nt) {
 #ifdef __HIP_DEVICE_COMPILE__
-    constexpr bool GLU = MODE != kPlain, NATIVE = YT == PM_BF16;
+    constexpr bool GLU = MODE != kPlain;
     constexpr int kStageA = BM * kTileK, kCodes = kStageA + kTileN * kTileK;
     constexpr int kStage = kCodes + kScaleBytes;
     constexpr int LA = BM / 64, LB = kTileN / 64, L = LA + LB + 1;  // a wave's loads per stage
@@ -493,13 +498,13 @@ inline size_t tile_lds(const GroupedCall& C, int bm, int stages) {
            (2 * bm + C.n_experts + 1) * sizeof(int);
 }
 
-template <int YT, int MODE, int BM, int S>
+template <int YT, bool NATIVE, int MODE, int BM, int S>
 hipError_t run_tiles8(const GroupedCall& C, hipStream_t st) {
     const int out = MODE != kPlain ? C.rows / 2 : C.rows;
     const int per = MODE != kPlain ? kTileN / 2 : kTileN;
     const int nt = (out + per - 1) / per;
     const size_t lds = tile_lds(C, BM, S);
-    auto* f = fp8_tile_kernel<YT, MODE, BM, S>;
+    auto* f = fp8_tile_kernel<YT, NATIVE, MODE, BM, S>;
     static std::atomic<uint64_t> allowed{0};
     hipError_t e = allow_lds(reinterpret_cast<const void*>(f), kTileMaxLds, &allowed);
     if (e != hipSuccess) return e;
@@ -509,17 +514,17 @@ hipError_t run_tiles8(const GroupedCall& C, hipStream_t st) {
     return hipGetLastError();
 }
 
-template <int YT, int BM, int S>
+template <int YT, bool NATIVE, int BM, int S>
 hipError_t run_tiles8_mode(const GroupedCall& C, hipStream_t st) {
-    if (!(C.flags & PM_GROUPED_SWIGLU)) return run_tiles8<YT, kPlain, BM, S>(C, st);
-    if ((C.rows / 2) % 128 == 0) return run_tiles8<YT, kGlu, BM, S>(C, st);
-    return run_tiles8<YT, kGluSplit, BM, S>(C, st);
+    if (!(C.flags & PM_GROUPED_SWIGLU)) return run_tiles8<YT, NATIVE, kPlain, BM, S>(C, st);
+    if ((C.rows / 2) % 128 == 0) return run_tiles8<YT, NATIVE, kGlu, BM, S>(C, st);
+    return run_tiles8<YT, NATIVE, kGluSplit, BM, S>(C, st);
 }
 
 template <int YT>
 hipError_t run_exact(const GroupedCall& C, hipStream_t st) {
-    return tile_lds(C, 128, 3) <= kTileMaxLds ? run_tiles8_mode<YT, 128, 3>(C, st)
-                                              : run_tiles8_mode<YT, 128, 2>(C, st);
+    return tile_lds(C, 128, 3) <= kTileMaxLds ? run_tiles8_mode<YT, false, 128, 3>(C, st)
+                                              : run_tiles8_mode<YT, false, 128, 2>(C, st);
 }
 
 }  // namespace
@@ -527,11 +532,14 @@ hipError_t run_exact(const GroupedCall& C, hipStream_t st) {
 bool fp8_tiles128_fit(const GroupedCall& C) { return tile_lds(C, 128, 3) <= kTileMaxLds; }
 
 hipError_t launch_fp8_tiles(const GroupedCall& C, int rows, hipStream_t st) {
-    if (C.y_type == PM_BF16)
-        return rows == 256 ? run_tiles8_mode<PM_BF16, 256, 2>(C, st)
-                           : run_tiles8_mode<PM_BF16, 128, 3>(C, st);
-    return C.y_type == PM_F16 ? run_exact<PM_F16>(C, st)
-                              : run_exact<PM_F32>(C, st);
+    if (fp8_cuts_off(C))
+        return rows == 256 ? run_tiles8_mode<PM_BF16, true, 256, 2>(C, st)
+                           : run_tiles8_mode<PM_BF16, true, 128, 3>(C, st);
+    switch (C.y_type) {
+    case PM_F32: return run_exact<PM_F32>(C, st);
+    case PM_F16: return run_exact<PM_F16>(C, st);
+    default: return run_exact<PM_BF16>(C, st);
+    }
 }
 
 }  // namespace pm

@@ -204,7 +204,8 @@ static pm_status check_grouped(pm_grouped_shape s, pm_grouped_rows r, const void
     if (int64_t(s.rows) * std::max(s.cols, 1) >= (int64_t(1) << 30))
         return failf(PM_ERR_SHAPE, "grouped: a matrix of %d x %d holds 2^30 weights or more",
                      s.rows, s.cols);
-    if (flags & ~uint32_t(PM_GROUPED_GATHER | PM_GROUPED_SCATTER | PM_GROUPED_SWIGLU))
+    if (flags & ~uint32_t(PM_GROUPED_GATHER | PM_GROUPED_SCATTER | PM_GROUPED_SWIGLU |
+                          (x_type == kE4M3 ? PM_GROUPED_FP32_SUMS : 0)))
         return failf(PM_ERR_ARG, "grouped: flags 0x%x", flags);
     if ((flags & PM_GROUPED_SWIGLU) && s.rows % 2)
         return failf(PM_ERR_SHAPE, "grouped: gate and up of %d rows together", s.rows);

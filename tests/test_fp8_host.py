@@ -12,6 +12,7 @@ import torch
 import bitplane_quantized_expert_amd as pm
 import fp8_cases as fc
 from bitplane_quantized_expert_amd import build
+import test_routed_host as routed
 from test_routed_host import A, B, D, OFF, ORD, WS, refused, rows, shape, status
 
 S1, S2 = A + (1 << 35), B + (1 << 35)
@@ -98,6 +99,19 @@ def test_grouped_fp8_refusals():
     refused(fp8(y=S2 + 28), pm.PM_ERR_ARG, "overlap")
     assert fp8(r=rows(n=0, off=None, order=None), x=None, y=None) == pm.PM_OK
     assert fp8(s=shape(r=0), y=None) == pm.PM_OK
+
+
+def test_fp32_sums_flag():
+    """PM_GROUPED_FP32_SUMS is of the 8-bit products alone, and goes with every
+    other flag and type."""
+    many = pm.PM_GROUPED_GATHER | pm.PM_GROUPED_SCATTER | pm.PM_GROUPED_SWIGLU
+    for yt in (pm.PM_F32, pm.PM_F16, pm.PM_BF16):
+        for flags in (0, many):
+            assert fp8(r=rows(n=0), yt=yt, flags=flags | pm.PM_GROUPED_FP32_SUMS) == pm.PM_OK
+    refused(fp8(flags=pm.PM_GROUPED_FP32_SUMS | 8), pm.PM_ERR_ARG, "flags")
+    refused(fp8(flags=pm.PM_GROUPED_FP32_SUMS, y=B), pm.PM_ERR_ARG, "overlap")
+    refused(routed.gemm(flags=pm.PM_GROUPED_FP32_SUMS), pm.PM_ERR_ARG, "flags")
+    refused(routed.w4(flags=pm.PM_GROUPED_FP32_SUMS), pm.PM_ERR_ARG, "flags")
 
 
 def test_encode_fp8_refusals():
