@@ -1,6 +1,7 @@
 """The 8-bit operators where their arithmetic is at its ends: quotients beside a
 midpoint at the smallest scales, gates whose exponential is almost infinite,
-infinite scales, the sums that the matrix cores cut off."""
+infinite scales, the sums that the matrix cores cut off, and kernels that only
+many experts or many rows reach."""
 import numpy as np
 import pytest
 import torch
@@ -8,7 +9,7 @@ import torch
 import bitplane_quantized_expert_amd as pm
 import fp8_cases as fc
 import routed_cases as rc
-from test_gpu_fp8 import SCATTER, SWIGLU, check_encode, report
+from test_gpu_fp8 import GATHER, SCATTER, SWIGLU, check_encode, report, run_grouped8
 
 pytestmark = pytest.mark.gpu
 
@@ -284,3 +285,92 @@ def test_grouped8_fp32_sums_in_a_graph():
             pm.pm_grouped_gemm_fp8(W, ws, x, xs, out, off, ordr, 1, SWIGLU | SCATTER | FP32, s)
         torch.cuda.synchronize()
         assert torch.equal(z[0], y) and torch.equal(z[1], y)
+
+
+# ---------------------------------------------------------------- kernels of many rows or experts
+def whole_numbers(n, E, R, C, seed):
+    """Codes of small whole numbers, and scales of powers of two: every partial
+    sum is exact, also where products are cut off 13 bits below the largest."""
+    g = rc.gen(seed)
+
+    def ints(*shape):
+        return torch.randint(-8, 9, shape, generator=g, device="cuda").float().to(fc.F8)
+
+    def scales(lo, hi, *shape):
+        return torch.exp2(torch.randint(lo, hi, shape, generator=g, device="cuda").float())
+
+    return (ints(E, R, C), scales(-8, -5, E, -(-R // 128), -(-C // 128)), ints(n, C),
+            scales(-1, 1, n, -(-C // 128)))
+
+
+def check_exact(counts, R, C, y_ty, flags, seed, more=0, flags_more=0):
+    """Equal to the exact sums where there is no SiLU; with it, 16 steps of fp32
+    and the rounding to y's type are allowed."""
+    E = len(counts)
+    off, ordr = rc.groups(counts, seed, sum(counts) + more)
+    n = ordr.numel()
+    W, ws, x, xs = whole_numbers(n, E, R, C, seed)
+    out = R // 2 if flags & SWIGLU else R
+    y = torch.full((n, out), -7.0, dtype=rc.TYPES[y_ty], device="cuda")
+    pm.pm_grouped_gemm_fp8(W, ws, x, xs, y, off, ordr, 1, flags | flags_more)
+    x64, half, seen = fc.decode(x, xs, 1), rc.HALF_STEP[y.dtype], 0
+    for e in range(E):
+        a, b = int(off[e]), int(off[e + 1])
+        if a == b:
+            continue
+        use = ordr[a:b].long()
+        at = use if flags & SCATTER else torch.arange(a, b, device="cuda")
+        rows = use if flags & GATHER else torch.arange(a, b, device="cuda")
+        p = x64[rows] @ fc.decode(W[e], ws[e], 128).T
+        seen += b - a
+        if not flags & SWIGLU:
+            assert torch.equal(y[at], p.to(y.dtype)), e
+            continue
+        g, u = p[:, :out], p[:, out:]
+        p = g * torch.sigmoid(g) * u
+        lim = (16 * 2.0 ** -24 + half * (1 + 2.0 ** -19)) * p.abs() + \
+            torch.finfo(y.dtype).smallest_normal * half
+        bad = ~((y[at].double() - p).abs() <= lim)
+        assert not bad.any(), (e, bad.nonzero()[0].tolist(), int(bad.sum()))
+    assert int((y[:, 0] != -7.0).sum()) <= seen
+
+
+@pytest.mark.parametrize("C", [16, 144, 400])
+@pytest.mark.parametrize("R,flags", [(4096, SCATTER), (4096, GATHER | SWIGLU),
+                                     (4104, GATHER | SWIGLU)])
+def test_grouped8_exact_256_rows(R, flags, C):
+    """Tiles of 256 rows, which take bf16 results from two tiles for each compute
+    unit on, with fewer blocks of inputs than stages and more: plain, gate and
+    up, and up that begins inside a block."""
+    report(f"fp8 exact 256 rows {R} x {C} flags {flags}")
+    cus = torch.cuda.get_device_properties(0).multi_processor_count
+    n = -(-2 * cus // (R // 256)) * 256
+    counts = [n // 2 + 77, n - n // 2 + 200]
+    assert sum(counts) // 256 * -(-R // 256) >= 2 * cus and sum(counts) >= 384 * 2
+    check_exact(counts, R, C, "bf16", flags, R + C, more=5)
+
+
+@pytest.mark.parametrize("y_ty", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("R,flags", [(320, SCATTER), (512, SWIGLU), (264, GATHER | SWIGLU)])
+@pytest.mark.parametrize("C", [128, 272, 1040])
+def test_grouped8_exact_tiles(y_ty, R, flags, C):
+    report(f"fp8 exact tiles {R} x {C} {y_ty} flags {flags}")
+    check_exact([140, 0, 33, 290], R, C, y_ty, flags, R + C)
+
+
+@pytest.mark.parametrize("y_ty", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("R,C,flags", [(72, 16, SCATTER), (72, 272, 0), (256, 16, SWIGLU),
+                                       (256, 272, GATHER | SWIGLU), (72, 400, SWIGLU),
+                                       (40, 16, GATHER | SWIGLU)])
+def test_grouped8_many_experts_and_rows(y_ty, R, C, flags):
+    """More than 2047 experts, whose table leaves room for two stages beside
+    128-row tiles, and rows enough that fp32 and fp16 results take them (and
+    bf16 ones with fp32 sums)."""
+    report(f"fp8 2100 experts {R} x {C} {y_ty} flags {flags}")
+    g = np.random.default_rng(R + C)
+    counts = np.bincount(g.integers(0, 2100, 19_000), minlength=2100)
+    counts[7], counts[2099] = 300, 129
+    check_exact(counts.tolist(), R, C, y_ty, flags, R + C, more=3,
+                flags_more=pm.PM_GROUPED_FP32_SUMS)
+    if C == 272:
+        run_grouped8(counts.tolist(), R, C, y_ty, 10, flags, seed=3, pad=1)
