@@ -2,6 +2,7 @@
 
   bitplane_quantized_expert_amd/libpm.so   the product library (include/pm.h)
   synth/libpmsynth.so                      device filler of the seeded inputs
+  tests/native/libpmfacts.so               what the kernels assume of the hardware, for the tests
 """
 import os
 import subprocess
@@ -35,6 +36,8 @@ TARGETS = [
       os.path.join(PKG, "csrc", "pm_fp8_encode.hip")]),
     (os.path.join(ROOT, "synth", "libpmsynth.so"),
      [os.path.join(ROOT, "synth", "synth_device.hip")]),
+    (os.path.join(ROOT, "tests", "native", "libpmfacts.so"),
+     [os.path.join(ROOT, "tests", "native", "device_facts.hip")]),
 ]
 
 # Per-source extra flags.  The LUT kernels issue many independent table

@@ -25,6 +25,7 @@
 
 #include <type_traits>
 
+#include "pm_rank.h"
 #include "pm_route_sort.h"
 
 namespace pm {
@@ -127,19 +128,19 @@ __device__ inline double lane_value(double v, int lane) {
 
 // How far apart in fp32 two ranks (or two groups' sums of two) may be and still
 // be the other way round, where the larger of them, or the two of a group, are
-// `size`.  A sigmoid as rank_tokens forms it is off by less than 2^-23 (1.11e-7 at
-// most, found by trying every fp32 logit); a softmax's e / sum by 5 roundings of
-// 2^-24 of it (v_rcp_f32: two).  Either side has this error twice at most (two
-// ranks, or both of the ranks that are compared).  Sums with a bias, a group's sum,
-// and the difference from the bound are each rounded to 2^-24 of `size`.
+// `size`.  A sigmoid is off by less than kSigmoidError (pm_rank.h); a softmax's
+// e / sum by 5 roundings of 2^-24 of it (v_rcp_f32: two).  Either side has this error
+// twice at most (two ranks, or both of the ranks that are compared).  Sums with a
+// bias, a group's sum, and the difference from the bound are each rounded to 2^-24 of
+// `size`.
 __device__ inline float rank_slack(bool softmax, float size) {
-    return (softmax ? 0x1.5p-21f : 0x1p-22f) + size * 0x1.9p-23f;
+    return (softmax ? 0x1.5p-21f : 2 * kSigmoidError) + size * 0x1.9p-23f;
 }
 // The same without a bias, of ranks from v down: small scores are told apart as
-// well, as they are off by 2^-17.9 of themselves (|l| < 88 where they are not 0), or
-// what is lost below 2^-126.
+// well, as they are off by kSigmoidRelative of themselves at most, either side twice
+// (2^-14 leaves room), or where they are below kSigmoidSmall by less than that.
 __device__ inline float score_slack(bool softmax, float v) {
-    return fminf(rank_slack(softmax, v), v * 0x1p-14f + 0x1p-124f);
+    return fminf(rank_slack(softmax, v), v * 0x1p-14f + 2 * kSigmoidSmall);
 }
 
 template <int VPT>
@@ -501,8 +502,7 @@ private:
                 } else {
 #pragma unroll
                     for (int v = 0; v < VPT; ++v) {
-                        const float x = __builtin_amdgcn_rcpf(
-                            1.0f + __builtin_amdgcn_exp2f(now.v[v] * -1.44269504f));
+                        const float x = sigmoid_rank(now.v[v]);
                         r.key[v] = rank_key(x + bias[v], now.v[v] > -INFINITY);
                     }
                 }
