@@ -1,7 +1,7 @@
-"""The 8-bit operators where their arithmetic is at its ends: quotients beside a
-midpoint at the smallest scales, gates whose exponential is almost infinite,
-infinite scales, the sums that the matrix cores cut off, and kernels that only
-many experts or many rows reach."""
+"""The scored router and the 8-bit operators at their ends: rows at any element,
+infinities, quotients beside a midpoint at the smallest scales, gates whose
+exponential is almost infinite, infinite scales, the sums that the matrix cores
+cut off, and kernels that only many experts or many rows reach."""
 import numpy as np
 import pytest
 import torch
@@ -9,9 +9,127 @@ import torch
 import bitplane_quantized_expert_amd as pm
 import fp8_cases as fc
 import routed_cases as rc
-from test_gpu_fp8 import GATHER, SCATTER, SWIGLU, check_encode, report, run_grouped8
+from test_gpu_fp8 import (GATHER, SCATTER, SWIGLU, check_encode, check_scored, report,
+                          run_grouped8, run_scored)
 
 pytestmark = pytest.mark.gpu
+
+
+# ---------------------------------------------------------------- scored router
+@pytest.mark.parametrize("ty", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("E", [1, 2, 64, 128, 256, 512, 1024, 2048, 4096])
+def test_scored_route_rows_at_any_element(ty, E):
+    """Rows that begin at any element, an odd distance apart, of as many experts
+    as whole lanes hold and of hardly any; every expert selected, too."""
+    report(f"scored route {E} {ty} rows at odd places")
+    g = rc.gen(E)
+    T = 37 if E > 1000 else 150
+    for at, more in ((0, 0), (1, 2), (3, 4)):
+        buf = torch.randn(T, E + at + more, generator=g, device="cuda").to(rc.TYPES[ty])
+        l = buf[:, at:at + E]
+        assert l.stride(0) == E + at + more
+        bias = torch.randn(E, generator=g, device="cuda").mul_(0.1)
+        for K in {1, min(E, 10), min(E, 13), min(E, 64)}:
+            for score in ("sigmoid", "softmax"):
+                check_scored(l, bias if K % 2 else None, K, f"{K} {score}", score=score, renorm=True)
+                if E >= 64 and K <= E // 4:
+                    check_scored(l, bias, K, f"{K} {score} groups", score=score, n_groups=8,
+                                 top_groups=2, group_best=2)
+
+
+def test_scored_route_infinities():
+    """Rows of +inf alone, beside -inf and NaN, in whole groups; biases of +inf."""
+    report("scored route infinities")
+    E, inf = 128, float("inf")
+    l = torch.randn(24, E, generator=rc.gen(3), device="cuda")
+    l[0] = inf
+    l[1] = inf
+    l[1, ::2] = -inf
+    l[2, :] = float("nan")
+    l[2, 5:9] = inf
+    l[3, 16:32] = inf
+    l[4, 16:32] = -inf
+    l[5, 100] = inf
+    bias = torch.randn(E, generator=rc.gen(4), device="cuda").mul_(0.1)
+    far = bias.clone()
+    far[7::16] = inf
+    huge = bias.clone()
+    huge[3::8], huge[4::8] = 3.0e38, -3.0e38
+    for score in ("sigmoid", "softmax"):
+        for b in (None, bias, far, huge):
+            for K in (1, 6, 40):
+                check_scored(l, b, K, f"{score} {K}", score=score, renorm=True)
+                if K < 40:
+                    check_scored(l, b, K, f"{score} {K} groups", score=score, n_groups=8,
+                                 top_groups=3, group_best=2)
+
+
+def test_scored_route_far_rows():
+    """Rows of logits beyond 2^32 bytes."""
+    report("scored route far rows")
+    T, E, ld = 700, 40, 1 << 22
+    if torch.cuda.mem_get_info()[0] < 20 << 30:
+        pytest.skip("too little memory")
+    buf = torch.zeros(T * ld, dtype=torch.bfloat16, device="cuda").view(T, ld)
+    buf[:, :E] = torch.randn(T, E, generator=rc.gen(6), device="cuda").bfloat16()
+    check_scored(buf[:, :E], None, 4, score="sigmoid")
+
+
+def test_scored_route_against_64_bits():
+    """Many tokens of random rules, against the same steps by torch in 64 bits:
+    logits of few values, of near ones and of any; biases small and large."""
+    report("scored route against 64 bits")
+    rng = np.random.default_rng(31)
+    for turn in range(60):
+        n = int(rng.choice([1, 2, 4, 8, 16, 32, 64]))
+        size = int(rng.integers(1, 4096 // n + 1)) if turn % 3 == 0 else int(rng.integers(1, 17))
+        E, T = n * size, int(rng.choice([5, 300, 4000]))
+        kept = int(rng.integers(1, n + 1))
+        K = int(rng.integers(1, min(64, kept * size) + 1))
+        best, score = int(rng.integers(1, 3)), ("sigmoid", "softmax")[turn % 2]
+        g = rc.gen(100 + turn)
+        l = torch.randn(T, E, generator=g, device="cuda") * float(rng.choice([0.01, 1.0, 6.0, 40.0]))
+        if turn % 5 == 1:
+            l = l.mul(4).round().div(4)
+        if turn % 5 == 2:
+            l = 0.5 + l * 2.0 ** -22
+        bias = None
+        if turn % 4:
+            bias = torch.randn(E, generator=g, device="cuda") * float(
+                rng.choice([2.0 ** -24, 0.05, 30.0, 1e4]))
+        ids, w, off, order = run_scored(l, bias, K, score=score, n_groups=n, top_groups=kept,
+                                        group_best=best, renorm=bool(turn & 1), scale=1.5)
+        x = l.double()
+        s = 1.0 / (1.0 + torch.exp(-x))
+        if score == "softmax":
+            p = torch.exp(x - x.amax(1, keepdim=True))
+            s = p / p.sum(1, keepdim=True)
+        c = s if bias is None else s + bias.double()
+        if n > 1:
+            top = c.reshape(T, n, size).topk(min(best, size), dim=2).values.sum(2)
+            first = torch.sort(top, dim=1, descending=True, stable=True).indices[:, :kept]
+            keep = (first[:, :, None] == torch.arange(n, device="cuda")).any(1)
+            c = torch.where(keep.repeat_interleave(size, 1), c, -float("inf"))
+        got = ids.long()
+        # by value: what is selected counts as much as what should be, to the steps
+        # of 64 bits that a sum of another order and another exponential take
+        want = torch.sort(c, dim=1, descending=True, stable=True)
+        mine = c.gather(1, got)
+        slack = 2.0 ** -48 * (1 + (0 if bias is None else float(bias.abs().max())))
+        what = f"turn {turn}: {T} x {E}, top-{K} of {kept} of {n}, {score}"
+        assert bool(((mine - want.values[:, :K]).abs() <= slack).all()), what
+        assert bool((torch.sort(got, 1).values.diff(dim=1) > 0).all()), what
+        if score == "sigmoid" and turn % 5 != 2:
+            # equal logits count the same exactly: ties to the lower id
+            same = mine[:, 1:] == mine[:, :-1]
+            assert bool((got.diff(dim=1)[same] > 0).all()), what
+        v = s.gather(1, got)
+        if turn & 1:
+            v = v / v.sum(1, keepdim=True)
+        assert bool(((w.double() - 1.5 * v).abs() <= 1.01 * 2.0 ** -24 * 1.5 * v + 2.0 ** -149).all()), what
+        flat = got.reshape(-1)
+        assert torch.equal(order.long(), torch.sort(flat, stable=True).indices), what
+        assert torch.equal(off[1:].long(), torch.bincount(flat, minlength=E).cumsum(0)), what
 
 
 # ---------------------------------------------------------------- encoder
@@ -374,3 +492,38 @@ def test_grouped8_many_experts_and_rows(y_ty, R, C, flags):
                 flags_more=pm.PM_GROUPED_FP32_SUMS)
     if C == 272:
         run_grouped8(counts.tolist(), R, C, y_ty, 10, flags, seed=3, pad=1)
+
+
+@pytest.mark.parametrize("y_ty", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("R", [1, 2, 3, 6, 130])
+@pytest.mark.parametrize("C", [16, 112, 144])
+def test_grouped8_few_outputs(y_ty, R, C):
+    """Hardly any outputs or inputs, one row and many, and top_k beyond the uses."""
+    report(f"fp8 {R} x {C} {y_ty}")
+    for counts in ([1], [0, 2, 0, 7], [90, 40]):
+        run_grouped8(counts, R, C, y_ty, 1, SCATTER, seed=R, wide=3)
+        run_grouped8(counts, R, C, y_ty, 1 << 30, GATHER, seed=R + 1, pad=1)
+        if R % 2 == 0:
+            run_grouped8(counts, R, C, y_ty, 2, GATHER | SWIGLU, seed=R + 2, pad=1)
+
+
+def test_grouped8_same_use_twice():
+    """A use that occurs twice: gathered rows are those of the use each time;
+    scattered, one of its results is left."""
+    report("fp8 same use twice")
+    E, R, C, n = 2, 80, 272, 60
+    W, ws = fc.make_weights(E, R, C, 1)
+    x, xs = fc.make_x(n, C, 2)
+    off = torch.tensor([0, 30, 60], dtype=torch.int32, device="cuda")
+    order = torch.arange(n, dtype=torch.int32, device="cuda")
+    order[7], order[40] = 3, 12
+    for y_ty in ("f32", "bf16"):
+        y = torch.full((n, R), -7.0, dtype=rc.TYPES[y_ty], device="cuda")
+        pm.pm_grouped_gemm_fp8(W, ws, x, xs, y, off, order, 1, GATHER)
+        want = fc.grouped_plain(W, ws, x, xs, off, order, n, 1, True, False, False, y_ty == "bf16")
+        rc.check_grouped(y, -7.0, want)
+        z = torch.full_like(y, -7.0)
+        pm.pm_grouped_gemm_fp8(W, ws, x, xs, z, off, order, 1, GATHER | SCATTER)
+        for use, rows in ((3, (3, 7)), (12, (12, 40))):
+            assert any(torch.equal(z[use], y[r]) for r in rows), use
+        assert bool((z[7] == -7.0).all()) and bool((z[40] == -7.0).all())
