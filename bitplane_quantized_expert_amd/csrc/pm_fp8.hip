@@ -25,15 +25,22 @@ namespace pm {
 // Tiles from a 320th of the inputs (rows per group) on, at most 13; where no compute
 // unit has a second tile, they take bf16 from 4 rows on.  Halves, converted
 // anew for each tile, pay from 8 rows on, and from 16 where there is one tile
-// each.  The rule loses up to 9 % of bf16 calls at 2 or 3 rows, of fp32 ones 16 %
-// at 8 rows of 256 inputs.
+// each.  What the rule loses in the table: of bf16 calls 10 % at 4 rows of 8192 inputs
+// (118 for 107, one tile each), 8 % at 2 rows of 16 experts of 4096 (27 for 25), 7 % at
+// 12 rows of 128 experts of 4096 (238 for 223); of fp32 ones 13 % at 8 rows of 256
+// inputs (17 for 15).
 // Of bf16 results, tiles of 256 rows instead of 128 from 384 rows per group on,
 // where there are two for each compute unit (128/256 us at 192, 256, 320, 384, 512,
 // 1024 rows: 209/203 258/267 307/352 356/353 461/452 883/828, 128 experts of 4096 x
 // 1024; 168/163 207/210 239/253 274/260 344/328 630/576, 64 of 2048 x 4096 with gate
 // and up), or where 128-row tiles' three stages leave no room in LDS for the
-// table of experts (above some 2000).  The groups' sizes are on the device; these
-// are rows per group if every expert had some.
+// table of experts (above some 2000).  The rule counts tiles and not the rounds that
+// the compute units take for them, and asking for two tiles each keeps 128 rows
+// where 256 are faster by 9 to 19 %: 158/133 at 384 rows of 16 experts of 4096 x 4096
+// (89/78 at 128), 133/120 127/109 139/113 at 256, 320, 384 of 8 of 4096 x 7168.  It
+// loses less than 2 % where it takes 256 (370/375 at 512 rows of 256 of 1024 x 2048).
+// The groups' sizes are on the device; these are rows per group if every expert had
+// some.
 hipError_t launch_grouped8(const GroupedCall& C, hipStream_t st) {
     const int64_t groups = std::min(C.n_experts, C.n_rows), cus = compute_units();
     const int64_t x_rows = C.flags & PM_GROUPED_GATHER ? (C.n_rows - 1) / C.top_k + 1 : 256;

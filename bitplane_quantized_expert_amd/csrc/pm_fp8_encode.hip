@@ -7,7 +7,7 @@
 // The quotient is not formed by a division: its own rounding would meet the
 // border of two codes in some bf16 blocks in a hundred values, and a dozen
 // instructions a value would bound the kernel (24 in all took 42 us for 16384 x 4096
-// bf16 values, these 8 take 34).  With t = x / scale or up to 2^-20 of it more, and h = t cut off to
+// bf16 values, these 8 take 34.5).  With t = x / scale or up to 2^-20 of it more, and h = t cut off to
 // 12 bits, which every border between two codes has, the sign of the remainder
 // |x| - |h| scale says on which side of h the quotient lies, and h moved there by
 // one ulp of fp32 rounds as the quotient does.  One fma gives that sign while the
@@ -172,7 +172,7 @@ __device__ inline void store16(const EncodeCall& C, int64_t row, int col, int l,
 }
 
 // One scale per row and 128 inputs.  A lane goes on by the blocks of the grid; its
-// place is moved, not divided anew.  Measured: 16384 x 4096 bf16 34.4 us, 5.9 TB/s
+// place is moved, not divided anew.  Measured: 16384 x 4096 bf16 34.5 us, 5.9 TB/s
 // (6.2 is what an elementwise kernel of one read and one write reaches); with
 // loads through the caches 36.7, with two blocks of a lane on their way together
 // 34.8, with 8 workgroups per compute unit instead of 32 36.5.
@@ -211,7 +211,7 @@ __global__ __launch_bounds__(256) void encode_rows_kernel(const EncodeCall C, in
 // that two of them share (rows need not begin at a line).  Measured: 64 matrices
 // of 2048 x 4096 bf16 282 us, 5.7 TB/s (308 without regard to the XCDs, 298 with
 // loads through the caches, 286 with 2 rows and twice the threads); 40 of 1426 x
-// 1008 fp32 60.4 us, 4.8 TB/s (a twelfth of the workgroups has 18 rows); 80 of 1426
+// 1008 fp32 59.7 to 60.5 us, 4.8 TB/s (a twelfth of the workgroups has 18 rows); 80 of 1426
 // x 1008 bf16 82 us (109 without regard to the XCDs; 75 through the caches: lines
 // that two blocks share).
 template <int TYPE, int R>

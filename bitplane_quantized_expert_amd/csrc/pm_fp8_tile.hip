@@ -23,9 +23,10 @@
 // Either way a block's sum meets the factor sw * sx in one fp32 fma per element.
 //
 // What bounds them, and how it is met:
-// - Many rows (65536 over 32 experts of 2048 x 4096, gate and up: 504 to 515 us, 2.13
-//   to 2.18 PFLOP/s, the matrix cores 62 % busy): 4 fmas and 4 factors an element
-//   of a block beside its 32 cycles of product, all in one wave's order.  So each
+// - Many rows (65536 over 32 experts of 2048 x 4096, gate and up: 540 to 563 us, 1.95
+//   to 2.04 PFLOP/s, the matrix cores 56 % busy): 4 fmas and 4 factors an element
+//   of a block beside its 32 cycles of product, all in one wave's order, and SiLU,
+//   30 us of it, with the matrix cores idle.  So each
 //   product is pinned where it is written, its sums are added two products later
 //   (no wait for the result), and the loads of a stage lie a few products apart;
 //   left to the compiler the sums wait, in 193 spilled registers.  A product
