@@ -36,7 +36,7 @@ namespace pm {
 // and up), or where 128-row tiles' three stages leave no room in LDS for the
 // table of experts (above some 2000).  The rule counts tiles and not the rounds that
 // the compute units take for them, and asking for two tiles each keeps 128 rows
-// where 256 are faster by 9 to 19 %: 158/133 at 384 rows of 16 experts of 4096 x 4096
+// where 256 are faster by 10 to 19 %: 158/133 at 384 rows of 16 experts of 4096 x 4096
 // (89/78 at 128), 133/120 127/109 139/113 at 256, 320, 384 of 8 of 4096 x 7168.  It
 // loses less than 2 % where it takes 256 (370/375 at 512 rows of 256 of 1024 x 2048).
 // The groups' sizes are on the device; these are rows per group if every expert had
